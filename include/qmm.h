@@ -63,6 +63,17 @@ typedef enum qmm_status {
 #define QMM_Q5_K 13
 #define QMM_Q6_K 14
 
+/* Types of activations, residuals, norm weights, logits and group scales. */
+#define QMM_F32 0
+#define QMM_F16 1
+#define QMM_BF16 30
+
+/* Scores and group scores of moe_router. */
+#define QMM_SCORE_SOFTMAX 0
+#define QMM_SCORE_SIGMOID 1
+#define QMM_GROUP_MAX 0
+#define QMM_GROUP_TOP2 1
+
 /* Operation codes for qmm_workspace_bytes. */
 #define QMM_OP_MMQ 1        /* mmq_* and mmq_*_f32                               */
 #define QMM_OP_MOE 2        /* moe_grouped_mmq, weighted (expert_weights != NULL) */
@@ -89,6 +100,38 @@ typedef enum qmm_status {
 int q8_1_quantize(const float* x, void* xq, int64_t T, int64_t K, void* stream);
 
 /*
+ * q8_1_dequantize -- Q8_1 rows xq[T][K/32] -> x[T][K] of x_type (QMM_F32,
+ * QMM_F16 or QMM_BF16): every int8 times its block's f16 scale, exact in
+ * fp32 and rounded once to x_type (an f16 result above 65504 is infinite).
+ * For consumers of Q8_1 activations that are not quantized.  Requires T >= 0,
+ * K > 0, K % 32 == 0, T * K <= 2^40; T == 0 is a no-op.
+ */
+int q8_1_dequantize(const void* xq, void* x, int x_type, int64_t T, int64_t K, void* stream);
+
+/*
+ * rms_norm_q8_1 -- the residual's addition, the root-mean-square norm and the
+ * Q8_1 quantizer in one pass ([GAP] lever T4: the producer emits the next
+ * product's input format directly).  Per row of K values:
+ *   h = x                           without a residual
+ *   h = residual_out = x + residual rounded once to res_type, otherwise
+ *   n = h * rstd * (weight + weight_offset), rstd = 1/sqrt(mean(h^2) + eps)
+ *   xq = Q8_1(n), the steps of q8_1_quantize on the fp32 n
+ *   y = n rounded to y_type         when y is not NULL
+ * x, residual, weight [K] and y may each be QMM_F32, QMM_F16 or QMM_BF16;
+ * sums and statistics are fp32.  residual and residual_out are both given or
+ * both NULL (res_type is then ignored), and may be the same buffer: the
+ * stream is then updated in place.  No other buffers may overlap.  A row's
+ * result depends on that row, K and the types alone, not on T.
+ * Input must be finite, mean(h^2) below the fp32 range and |n| <= 127 * 65504.
+ * A row of zeros with eps == 0 gives NaN in y and an unspecified Q8_1 row.
+ * Requires 0 <= T < 2^31, 0 < K <= 2^30, K % 32 == 0, eps >= 0.  T == 0 is a
+ * no-op.
+ */
+int rms_norm_q8_1(const void* x, int x_type, const void* residual, void* residual_out, int res_type,
+                  const void* weight, int w_type, float weight_offset, float eps, void* xq, void* y, int y_type,
+                  int64_t T, int64_t K, void* stream);
+
+/*
  * mmvq_q4k / mmvq_q6k -- decode matvec y[T][M] = xq[T][K] . W[M][K]^T for
  * 1 <= T <= QMM_MMVQ_MAX_T ([8e] §2-§3.2: integer 4-way dot products of
  * unpacked 4-bit (6-bit) weights with int8 activations; the Q4_K min term
@@ -107,6 +150,22 @@ int mmvq_q4k(const void* w, const void* xq, float* y, int64_t M, int64_t K, int6
 int mmvq_q5k(const void* w, const void* xq, float* y, int64_t M, int64_t K, int64_t T, void* stream);
 int mmvq_q6k(const void* w, const void* xq, float* y, int64_t M, int64_t K, int64_t T,
              void* stream);
+
+/*
+ * mmvq_q4g -- matvec of 4-bit weights with group scales (no super-blocks),
+ * y[T][M] = xq[T][K] . W[M][K]^T for 1 <= T <= QMM_MMVQ_MAX_T, with
+ *   W[m][k] = scales[m][k/group] * (q[m][k] - z[m][k/group])
+ * w       [M][K/2] bytes: q[2i] in the low and q[2i+1] in the high half of byte i
+ * scales  [M][K/group] of scale_type, QMM_F16 or QMM_BF16
+ * zeros   [M][ceil(K/group/2)] bytes, the zero points z of groups 2i and
+ *         2i+1 in the low and high half of byte i; NULL: z = 8 everywhere
+ * Integer dot products per 32-value block, scaled and summed in fp32.
+ * Output fp32, y[t*M + i]; identical inputs give identical bits.
+ * Requires 1 <= M <= 2^26, 32 <= K <= 2^24, group % 32 == 0, K % group == 0;
+ * pointers 16-byte aligned, outputs apart from inputs.
+ */
+int mmvq_q4g(const void* w, const void* scales, int scale_type, const void* zeros, const void* xq, float* y,
+             int64_t M, int64_t K, int64_t group, int64_t T, void* stream);
 
 /*
  * mmvq_pair -- two one-token matvecs on the same activation row, in one
@@ -196,6 +255,34 @@ int mmq_q5k_f32(const void* w, const float* x, float* y, int64_t M, int64_t K, i
                 void* ws, size_t ws_bytes, void* stream);
 int mmq_q6k_f32(const void* w, const float* x, float* y, int64_t M, int64_t K, int64_t T,
                 void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_router -- routing of T tokens to E experts: the ids and weights that
+ * moe_grouped_mmq and moe_ffn take, from the router's logits [T][E] (type
+ * QMM_F32, QMM_F16 or QMM_BF16).
+ *   score  s = softmax(logits) over the E experts, or sigmoid(logits)
+ *   value  c = s + bias[E] (fp32; NULL: none).  The bias only selects.
+ *   groups n_groups runs of E/n_groups experts each have the largest c of
+ *          their experts (QMM_GROUP_MAX) or the sum of the two largest
+ *          (QMM_GROUP_TOP2); the topk_groups best groups are kept
+ *   ids    the top_k experts of the kept groups by c, in decreasing order
+ *   weights s of the chosen (without the bias), divided by their sum if
+ *          renormalize, times scale; fp32
+ * The order is that of c without rounding error (as in 64 bits; without a
+ * bias the order of the logits), equal values in the order of the experts or
+ * groups.  A logit of -inf (or NaN) masks its expert: score 0 and after all
+ * others of the kept groups whatever its bias, with weight 0 if it is chosen
+ * for want of others; a group without unmasked experts comes last.  A token
+ * with every expert masked gets ids in range and weights 0.  +inf counts as
+ * the largest finite fp32 value.
+ * Requires 0 <= T <= 2^26, 1 <= E <= 512, 1 <= n_groups <= 64, E % n_groups
+ * == 0, 1 <= topk_groups <= n_groups, 1 <= top_k <= min(64, topk_groups * E /
+ * n_groups); 16-byte aligned pointers.  bias must be finite.  T == 0 is a
+ * no-op; n_groups == 1 ignores group_score.
+ */
+int moe_router(const void* logits, int type, int64_t T, int64_t E, int64_t top_k, int scoring, const float* bias,
+               int64_t n_groups, int64_t topk_groups, int group_score, int renormalize, float scale, int32_t* ids,
+               float* weights, void* stream);
 
 /*
  * moe_grouped_mmq -- routed-expert grouped GEMM ([GAP] lever T2 and its

@@ -40,9 +40,12 @@ Readings where the pages are silent (each pinned by a test unless marked):
 """
 from .formats import (  # noqa: F401
     q4k_fields, q4k_dequant, q5k_fields, q5k_dequant, q6k_fields, q6k_dequant, q8_1_fields, q8_1_dequant,
+    q4g_dequant,
 )
 from .quantize import quantize_q8_1  # noqa: F401
 from .matmul import (  # noqa: F401
     dense, abs_bound, q4k_subdots, q5k_subdots, q6k_subdots, q4k_factored, q5k_factored, q6k_factored,
 )
 from .moe import route_buckets, grouped, grouped_blocks, combine, swiglu  # noqa: F401
+from .norm import rms_norm  # noqa: F401
+from .routing import route  # noqa: F401

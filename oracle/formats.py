@@ -186,3 +186,23 @@ def q8_1_dequant(xq: np.ndarray) -> np.ndarray:
     d, q, _, _ = q8_1_fields(xq)
     x = d[..., None] * q.astype(np.float64)
     return x.reshape(xq.shape[:-2] + (xq.shape[-2] * 32,))
+
+
+def q4g_dequant(w: np.ndarray, scales: np.ndarray, zeros=None) -> np.ndarray:
+    """4-bit weights with group scales -> float64 ``[M, K]``.
+
+    ``w`` uint8 ``[M, K/2]`` with value 2i in the low and 2i + 1 in the high
+    half of byte i; ``scales`` ``[M, groups]``; ``zeros`` uint8 ``[M,
+    ceil(groups/2)]`` packed the same way, or None for a zero point of 8.
+    """
+    M, half = w.shape
+    K, groups = 2 * half, scales.shape[1]
+    out = np.empty((M, K), dtype=np.float64)
+    out[:, 0::2] = w & 15
+    out[:, 1::2] = w >> 4
+    z = np.full((M, groups), 8.0)
+    if zeros is not None:
+        z[:, 0::2] = (zeros & 15)
+        z[:, 1::2] = (zeros >> 4)[:, :groups // 2]
+    size = K // groups
+    return (out - np.repeat(z, size, axis=1)) * np.repeat(np.asarray(scales, np.float64), size, axis=1)

@@ -40,7 +40,7 @@ ACT_BLOCK = 32
 
 __all__ = [
     "Q4K_BLOCK_BYTES", "Q5K_BLOCK_BYTES", "Q6K_BLOCK_BYTES", "Q8_1_BLOCK_BYTES", "SUPER_BLOCK", "ACT_BLOCK",
-    "rng", "q4k_weights", "q5k_weights", "q6k_weights", "activations", "router", "workload",
+    "rng", "q4g_weights", "q4k_weights", "q5k_weights", "q6k_weights", "activations", "router", "workload",
     "WORKLOADS",
 ]
 
@@ -104,6 +104,21 @@ def q6k_weights(g: np.random.Generator, M: int, K: int, d_sigma: float = 0.01) -
     out[:, 192:208] = sc.view(np.uint8)
     out[:, 208:210] = d.view(np.uint8).reshape(nb, 2)
     return out.reshape(M, K // SUPER_BLOCK, Q6K_BLOCK_BYTES)
+
+
+def q4g_weights(g: np.random.Generator, M: int, K: int, group: int, zeros: bool = False):
+    """Random 4-bit weights with group scales: (values uint8 [M, K/2], scales float32
+    [M, K/group] that float16 and bfloat16 hold exactly, zero points uint8
+    [M, ceil(K/group/2)] or None).  Bytes are uniform; scales are multiples of
+    2^-9 in [1, 255] * 2^-9, some of them negative."""
+    if group % 32 or K % group:
+        raise ValueError("group must be a multiple of 32 that divides K")
+    n = K // group
+    w = g.integers(0, 256, size=(M, K // 2), dtype=np.uint8)
+    s = (g.integers(1, 256, size=(M, n)) * 2.0**-9).astype(np.float32)
+    s = np.where(g.random(size=(M, n)) < 0.1, -s, s).astype(np.float32)
+    z = g.integers(0, 256, size=(M, (n + 1) // 2), dtype=np.uint8) if zeros else None
+    return w, s, z
 
 
 def activations(g: np.random.Generator, T: int, K: int, outlier_frac: float = 0.0,

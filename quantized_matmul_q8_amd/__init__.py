@@ -24,7 +24,7 @@ from ._lib import (  # noqa: F401
 )
 
 __all__ = [
-    "q8_1_quantize", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
+    "q8_1_quantize", "q8_1_dequantize", "rms_norm_q8_1", "moe_router", "mmvq_q4g", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
     "mmq_q6k_f32",
     "moe_grouped_mmq", "moe_grouped_swiglu", "moe_ffn", "moe_slot_mmvq",
     "swiglu_q8_1", "workspace", "workspace_bytes", "debug_subdots", "probe_read", "probe_read_geom",
@@ -126,6 +126,164 @@ def q8_1_quantize(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Ten
         raise ValueError(f"x: K = {K} is not a multiple of 32")
     out = _out(out, (T, K // 32, 40), torch.uint8, x.device)
     _lib.call("q8_1_quantize", _p(x), _p(out), T, K, _stream(x.device))
+    return out
+
+
+_TYPES = {torch.float32: _lib.QMM_F32, torch.float16: _lib.QMM_F16, torch.bfloat16: _lib.QMM_BF16}
+
+
+def _typed(t: torch.Tensor, name: str, ndim: int) -> int:
+    """Checks a tensor that may be fp32, f16 or bf16; returns its type code."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    _need(t, t.dtype, name, ndim)
+    return code
+
+
+def _on(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _enqueue(device: torch.device, name: str, *args) -> None:
+    """Calls ``name`` on the current stream of ``device``, whichever device is current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _lib.call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _lib.call(name, *args, stream)
+
+
+def q8_1_dequantize(xq: torch.Tensor, dtype: torch.dtype = torch.float32,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Q8_1 blocks ``[T, K/32, 40]`` -> the values ``[T, K]`` that they stand for, in
+    ``dtype`` (float32: exact; float16 or bfloat16: rounded once)."""
+    _need(xq, torch.uint8, "xq", 3)
+    T, K = xq.shape[0], xq.shape[1] * 32
+    if xq.shape[2] != 40:
+        raise ValueError(f"xq: expected [rows, K/32, 40], got {tuple(xq.shape)}")
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    out = _out(out, (T, K), dtype, xq.device)
+    _enqueue(xq.device, "q8_1_dequantize", xq.data_ptr(), out.data_ptr(), _TYPES[dtype], T, K)
+    return out
+
+
+def rms_norm_q8_1(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residual: torch.Tensor | None = None,
+                  weight_offset: float = 0.0, y_dtype: torch.dtype | None = None,
+                  residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  y: torch.Tensor | None = None):
+    """RMS norm of ``x[T, K]`` (plus ``residual[T, K]``) into Q8_1 blocks, in one pass.
+
+    ``h = x + residual`` (rounded to the residual's dtype) and ``n = h /
+    sqrt(mean(h^2) + eps) * (weight + weight_offset)``.  Returns ``(xq,
+    residual_out, y)``: the Q8_1 blocks ``[T, K/32, 40]`` of n; ``h`` (None
+    without a residual); n itself in ``y_dtype`` (None if neither ``y_dtype``
+    nor ``y`` is given).  ``residual_out=residual`` updates the stream in
+    place.  Every tensor may be float32, float16 or bfloat16 on its own.
+    """
+    xt = _typed(x, "x", 2)
+    wt = _typed(weight, "weight", 1)
+    T, K = x.shape
+    if K % 32:
+        raise ValueError(f"x: K = {K} is not a multiple of 32")
+    if weight.shape[0] != K:
+        raise ValueError(f"weight must have shape ({K},), got {tuple(weight.shape)}")
+    if not eps >= 0.0:
+        raise ValueError(f"eps must be at least 0, got {eps}")
+    dev, rt = x.device, 0
+    if residual is not None:
+        rt = _typed(residual, "residual", 2)
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+        residual_out = _out(residual_out, (T, K), residual.dtype, dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is not None and y_dtype is None:
+        y_dtype = y.dtype
+    yt = 0
+    if y_dtype is not None:
+        if y_dtype not in _TYPES:
+            raise TypeError(f"y_dtype must be float32, float16 or bfloat16, got {y_dtype}")
+        yt = _TYPES[y_dtype]
+        y = _out(y, (T, K), y_dtype, dev, "y")
+    _on(dev, weight=weight, residual=residual)
+    out = _out(out, (T, K // 32, 40), torch.uint8, dev)
+    _enqueue(dev, "rms_norm_q8_1", x.data_ptr(), xt, None if residual is None else residual.data_ptr(),
+             None if residual is None else residual_out.data_ptr(), rt, weight.data_ptr(), wt, weight_offset, eps,
+             out.data_ptr(), None if y is None else y.data_ptr(), yt, T, K)
+    return out, residual_out, y
+
+
+_SCORING = {"softmax": _lib.QMM_SCORE_SOFTMAX, "sigmoid": _lib.QMM_SCORE_SIGMOID}
+_GROUP_SCORE = {"max": _lib.QMM_GROUP_MAX, "top2": _lib.QMM_GROUP_TOP2}
+
+
+def moe_router(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax", bias: torch.Tensor | None = None,
+               n_groups: int = 1, topk_groups: int | None = None, group_score: str = "max", renormalize: bool = False,
+               scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """Routes tokens: ``logits[T, E]`` -> (int32 ids, fp32 weights), both ``[T, top_k]``, as
+    :func:`moe_grouped_mmq` and :func:`moe_ffn` take them.
+
+    ``scoring``: "softmax" or "sigmoid"; ``bias`` fp32 [E] is added to the
+    scores for the choice only.  Of ``n_groups`` equal groups of experts the
+    ``topk_groups`` (default: all) with the best ``group_score`` ("max", or
+    "top2": the sum of the two best) are kept.  Equal values go to the lower
+    index; logits of -inf mask experts.  The weights are the scores of the
+    chosen, divided by their sum if ``renormalize``, times ``scale``.
+    """
+    code = _typed(logits, "logits", 2)
+    if scoring not in _SCORING or group_score not in _GROUP_SCORE:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)} and group_score of {sorted(_GROUP_SCORE)}")
+    T, E = logits.shape
+    topk_groups = n_groups if topk_groups is None else topk_groups
+    dev = logits.device
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.shape[0] != E:
+            raise ValueError(f"bias must have shape ({E},), got {tuple(bias.shape)}")
+        _on(dev, bias=bias)
+    ids = _out(ids, (T, top_k), torch.int32, dev, "ids")
+    weights = _out(weights, (T, top_k), torch.float32, dev, "weights")
+    _enqueue(dev, "moe_router", logits.data_ptr(), code, T, E, top_k, _SCORING[scoring],
+             None if bias is None else bias.data_ptr(), n_groups, topk_groups, _GROUP_SCORE[group_score],
+             int(bool(renormalize)), scale, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def mmvq_q4g(w: torch.Tensor, scales: torch.Tensor, xq: torch.Tensor, *, zeros: torch.Tensor | None = None,
+             out: torch.Tensor | None = None) -> torch.Tensor:
+    """Matvec of 4-bit weights with group scales x Q8_1 activations (T <= 8) -> fp32 [T, M].
+
+    ``w`` uint8 [M, K/2], value 2i in the low half of byte i; ``scales`` float16
+    or bfloat16 [M, K/group] (the group size follows from the shapes and is a
+    multiple of 32); ``zeros`` uint8 [M, ceil(K/group/2)], the groups' 4-bit
+    zero points packed like the values, or None for 8.
+    """
+    _need(w, torch.uint8, "w", 2)
+    M, K = w.shape[0], w.shape[1] * 2
+    st = _typed(scales, "scales", 2)
+    if st == _lib.QMM_F32:
+        raise TypeError("scales must be float16 or bfloat16")
+    groups = scales.shape[1]
+    if scales.shape[0] != M or groups < 1 or K % (32 * groups):
+        raise ValueError(f"scales must be [{M}, K/group] with group a multiple of 32 that divides K = {K}, got "
+                         f"{tuple(scales.shape)}")
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", 2)
+        if tuple(zeros.shape) != (M, (groups + 1) // 2):
+            raise ValueError(f"zeros must have shape {(M, (groups + 1) // 2)}, got {tuple(zeros.shape)}")
+    T = _acts(xq, K)
+    dev = w.device
+    _on(dev, scales=scales, zeros=zeros, xq=xq)
+    out = _out(out, (T, M), torch.float32, dev)
+    _enqueue(dev, "mmvq_q4g", w.data_ptr(), scales.data_ptr(), st, None if zeros is None else zeros.data_ptr(),
+             xq.data_ptr(), out.data_ptr(), M, K, K // groups, T)
     return out
 
 

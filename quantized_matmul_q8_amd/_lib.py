@@ -31,12 +31,23 @@ QMM_OP_MOE = 2
 QMM_OP_MOE_SLOTS = 3
 QMM_OP_MOE_FFN = 4
 QMM_MMVQ_MAX_T = 8
+QMM_F32 = 0
+QMM_F16 = 1
+QMM_BF16 = 30
+QMM_SCORE_SOFTMAX = 0
+QMM_SCORE_SIGMOID = 1
+QMM_GROUP_MAX = 0
+QMM_GROUP_TOP2 = 1
 
-_vp, _i64, _sz, _i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_vp, _i64, _sz, _i, _f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
 # name -> (restype, argtypes); every symbol declared in include/qmm.h
 SIGNATURES = {
     "q8_1_quantize": (_i, [_vp, _vp, _i64, _i64, _vp]),
+    "q8_1_dequantize": (_i, [_vp, _vp, _i, _i64, _i64, _vp]),
+    "rms_norm_q8_1": (_i, [_vp, _i, _vp, _vp, _i, _vp, _i, _f, _f, _vp, _vp, _i, _i64, _i64, _vp]),
+    "mmvq_q4g": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+    "moe_router": (_i, [_vp, _i, _i64, _i64, _i64, _i, _vp, _i64, _i64, _i, _i, _f, _vp, _vp, _vp]),
     "mmvq_q4k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q5k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q6k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),

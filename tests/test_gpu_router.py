@@ -1,0 +1,191 @@
+"""GPU: moe_router against the float64 oracle.
+
+The ids have to be equal, near ties included.  Tolerance of the weights
+(relative): a softmax weight is exp(x - m) of an fp32 difference, whose
+rounding is at most |x - m| * 2^-24, two more for exp; the sum over E experts
+has positive terms in chains of at most E/4 + 8 additions (any split over four
+or more lanes) and inherits the terms' errors, on average at most ln(E) <= 7
+for the differences (sum p_i |x_i - m| <= ln E where m is the largest), and
+two for exp; division and scale add two.  Sigmoid: exp, addition, division,
+then the sum of top_k terms, division and scale.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import qmm_synth
+from _gpu import DEV, dev, host, say
+
+import quantized_matmul_q8_amd as qmm
+
+pytestmark = pytest.mark.gpu
+
+
+def check(x, top_k, scoring="softmax", bias=None, n_groups=1, topk_groups=None, group_score="max", renormalize=False,
+          scale=1.0, dtype=torch.float32):
+    x = torch.from_numpy(np.ascontiguousarray(x)).to(dtype)
+    T, E = x.shape
+    say("moe_router", f"T={T} E={E} top_k={top_k} {scoring} bias={bias is not None} groups={n_groups}/{topk_groups} "
+        f"{group_score} renormalize={renormalize} {dtype}")
+    ids, w = qmm.moe_router(x.to(DEV), top_k, scoring=scoring, bias=None if bias is None else dev(bias),
+                            n_groups=n_groups, topk_groups=topk_groups, group_score=group_score,
+                            renormalize=renormalize, scale=scale)
+    xf = x.float().numpy()
+    i2, w2 = oracle.route(xf, top_k, scoring, bias, n_groups, topk_groups or n_groups, group_score, renormalize, scale)
+    ids, w = host(ids), host(w)
+    bad = np.argwhere((ids != i2).any(axis=1)).ravel()
+    assert not len(bad), f"{len(bad)} rows differ; row {bad[0]}: {ids[bad[0]]} for {i2[bad[0]]}"
+    if scoring == "softmax":
+        lx = np.take_along_axis(np.nan_to_num(xf, nan=-np.inf), i2.astype(np.int64), 1)
+        lx = np.minimum(lx.astype(np.float64), np.finfo(np.float32).max)
+        m = lx.max(1, keepdims=True) if renormalize else np.minimum(
+            np.where(np.isnan(xf), -np.inf, xf).max(1, keepdims=True), np.finfo(np.float32).max)
+        with np.errstate(invalid="ignore"):
+            far = np.where(w2 > 0, np.abs(lx - m), 0.0)
+        tol = (far + 2 + E / 4 + 8 + 7 + 2 + 2) * 2.0**-24
+    else:
+        tol = (4 + top_k + 4 + 2) * 2.0**-24
+    assert np.all(np.abs(w - w2) <= tol * w2 + 2.0**-126 * abs(scale) * (1 + top_k)), np.abs(w / w2 - 1).max()
+    return ids, w
+
+
+@pytest.mark.parametrize("E,top_k", [(1, 1), (2, 1), (2, 2), (3, 2), (5, 5), (8, 2), (16, 4), (33, 6), (63, 8), (64, 8),
+                                     (64, 64), (65, 3), (96, 6), (127, 10), (128, 8), (130, 8), (160, 6), (192, 16),
+                                     (255, 9), (256, 8), (257, 64), (320, 12), (384, 6), (511, 32), (512, 10), (512, 64)])
+@pytest.mark.parametrize("T", [1, 37])
+def test_sizes(T, E, top_k):
+    x = qmm_synth.activations(qmm_synth.rng(T + E), T, E) * 1.5
+    b = 0.05 * qmm_synth.activations(qmm_synth.rng(E), 1, E)[0]
+    check(x, top_k)
+    check(x, top_k, "sigmoid", b, renormalize=True, scale=2.5, dtype=torch.bfloat16)
+    check(x, top_k, "softmax", b, renormalize=True, dtype=torch.float16)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("E,groups,keep,top_k", [(256, 8, 4, 8), (128, 4, 1, 6), (60, 4, 3, 9), (512, 64, 8, 10),
+                                                 (64, 64, 20, 20), (510, 5, 5, 4), (96, 2, 1, 48), (512, 2, 1, 3)])
+def test_groups(scoring, with_bias, renormalize, E, groups, keep, top_k):
+    x = qmm_synth.activations(qmm_synth.rng(E + keep), 29, E) * 2
+    b = 0.1 * qmm_synth.activations(qmm_synth.rng(E), 1, E)[0] if with_bias else None
+    for score in ("max", "top2"):
+        check(x, top_k, scoring, b, groups, keep, score, renormalize, 1.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,E", [(1000, 128), (4099, 96), (70000, 8)])
+def test_many_tokens(T, E):
+    x = qmm_synth.activations(qmm_synth.rng(T), T, E)
+    check(x[:1500], min(8, E))
+    ids, w = qmm.moe_router(dev(x), min(8, E))
+    i2, w2 = qmm.moe_router(dev(x[-1500:]), min(8, E))      # a token's routing does not depend on the others
+    assert torch.equal(ids[-1500:], i2) and torch.equal(w[-1500:], w2)
+    assert np.array_equal(host(ids)[-1500:], oracle.route(x[-1500:], min(8, E))[0])
+
+
+@pytest.mark.parametrize("E,groups", [(64, 1), (256, 8), (100, 4), (512, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_equal_values_go_to_the_lower_index(E, groups, scoring):
+    g = qmm_synth.rng(E)
+    x = g.integers(-2, 3, size=(60, E)).astype(np.float32)       # five different logits
+    x[0] = 1.0
+    x[1, ::2], x[1, 1::2] = 0.0, -0.0
+    b = np.zeros(E, np.float32)
+    for score in ("max", "top2"):
+        check(x, min(16, E // groups), scoring, None, groups, max(1, groups // 2), score, dtype=torch.bfloat16)
+        check(x, min(16, E // groups), scoring, b, groups, max(1, groups // 2), score)
+    check(x, 5, scoring, g.integers(-1, 2, size=E).astype(np.float32))
+
+
+@pytest.mark.parametrize("E,groups", [(128, 1), (256, 8), (384, 1), (512, 4)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_values_closer_than_fp32_resolves(E, groups, scoring):
+    # every second expert's bias brings it within an fp32 rounding of its neighbour
+    g = qmm_synth.rng(E + 1)
+    x = (g.standard_normal((1, E)) * 1.5).astype(np.float32).repeat(8, 0)
+    s = 1 / (1 + np.exp(-x[0].astype(np.float64)))
+    if scoring == "softmax":
+        s = np.exp(x[0].astype(np.float64))
+        s /= s.sum()
+    b = (0.3 * g.standard_normal(E)).astype(np.float32)
+    b[1::2] = (s[0::2] + b[0::2].astype(np.float64) - s[1::2]).astype(np.float32)
+    x[1:] = g.permuted(x[1:], axis=1)
+    for score in ("max", "top2"):
+        check(x, min(32, E // groups), scoring, b, groups, max(1, groups // 2), score, True)
+    # the sums of two groups' best within a rounding of each other
+    if groups > 1:
+        per = E // groups
+        y = np.full((4, E), -4.0, np.float32)
+        y[:, 0:2], y[:, per:per + 2] = [[0.5, 0.25]], [[0.75, 0.0]]
+        y[1, per + 1] = np.log(1 / (1 / (1 + np.exp(-.5)) + 1 / (1 + np.exp(-.25)) - 1 / (1 + np.exp(-.75))) - 1) * -1
+        y[2, per + 1] = np.nextafter(y[1, per + 1], np.float32(9))
+        y[3, per + 1] = np.nextafter(y[1, per + 1], np.float32(-9))
+        check(y, 2, scoring, None, groups, 1, "top2")
+
+
+def test_masks():
+    g = qmm_synth.rng(77)
+    for E, groups, keep, k in [(128, 1, 1, 8), (64, 8, 3, 20), (10, 2, 1, 5), (512, 1, 1, 64), (300, 4, 2, 12)]:
+        x = (g.standard_normal((40, E)) * 2).astype(np.float32)
+        x[g.random((40, E)) < 0.6] = -np.inf
+        x[0] = -np.inf                                   # nothing left
+        x[1, 1:] = -np.inf                               # one left
+        x[2] = np.nan
+        x[3, :-1] = -np.inf                              # the last one left
+        x[4, E // groups:] = -np.inf                     # the first group only
+        x[5] = np.finfo(np.float32).min                  # the type's lowest value masks nothing
+        x[6, ::3] = np.nan
+        b = (g.standard_normal(E)).astype(np.float32)
+        for scoring in ("softmax", "sigmoid"):
+            for bias in (None, b):
+                for renorm in (False, True):
+                    for score in ("max", "top2"):
+                        ids, w = check(x, k, scoring, bias, groups, keep, score, renorm)
+                        assert np.all(w[0] == 0) and np.all(w[2] == 0)
+                        assert all(len(set(r)) == k for r in ids.tolist())
+
+
+def test_extreme_logits():
+    g = qmm_synth.rng(5)
+    x = (g.standard_normal((12, 96)) * 50).astype(np.float32)
+    x[0, 7] = np.inf
+    x[1, [3, 90]] = np.inf
+    x[2] *= 1e30
+    x[3] -= 1e4                                          # sigmoid underflows for all
+    x[4, :] = -100.0
+    x[5] = -200.0
+    x[5, 4] = 88.0
+    for renorm in (False, True):
+        check(x, 6, "softmax", None, renormalize=renorm)
+    check(x[2:], 6, "sigmoid")
+    check(x[5:], 6, "softmax", (0.2 * g.standard_normal(96)).astype(np.float32), renormalize=True)
+    half = np.clip(x, -65504, 65504)
+    check(half, 6, "softmax", dtype=torch.float16)
+
+
+def test_buffers_and_refusals():
+    x = dev(qmm_synth.activations(qmm_synth.rng(2), 6, 64))
+    ids, w = qmm.moe_router(x, 4)
+    bi = torch.full((9, 4), -5, dtype=torch.int32, device=DEV)
+    bw = torch.full((9, 4), -5.0, device=DEV)
+    a, b = qmm.moe_router(x, 4, ids=bi[:6], weights=bw[:6])
+    assert a.data_ptr() == bi.data_ptr() and b.data_ptr() == bw.data_ptr()
+    assert torch.equal(bi[:6], ids) and torch.equal(bw[:6], w) and torch.all(bi[6:] == -5) and torch.all(bw[6:] == -5)
+    e = qmm.moe_router(x[:0], 4)
+    assert tuple(e[0].shape) == (0, 4) and tuple(e[1].shape) == (0, 4)
+    for bad in (lambda: qmm.moe_router(x, 4, scoring="relu"), lambda: qmm.moe_router(x, 4, group_score="sum"),
+                lambda: qmm.moe_router(x, 4, bias=torch.zeros(63, device=DEV)),
+                lambda: qmm.moe_router(x.t(), 4), lambda: qmm.moe_router(x[:, :32], 4),
+                lambda: qmm.moe_router(x, 4, ids=bi), lambda: qmm.moe_router(x, 4, bias=torch.zeros(64))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        qmm.moe_router(x.double(), 4)
+    with pytest.raises(TypeError):
+        qmm.moe_router(x, 4, bias=torch.zeros(64, dtype=torch.bfloat16, device=DEV))
+    for bad in (lambda: qmm.moe_router(x, 0), lambda: qmm.moe_router(x, 65), lambda: qmm.moe_router(x, 4, n_groups=7),
+                lambda: qmm.moe_router(x, 9, n_groups=8, topk_groups=1),
+                lambda: qmm.moe_router(torch.zeros(1, 513, device=DEV), 4)):
+        with pytest.raises(qmm.QmmError):
+            bad()
