@@ -161,7 +161,7 @@ int mmvq_q6k(const void* w, const void* xq, float* y, int64_t M, int64_t K, int6
  *         2i+1 in the low and high half of byte i; NULL: z = 8 everywhere
  * Integer dot products per 32-value block, scaled and summed in fp32.
  * Output fp32, y[t*M + i]; identical inputs give identical bits.
- * Requires 1 <= M <= 2^26, 32 <= K <= 2^24, group % 32 == 0, K % group == 0;
+ * Requires 1 <= M <= 2^26, 32 <= K <= 2^20, group % 32 == 0, K % group == 0;
  * pointers 16-byte aligned, outputs apart from inputs.
  */
 int mmvq_q4g(const void* w, const void* scales, int scale_type, const void* zeros, const void* xq, float* y,

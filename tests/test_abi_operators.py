@@ -77,7 +77,7 @@ def q4g(**kw):
 def test_q4g_errors():
     assert q4g(st=F32) == _lib.QMM_ERR_UNSUPPORTED
     for kw in (dict(M=0), dict(M=(1 << 26) + 1), dict(K=0, g=32), dict(K=48, g=48), dict(K=256, g=16), dict(K=256, g=96),
-               dict(K=256, g=512), dict(K=256, g=0), dict(T=0), dict(T=9), dict(K=(1 << 24) + 32, g=32)):
+               dict(K=256, g=512), dict(K=256, g=0), dict(T=0), dict(T=9), dict(K=(1 << 20) + 32, g=32)):
         assert q4g(**kw) == _lib.QMM_ERR_SHAPE, kw
     for p in ("w", "s", "x", "y"):
         assert q4g(**{p: NUL}) == _lib.QMM_ERR_NULL
