@@ -303,9 +303,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // with s (1 - s) |x| < 0.23.  So |error of c| <= (1 + kappa s + |c|) * 2^-24
 // with kappa 56 and 3.  Neighbours of the first top_k + 1 that are closer than
 // both errors, or groups at the border of the kept, make the token unsure.
-// With sigmoid scores the n best then get their c in 64 bits and are ranked
-// again; if the n-th, whose 32-bit c bounds the rest, is not clearly below the
-// chosen, and for what else is unsure, route_token takes the token.
+// The n best then get their exponentials in 64 bits and are ranked again; if
+// that leaves a doubt (the softmax's sum, still in 32 bits; the n-th, whose
+// 32-bit c bounds the rest, not clearly below the chosen), and for the groups,
+// route_token takes the token.
 template <int V>
 __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArgs a) {
   // with groups, per wave a float per token and expert, or route_token's double per expert
@@ -527,31 +528,34 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
     const uint64_t closes = __ballot(close);
     if (closes) {  // any of the wave's tokens
       const bool token = (closes >> (lane & 48) & 0xffff) != 0;
-      if (softmax) {
-        unsure = unsure || token;
-      } else {
-        // the n best again, in 64 bits; masked ones stay behind, in their order
-        double d = -1e300 * (li + 1) / 64;
-        if (live) d = 1.0 / (1.0 + exp(-static_cast<double>(mine_x))) + static_cast<double>(b);
-        if (li >= n) d = -DBL_MAX;
-        int place = 0;
-        const int64_t k64 = order_key(d);
-        const int2 own = make_int2(static_cast<int>(k64 >> 32), static_cast<int>(k64 & 0xffffffff));
-#pragma unroll
-        for (int r = 1; r < 16; ++r) {
-          const int src = (lane & 48) | ((li + r) & 15);
-          const int hi = __shfl(own.x, src), lo = __shfl(own.y, src), id = __shfl(my_id, src);
-          const int64_t o = static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo);
-          place += o > k64 || (o == k64 && id < my_id) ? 1 : 0;
-        }
-        // every expert that is not among the n has a 32-bit c of at most the n-th's
-        const float last = __shfl(now, (lane & 48) | (n - 1)), last_s = __shfl(score, (lane & 48) | (n - 1));
-        const bool last_live = __shfl(live ? 1 : 0, (lane & 48) | (n - 1)) != 0;
-        const double above = static_cast<double>(last) + 0x1p-22 * (1.0 + kappa * fabs(last_s) + fabs(last));
-        const bool bad = token && last_live && place < a.top_k && !(d > above);
-        if (token) rank = place;
-        unsure = unsure || (__ballot(bad) >> (lane & 48) & 0xffff) != 0;
+      // The n best again, their exponentials in 64 bits; masked ones stay behind, in their order.  The softmax's sum keeps
+      // a relative error below kappa * 2^-24 =: r, which moves the difference of two values by r |s - s'|.
+      const double r = softmax ? 0x1p-24 * kappa : 0.0;
+      double score64 = 0.0, d = -1e300 * (li + 1) / 64;
+      if (live) {
+        score64 = softmax ? exp(static_cast<double>(mine_x) - static_cast<double>(ref)) / static_cast<double>(sum)
+                          : 1.0 / (1.0 + exp(-static_cast<double>(mine_x)));
+        d = score64 + static_cast<double>(b);
       }
+      if (li >= n) d = -DBL_MAX;
+      int place = 0;
+      bool doubt = false;
+#pragma unroll
+      for (int k = 1; k < 16; ++k) {
+        const int src = (lane & 48) | ((li + k) & 15);
+        const double od = __shfl(d, src), os = __shfl(score64, src);
+        const int id = __shfl(my_id, src);
+        place += od > d || (od == d && id < my_id) ? 1 : 0;
+        doubt = doubt || (fabs(od - d) <= r * fabs(os - score64) && os != score64);
+      }
+      // every expert that is not among the n has a 32-bit c of at most the n-th's
+      const int last = (lane & 48) | (n - 1);
+      const float last_c = __shfl(now, last), last_s = __shfl(score, last);
+      const bool last_live = __shfl(live ? 1 : 0, last) != 0;
+      const double above = static_cast<double>(last_c) + 0x1p-22 * (1.0 + kappa * fabs(last_s) + fabs(last_c));
+      const bool bad = token && live && place < a.top_k && (doubt || (last_live && !(d - r * score64 > above)));
+      if (token) rank = place;
+      unsure = unsure || (__ballot(bad) >> (lane & 48) & 0xffff) != 0;
     }
   }
 
