@@ -112,21 +112,41 @@ struct Pieces {
   }
 };
 
-// The activations of blocks [b0, b0 + n) of T tokens in LDS: per token n x 16
-// bytes (values 0..15 of each block), n x 16 bytes (16..31) and n pairs (fp32
-// d, int32 S).  between() runs after the first loads are issued and before
-// their results are awaited: loads of its own come back after these.
+// LDS for the activations of `seg` blocks: up to four tokens share a record per
+// block, 32 bytes of values each, then (fp32 d, int32 S) each, so that one
+// address and constant offsets reach all of it.  The records' sizes (padded at
+// one and three tokens) let consecutive lanes read 16 bytes each without bank
+// conflicts.
+template <int T>
+struct Layout {
+  static constexpr int tokens(int g) { return T - 4 * g < 4 ? T - 4 * g : 4; }
+  static constexpr int record(int g) {
+    return tokens(g) == 1 ? 48 : tokens(g) == 2 ? 80 : tokens(g) == 3 ? 144 : 160;
+  }
+  static constexpr int kGroups = (T + 3) / 4;
+  static constexpr int kBlock = T > 4 ? 160 + record(1) : record(0);  // bytes of a block in all
+};
+
+// The activations of blocks [b0, b0 + n) of T tokens in LDS.  between() runs
+// after the first loads are issued and before their results are awaited:
+// loads of its own come back after these.
 template <int T, class Fn>
 __device__ __forceinline__ void stage(const Q4gArgs& a, int b0, int n, uint8_t* lds, Fn between) {
+  using Lay = Layout<T>;
   // eight values
   const auto get = [&](int t, int j) {
     const uint32_t* q = reinterpret_cast<const uint32_t*>(
         a.xq + static_cast<uint32_t>((t * a.nblk + b0 + (j >> 2)) * kQ8Bytes + 4 + 8 * (j & 3)));
     return make_uint2(q[0], q[1]);
   };
+  // token t's place in block b's record
+  const auto place = [&](int t, int b, int of_values, int of_factors) {
+    if (T > 4 && t >= 4) return lds + a.seg * 160 + b * Lay::record(Lay::kGroups - 1) + (t - 4) * of_values +
+                                (of_factors ? 32 * Lay::tokens(Lay::kGroups - 1) : 0);
+    return lds + b * Lay::record(0) + t * of_values + (of_factors ? 32 * Lay::tokens(0) : 0);
+  };
   const auto put = [&](int t, int j, uint2 q) {
-    uint8_t* at = lds + t * a.seg * 32 + (j & 2 ? a.seg * 16 : 0) + (j >> 2) * 16 + (j & 1) * 8;
-    *reinterpret_cast<uint2*>(at) =
+    *reinterpret_cast<uint2*>(place(t, j >> 2, 32, 0) + 8 * (j & 3)) =
         make_uint2(__builtin_amdgcn_perm(q.y, q.x, kEvenBytes), __builtin_amdgcn_perm(q.y, q.x, kOddBytes));
   };
   // a block's scale and sum
@@ -136,8 +156,7 @@ __device__ __forceinline__ void stage(const Q4gArgs& a, int b0, int n, uint8_t* 
     return make_uint2(x[0], x[9]);
   };
   const auto put_ds = [&](int t, int j, uint2 q) {
-    *reinterpret_cast<uint2*>(lds + a.seg * 32 * T + (t * a.seg + j) * 8) =
-        make_uint2(__builtin_bit_cast(uint32_t, h2f(q.x & 0xffffu)), q.y);
+    *reinterpret_cast<uint2*>(place(t, j, 8, 1)) = make_uint2(__builtin_bit_cast(uint32_t, h2f(q.x & 0xffffu)), q.y);
   };
   constexpr int N = T > 1 ? 8 : 2;
   Pieces<T, N> x(n * 4);
@@ -170,6 +189,7 @@ __device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkm
 template <int T, int L, int R, bool ZEROS>
 __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
+  using Lay = Layout<T>;
   constexpr int U = 2, kSub = 64 / L, kRows = kSub * R;
   const int lane = threadIdx.x & 63, li = lane % L, sub = lane / L;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -218,10 +238,16 @@ __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
           const int g = a.group_blk == 1 ? b : static_cast<int>(__umulhi(static_cast<uint32_t>(b), a.magic));
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const int64_t m = min(tile * kRows + r * kSub + sub, a.M - 1);
-            B.w[u][r] = ld16_a16(a.w + (m * a.nblk + b) * 16);
-            B.s[u][r] = static_cast<const uint16_t*>(a.scales)[m * a.groups + g];
-            B.z[u][r] = ZEROS ? static_cast<uint32_t>(a.zeros[m * zrow + (g >> 1)]) >> (4 * (g & 1)) : 8u;
+            // with L = 64 the row is the wave's: its addresses are scalar, the lane's part a 32-bit offset
+            const int64_t m = min(tile * kRows + r * kSub + (L == 64 ? 0 : sub), a.M - 1);
+            const uint8_t* row = a.w + m * a.nblk * 16;
+            const uint8_t* scales = static_cast<const uint8_t*>(a.scales) + m * a.groups * 2;
+            B.w[u][r] = ld16_a16(row + static_cast<uint32_t>(b * 16));
+            B.s[u][r] = *reinterpret_cast<const uint16_t*>(scales + static_cast<uint32_t>(g * 2));
+            if constexpr (ZEROS)
+              B.z[u][r] = static_cast<uint32_t>(a.zeros[m * zrow + static_cast<uint32_t>(g >> 1)]) >> (4 * (g & 1));
+            else
+              B.z[u][r] = 8u;
           }
         }
       }
@@ -248,10 +274,11 @@ __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
           }
 #pragma unroll
           for (int t = 0; t < T; ++t) {
-            const uint8_t* at = lds + t * a.seg * 32;
-            const uint4 p = *reinterpret_cast<const uint4*>(at + k * 16);
-            const uint4 q = *reinterpret_cast<const uint4*>(at + a.seg * 16 + k * 16);
-            const uint2 ds = *reinterpret_cast<const uint2*>(lds + a.seg * 32 * T + (t * a.seg + k) * 8);
+            const int g = t / 4, i = t % 4;
+            const uint8_t* at = lds + (g ? a.seg * 160 : 0) + k * Lay::record(g);
+            const uint4 p = *reinterpret_cast<const uint4*>(at + 32 * i);
+            const uint4 q = *reinterpret_cast<const uint4*>(at + 32 * i + 16);
+            const uint2 ds = *reinterpret_cast<const uint2*>(at + 32 * Lay::tokens(g) + 8 * i);
             const float d = __builtin_bit_cast(float, ds.x);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -321,7 +348,7 @@ __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
   }
   if (a.split > 1) {
     // the parts of each tile, added in their order
-    float* parts = reinterpret_cast<float*>(lds + static_cast<size_t>(a.seg) * 40 * T);
+    float* parts = reinterpret_cast<float*>(lds + static_cast<size_t>(a.seg) * Lay::kBlock);
     finish([&](int k, int row, float v) { parts[(wave * T + k) * kRows + row] = v; });
     __syncthreads();
     for (int i = threadIdx.x; i < slots * T * kRows; i += blockDim.x) {
@@ -352,13 +379,13 @@ static void launch(const Q4gArgs& args, int64_t M, hipStream_t st) {
   // unsplit, 4.5 in eight parts; eight tokens 34 and 14, for the activations' copy has more threads too)
   a.split = 1;
   while (a.split < 16 && a.split * 2 <= rounds && a.tiles * a.split * 2 <= static_cast<int64_t>(cus) * 16) a.split *= 2;
-  a.seg = std::min<int64_t>(a.nblk, (kLds - (a.split > 1 ? kParts : 0)) / (40 * T));
+  a.seg = std::min<int64_t>(a.nblk, (kLds - (a.split > 1 ? kParts : 0)) / Layout<T>::kBlock);
   const int waves = a.split * static_cast<int>(std::clamp<int64_t>(a.tiles / cus, 1, 16 / a.split));
   int64_t grid = (a.tiles + waves / a.split - 1) / (waves / a.split);
   // the activations are copied once per CU where they fit; in segments, and in parts, a wave has one tile
   if (a.seg == a.nblk && a.split == 1) grid = std::min<int64_t>(grid, cus);
   const dim3 g(static_cast<unsigned>(grid)), b(waves * 64);
-  const size_t lds = static_cast<size_t>(a.seg) * 40 * T + (a.split > 1 ? kParts : 0);
+  const size_t lds = static_cast<size_t>(a.seg) * Layout<T>::kBlock + (a.split > 1 ? kParts : 0);
   const auto go = [&](auto zeros) {
     constexpr bool Z = decltype(zeros)::value;
     constexpr int R2 = T > 1 ? 2 : 1;

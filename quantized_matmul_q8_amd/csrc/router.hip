@@ -324,6 +324,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   const auto fmin2 = [](float x, float y) { return fminf(x, y); };
   const auto add2 = [](float x, float y) { return x + y; };
   const bool softmax = a.scoring == QMM_SCORE_SOFTMAX;
+  // E > kFull * 16: this many v need no test for the last expert (the launch takes the smallest V)
+  constexpr int kFull = V <= 2 ? 0 : V <= 4 ? 2 : V <= 8 ? 4 : V <= 12 ? 8 : V <= 16 ? 12 : V <= 24 ? 16 : 24;
 
   float x[V], bias[V];
   const uint32_t at = static_cast<uint32_t>(min(static_cast<int64_t>(tok), a.T - 1 - t0)) * a.E;  // from the first token
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   for (int v = 0; v < V; ++v) {
     // NaN and what is behind the last expert count as masked, +inf as the largest finite value
     x[v] = fminf(fmaxf(x[v], -INFINITY), FLT_MAX);
-    x[v] = v * 16 + li < a.E ? x[v] : -INFINITY;
+    if (v >= kFull) x[v] = v * 16 + li < a.E ? x[v] : -INFINITY;
     top = fmaxf(top, x[v]);
   }
   top = row_reduce_f(top, fmax2);
@@ -446,8 +448,12 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float by = biased ? c[v] : x[v];
-    const int k = x[v] > -INFINITY ? order_key(by) : kMasked - (v * 16 + li);
-    key[v] = v * 16 + li < a.E && (kept >> v & 1) ? k : kTaken;
+    key[v] = x[v] > -INFINITY ? order_key(by) : kMasked - (v * 16 + li);
+    if (v >= kFull) key[v] = v * 16 + li < a.E ? key[v] : kTaken;
+  }
+  if (a.groups > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = kept >> v & 1 ? key[v] : kTaken;
   }
 
   // lane j < n gets the j-th best
