@@ -15,12 +15,12 @@
 // rounds stay in flight per wave, across the ends of its tiles: 64 KB per CU
 // with 16 waves.  With few rows `split` waves share a tile by parts of K.
 //
-// Bound by HBM at one token, 28672 x 8192, groups of 32: 27.3 us, 4.8 TB/s
-// (the copy rate of the card is 5.1); 4096 x 11008, groups of 128 with zero
-// points: 7.8 us, 3.0 TB/s (start-up and the activations' copy are about 3 us
-// of it).  Every further token adds 12 VALU instructions and 20 LDS cycles per
-// 2048 weights: 28672 x 8192 takes 30.0, 31.5, 37.0 and 46.7 us at 2, 3, 5
-// and 8 tokens.
+// Bound by HBM at one token, 28672 x 8192, groups of 32: 26.8 us, 4.9 TB/s
+// (a copy of 1 GiB reaches 5.1); 4096 x 11008, groups of 128 with zero points:
+// 7.6 us, 3.1 TB/s (start-up and the activations' copy are about 3 us of it).
+// Every further token adds 13 VALU instructions per 2048 weights, 85 in all at
+// five tokens: 28672 x 8192 takes 29.3, 31.1, 36.4 and 48.7 us at 2, 3, 5 and
+// 8 tokens, where the instructions take 17 and 24 us of the last two.
 //
 // Measured and not kept: the products on the matrix cores (16 x 16 x 64 with
 // four blocks kept apart by zeros, or 4 x 4 x 4 with the weights transposed

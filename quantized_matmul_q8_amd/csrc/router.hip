@@ -7,12 +7,12 @@
 // leaves the token to route_token, which takes the whole wave and 64 bits.
 //
 // Its bytes are few: latency bounds it up to some thousand tokens (1 x 128:
-// 3.4 us, 512 x 128: 4.4, most of it the launch), then the instructions: 16384
-// x 256, eight of them, no bias: 10.5 us, 1.7 TB/s; 32768 x 384 with a bias:
-// 28.6 us, 1.8 TB/s, about 6 of which are the last waves' tokens in 64 bits.
-// One token per wave in 64 bits throughout took 9.5, 43 and 88 us for 1 x 128,
-// 16384 x 256 and 32768 x 384; taking the best out one after the other instead
-// of the candidates' ranks 12.0 and 35.8 for the latter two.
+// 3.3 us, 512 x 128: 4.4, most of it the launch; 4099 x 256 with a bias and
+// groups 13.2), then the instructions: 16384 x 256, eight of them, no bias: 10.1
+// us, 1.8 TB/s; 32768 x 384 with a bias: 21.9 us, 2.4 TB/s.  One token per wave
+// in 64 bits throughout took 9.5, 43 and 88 us for 1 x 128, 16384 x 256 and
+// 32768 x 384; taking the best out one after the other instead of the
+// candidates' ranks 12.0 and 35.8 for the latter two.
 #include "typed.hpp"
 
 #include <float.h>
