@@ -123,7 +123,7 @@ int q8_1_dequantize(const void* xq, void* x, int x_type, int64_t T, int64_t K, v
  * stream is then updated in place.  No other buffers may overlap.  A row's
  * result depends on that row, K and the types alone, not on T.
  * Input must be finite, mean(h^2) below the fp32 range and |n| <= 127 * 65504.
- * A row of zeros with eps == 0 gives NaN in y and an unspecified Q8_1 row.
+ * A row of zeros gives zeros, with eps == 0 too.
  * Requires 0 <= T < 2^31, 0 < K <= 2^30, K % 32 == 0, eps >= 0.  T == 0 is a
  * no-op.
  */
@@ -275,7 +275,7 @@ int mmq_q6k_f32(const void* w, const float* x, float* y, int64_t M, int64_t K, i
  * for want of others; a group without unmasked experts comes last.  A token
  * with every expert masked gets ids in range and weights 0.  +inf counts as
  * the largest finite fp32 value.
- * Requires 0 <= T <= 2^26, 1 <= E <= 512, 1 <= n_groups <= 64, E % n_groups
+ * Requires 0 <= T <= 2^25, 1 <= E <= 512, 1 <= n_groups <= 64, E % n_groups
  * == 0, 1 <= topk_groups <= n_groups, 1 <= top_k <= min(64, topk_groups * E /
  * n_groups); 16-byte aligned pointers.  bias must be finite.  T == 0 is a
  * no-op; n_groups == 1 ignores group_score.

@@ -76,6 +76,12 @@ struct Raw8 {
   }
 };
 
+// 1 / sqrt(mean + eps); 0 for a row of zeros without an eps, whose values then stay 0.
+__device__ __forceinline__ float rms_scale(float sum, const NormArgs& a) {
+  const float ms = sum / static_cast<float>(a.K) + a.eps;
+  return ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms);
+}
+
 // One 32-value block by a quad of lanes, eight values each: the steps and so
 // the bytes of q8_1_block_8lanes.  Lane part p writes bytes 4 + 8p .. 11 + 8p,
 // and the first and last the scale and the sum.
@@ -152,7 +158,7 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
       for (int k = 0; k < waves; ++k) sum += s_sum[first + k];
       __syncthreads();  // before the next row's
     }
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
+    const float rstd = rms_scale(sum, a);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * a.row_threads + tid;
@@ -211,7 +217,7 @@ __global__ __launch_bounds__(1024) void rms_norm_q8_1_long_kernel(NormArgs a, in
     sum = 0.0f;
     for (int k = 0; k < 16; ++k) sum += s_sum[k];
     __syncthreads();
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
+    const float rstd = rms_scale(sum, a);
     for (int64_t i = threadIdx.x; i < n4; i += 1024) {
       const float4 h = a.res ? load4(res_type, a.res_out, row4 + i) : load4(x_type, a.x, row4 + i);
       const float4 w = load4(a.w_type, a.w, i);

@@ -601,7 +601,7 @@ extern "C" int moe_router(const void* logits, int type, int64_t T, int64_t E, in
   if (!known_type(type) || (scoring != QMM_SCORE_SOFTMAX && scoring != QMM_SCORE_SIGMOID) ||
       (group_score != QMM_GROUP_MAX && group_score != QMM_GROUP_TOP2))
     return QMM_ERR_UNSUPPORTED;
-  if (T < 0 || T > (int64_t{1} << 26) || E < 1 || E > kMoeMaxE || n_groups < 1 || n_groups > kRouterMaxGroups ||
+  if (T < 0 || T > (int64_t{1} << 25) || E < 1 || E > kMoeMaxE || n_groups < 1 || n_groups > kRouterMaxGroups ||
       (E % n_groups) != 0 || topk_groups < 1 || topk_groups > n_groups || top_k < 1 || top_k > kRouterMaxTopK ||
       top_k > topk_groups * (E / n_groups))
     return QMM_ERR_SHAPE;

@@ -60,7 +60,7 @@ def test_router_errors():
     assert router(sc=2) == _lib.QMM_ERR_UNSUPPORTED
     assert router(gs=2) == _lib.QMM_ERR_UNSUPPORTED
     for kw in (dict(E=0), dict(E=513), dict(k=0), dict(k=65), dict(E=4, k=5), dict(g=0), dict(g=3), dict(g=65, E=65),
-               dict(g=8, kg=0), dict(g=8, kg=9), dict(g=8, kg=1, k=9), dict(T=-1), dict(T=(1 << 26) + 1)):
+               dict(g=8, kg=0), dict(g=8, kg=9), dict(g=8, kg=1, k=9), dict(T=-1), dict(T=(1 << 25) + 1)):
         assert router(**kw) == _lib.QMM_ERR_SHAPE, kw
     for p in ("x", "i", "w"):
         assert router(**{p: NUL}) == _lib.QMM_ERR_NULL

@@ -127,6 +127,29 @@ def test_edge_rows():
     check(6, K, F16, F16, F16, x=torch.randn(6, K, generator=torch.Generator().manual_seed(2)).half(), eps=0.0)
 
 
+@pytest.mark.parametrize("K", [64, 4096, 40960])
+def test_rows_of_zeros_without_eps(K):
+    x = torch.zeros(3, K, device=DEV)
+    x[1] = torch.linspace(-2, 3, K, device=DEV)
+    xq, ro, y = qmm.rms_norm_q8_1(x, torch.ones(K, device=DEV), 0.0, residual=torch.zeros_like(x).half(), y_dtype=F32)
+    assert torch.all(y[[0, 2]] == 0) and torch.all(xq[[0, 2]] == 0)
+    n = oracle.rms_norm(ro[1:2].double().cpu().numpy(), np.ones(K), 0.0)
+    assert np.all(np.abs(host(y)[1] - n[0]) <= tolerance(K) * np.abs(n[0]))
+
+
+def test_more_rows_than_workgroups():
+    # rows of one block, past the launch's workgroups of four and eight rows
+    T = (1 << 22) + 5
+    x = torch.randn(T, 32, device=DEV, generator=torch.Generator(DEV).manual_seed(3)).bfloat16()
+    w = torch.ones(32, device=DEV)
+    xq, _, _ = qmm.rms_norm_q8_1(x, w)
+    tail, _, _ = qmm.rms_norm_q8_1(x[-1000:], w)
+    head, _, _ = qmm.rms_norm_q8_1(x[:1000], w)
+    assert torch.equal(xq[-1000:], tail) and torch.equal(xq[:1000], head)
+    back = qmm.q8_1_dequantize(xq, BF16)
+    assert torch.equal(back[-1000:], qmm.q8_1_dequantize(tail, BF16))
+
+
 def test_empty_and_refused():
     w = torch.ones(64, device=DEV)
     xq, ro, y = qmm.rms_norm_q8_1(torch.empty(0, 64, device=DEV), w, residual=torch.empty(0, 64, device=DEV), y_dtype=F16)
