@@ -110,7 +110,7 @@ __device__ __forceinline__ void q8_1_block_4lanes(const float (&v)[8], int part,
     *reinterpret_cast<uint32_t*>(dst + (part ? 36 : 0)) = part ? static_cast<uint32_t>(s) : f2h_bits(d);
 }
 
-template <int XT, int RT, int WT, int C>
+template <int XT, int RT, int WT, int C, bool LATE>
 __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
   const int64_t n8 = a.K / 8;
   const int tid = threadIdx.x % a.row_threads;
@@ -127,7 +127,7 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
       if (on && i < n8) {
         x[c].load(a.x, at + i);
         if constexpr (RT != kNoType) r[c].load(a.res, at + i);
-        w[c].load(a.w, i);
+        if constexpr (!LATE) w[c].load(a.w, i);
       }
     }
     float h[C][8], sum = 0.0f;
@@ -163,6 +163,7 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
     for (int c = 0; c < C; ++c) {
       const int i = c * a.row_threads + tid;
       if (on && i < n8) {
+        if constexpr (LATE) w[c].load(a.w, i);
         float n[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = h[c][j] * rstd * (w[c].get(j) + a.offset);
@@ -187,12 +188,15 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
   }
 }
 
-template <int XT, int RT, int C>
+// LATE: the weights are read after the sum, for fewer registers and so two
+// workgroups of more than 512 threads per CU (4096 x 11008, fp32: 57 us, 66
+// with the weights read with the row; 16384 x 8192 on 512 threads: 194 and 188).
+template <int XT, int RT, int C, bool LATE>
 __global__ __launch_bounds__(1024) void rms_norm_q8_1_kernel(NormArgs a) {
   __shared__ float s_sum[16];
-  if (a.w_type == QMM_F32) norm_rows<XT, RT, QMM_F32, C>(a, s_sum);
-  else if (a.w_type == QMM_F16) norm_rows<XT, RT, QMM_F16, C>(a, s_sum);
-  else norm_rows<XT, RT, QMM_BF16, C>(a, s_sum);
+  if (a.w_type == QMM_F32) norm_rows<XT, RT, QMM_F32, C, LATE>(a, s_sum);
+  else if (a.w_type == QMM_F16) norm_rows<XT, RT, QMM_F16, C, LATE>(a, s_sum);
+  else norm_rows<XT, RT, QMM_BF16, C, LATE>(a, s_sum);
 }
 
 // Rows of more than 32768 values: read again after the sum.
@@ -240,9 +244,10 @@ static void launch_norm(NormArgs a, hipStream_t st) {
   const int threads = std::max(256, a.row_threads), rows = a.K <= 2048 ? 256 / a.row_threads : 1;
   a.row_threads = a.K <= 2048 ? a.row_threads : threads;
   const dim3 g(static_cast<unsigned>(std::min((a.T + rows - 1) / rows, kMaxGrid))), b(threads);
-  if (chunks == 1) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 1>), g, b, 0, st, a);
-  else if (chunks == 2) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 2>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 4>), g, b, 0, st, a);
+  if (chunks == 1) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 1, false>), g, b, 0, st, a);
+  else if (chunks == 2 && threads <= 512) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 2, false>), g, b, 0, st, a);
+  else if (chunks == 2) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 2, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 4, true>), g, b, 0, st, a);
 }
 
 template <int XT>
