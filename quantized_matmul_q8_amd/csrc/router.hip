@@ -34,7 +34,7 @@ struct RouterArgs {
   int64_t T;
   int type, E, top_k, scoring, groups, keep, group_score, renorm;
   float scale;
-  uint32_t magic;  // ceil(2^32 / (E / groups))
+  uint32_t magic;  // ceil(2^20 / (E / groups))
 };
 
 __device__ __forceinline__ float load1(int type, const void* p, int64_t i) {
@@ -312,7 +312,6 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   // with groups, per wave a float per token and expert, or route_token's double per expert
   extern __shared__ double s_values[];
   __shared__ float s_group[kRouterWaves][4][kRouterMaxGroups];
-  __shared__ int s_kept[kRouterWaves][4][kRouterMaxGroups];
   __shared__ int2 s_cand[kRouterWaves][2][4][17];  // the 17th takes what is no candidate
   const int lane = threadIdx.x & 63, li = lane & 15, tok = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -386,7 +385,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
 
   const float kappa = softmax ? 56.0f : 3.0f;
   bool unsure = false;  // of the groups
-  uint32_t kept = ~0u;  // bit v: expert v*16 + li is in a kept group
+  uint32_t inside = 0;  // bit v: expert v*16 + li is in a kept group
   if (a.groups > 1) {
     const int per = a.E / a.groups;
     int span = 1;  // lanes that share a group
@@ -399,13 +398,16 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
     for (int g0 = 0; g0 < a.groups; g0 += 16) {
       const int g = g0 + li / span;
       float b0 = -INFINITY, b1 = -INFINITY;
+      const auto take = [&](int i) {
+        const float p = mine[g * per + i];
+        b1 = fmaxf(b1, fminf(b0, p));
+        b0 = fmaxf(b0, p);
+      };
       if (g < a.groups) {
+        const int all = per / span, first = li % span;  // rounds that every lane of a group has
 #pragma unroll 8
-        for (int i = li % span; i < per; i += span) {
-          const float p = mine[g * per + i];
-          b1 = fmaxf(b1, fminf(b0, p));
-          b0 = fmaxf(b0, p);
-        }
+        for (int i = 0; i < all; ++i) take(first + i * span);
+        if (first < per - all * span) take(first + all * span);
       }
       for (int d = 1; d < span; d <<= 1) {
         const float o0 = __shfl_xor(b0, d), o1 = __shfl_xor(b1, d);
@@ -416,31 +418,31 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
     }
     wave_fence();
     float low = INFINITY, high = -INFINITY;  // of the kept, of the others
-    for (int g = li; g < a.groups; g += 16) {
-      const float mine = s_group[wave][tok][g];
+    uint64_t kept = 0;                       // bit g: group g of the token
+    for (int g0 = 0; g0 < a.groups; g0 += 16) {
+      const int g = g0 + li;
+      const float mine = s_group[wave][tok][min(g, a.groups - 1)];
       int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < a.groups; ++j) {
         const float o = s_group[wave][tok][j];
         rank += o > mine || (o == mine && j < g) ? 1 : 0;
       }
-      const bool in = rank < a.keep;
-      s_kept[wave][tok][g] = in;
+      const bool in = g < a.groups && rank < a.keep;
+      kept |= (__ballot(in) >> (lane & 48) & 0xffff) << g0;
       if (in) low = fminf(low, mine);
-      else high = fmaxf(high, mine);
+      else if (g < a.groups) high = fmaxf(high, mine);
     }
-    wave_fence();
     low = row_reduce_f(low, fmin2);
     high = row_reduce_f(high, fmax2);
     // two scores' errors (s <= 1) and their sum's on either side; groups without unmasked experts tie exactly
     if (scored && high > -INFINITY)
       unsure = !(low - high > 0x1p-23f * (2.0f + 2.0f * kappa + 2.0f * (fabsf(low) + fabsf(high))));
-    kept = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = min(v * 16 + li, a.E - 1);
-      const int g = per == 1 ? e : static_cast<int>(__umulhi(static_cast<uint32_t>(e), a.magic));
-      kept |= (s_kept[wave][tok][g] ? 1u : 0u) << v;
+      // e / per: exact, for e times the multiplier's error is below 2^9 * 2^9
+      const uint32_t g = __umul24(static_cast<uint32_t>(v * 16 + li), a.magic) >> 20;
+      inside |= static_cast<uint32_t>(kept >> (g & 63) & 1) << v;
     }
   }
   int key[V];
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   }
   if (a.groups > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = kept >> v & 1 ? key[v] : kTaken;
+    for (int v = 0; v < V; ++v) key[v] = inside >> v & 1 ? key[v] : kTaken;
   }
 
   // lane j < n gets the j-th best
@@ -608,9 +610,9 @@ extern "C" int moe_router(const void* logits, int type, int64_t T, int64_t E, in
   if (T == 0) return QMM_OK;
   if (!logits || !ids || !weights) return QMM_ERR_NULL;
   if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return QMM_ERR_ALIGN;
-  const uint64_t per = static_cast<uint64_t>(E / n_groups);
+  const uint32_t per = static_cast<uint32_t>(E / n_groups);
   const RouterArgs a{logits, bias, ids, weights, T, type, static_cast<int>(E), static_cast<int>(top_k), scoring,
-                     static_cast<int>(n_groups), static_cast<int>(topk_groups), group_score, renormalize, scale, static_cast<uint32_t>(((uint64_t{1} << 32) + per - 1) / per)};
+                     static_cast<int>(n_groups), static_cast<int>(topk_groups), group_score, renormalize, scale, static_cast<uint32_t>(((1u << 20) + per - 1) / per)};
   hipStream_t st = to_stream(stream);
   const dim3 block(kRouterWaves * 64);
   if (top_k + (bias ? 2 : 0) > 16) {
