@@ -15,12 +15,15 @@
 // rounds stay in flight per wave, across the ends of its tiles: 64 KB per CU
 // with 16 waves.  With few rows `split` waves share a tile by parts of K.
 //
-// Bound by HBM at one token, 28672 x 8192, groups of 32: 26.8 us, 4.9 TB/s
-// (a copy of 1 GiB reaches 5.1); 4096 x 11008, groups of 128 with zero points:
-// 7.6 us, 3.1 TB/s (start-up and the activations' copy are about 3 us of it).
+// Bound by HBM at one token, 28672 x 8192, groups of 32: 24 us, 5.5 TB/s (a
+// copy of 1 GiB reaches 5.1); 4096 x 11008, groups of 128 with zero points: 7.0
+// us, 3.4 TB/s (start-up and the activations' copy are about 3 us of it).
 // Every further token adds 13 VALU instructions per 2048 weights, 85 in all at
-// five tokens: 28672 x 8192 takes 29.3, 31.1, 36.4 and 48.7 us at 2, 3, 5 and
-// 8 tokens, where the instructions take 17 and 24 us of the last two.
+// five tokens: 28672 x 8192 takes 26, 28, 33 and 46 us at 2, 3, 5 and 8 tokens,
+// where the instructions take 17 and 24 us of the last two.  The weights are
+// read past the caches' usual order: 26.7 us otherwise at one token, where
+// they do not fit the last-level cache (32000 x 4096, which does three times:
+// 13.5 us, and 14.6 this way).
 //
 // Measured and not kept: the products on the matrix cores (16 x 16 x 64 with
 // four blocks kept apart by zeros, or 4 x 4 x 4 with the weights transposed
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
             const int64_t m = min(tile * kRows + r * kSub + (L == 64 ? 0 : sub), a.M - 1);
             const uint8_t* row = a.w + m * a.nblk * 16;
             const uint8_t* scales = static_cast<const uint8_t*>(a.scales) + m * a.groups * 2;
-            B.w[u][r] = ld16_a16(row + static_cast<uint32_t>(b * 16));
+            B.w[u][r] = ld16_nt(row + static_cast<uint32_t>(b * 16));
             B.s[u][r] = *reinterpret_cast<const uint16_t*>(scales + static_cast<uint32_t>(g * 2));
             if constexpr (ZEROS)
               B.z[u][r] = static_cast<uint32_t>(a.zeros[m * zrow + static_cast<uint32_t>(g >> 1)]) >> (4 * (g & 1));

@@ -11,7 +11,7 @@
 // depends on K alone, so its result does not depend on T.
 //
 // Bound by HBM: 16384 x 8192, bf16 with a bf16 residual, 7.25 bytes a value:
-// 186 us, 5.2 TB/s (a copy of 1 GiB reaches 5.1); reading the row again after
+// 179 us, 5.4 TB/s (a copy of 1 GiB reaches 5.1); reading the row again after
 // the sum took 306 us.  A few rows are bound by the launch and three round
 // trips (1 x 4096: 3.0 us).  Reading 8192 x 11008 back to bf16: 44.5 us, 6.6
 // TB/s (part of it from the last-level cache), to fp32 81 us, 5.9 TB/s.
@@ -35,6 +35,7 @@ struct NormArgs {
   float offset, eps;
   int64_t T, K;
   int row_threads;  // 64, or the workgroup's threads
+  bool large;       // the stream is larger than what the last-level cache (256 MB) would keep of it
 };
 
 // Eight values 8i .. 8i + 7 as they are stored.
@@ -45,6 +46,23 @@ struct Raw8 {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) v[k] = static_cast<const uint4*>(p)[i * kWords + k];
+  }
+  // Data that is read once.  Only 16-bit values: the two loads of eight fp32 ones touch the same lines, and the second
+  // would miss (16384 x 4096, bf16: 93 -> 87 us; 4096 x 11008, fp32: 57 -> 64).
+  __device__ __forceinline__ void load_once(const void* p, int64_t i) {
+    if constexpr (kWords == 1) v[0] = ld16_nt(static_cast<const uint4*>(p) + i);
+    else load(p, i);
+  }
+  __device__ __forceinline__ void store_nt(void* p, int64_t i) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      v4u t;
+      t.x = v[k].x;
+      t.y = v[k].y;
+      t.z = v[k].z;
+      t.w = v[k].w;
+      __builtin_nontemporal_store(t, static_cast<v4u*>(p) + i * kWords + k);
+    }
   }
   __device__ __forceinline__ void store(void* p, int64_t i) const {
 #pragma unroll
@@ -125,8 +143,8 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
     for (int c = 0; c < C; ++c) {
       const int i = c * a.row_threads + tid;
       if (on && i < n8) {
-        x[c].load(a.x, at + i);
-        if constexpr (RT != kNoType) r[c].load(a.res, at + i);
+        x[c].load_once(a.x, at + i);
+        if constexpr (RT != kNoType) r[c].load_once(a.res, at + i);
         if constexpr (!LATE) w[c].load(a.w, i);
       }
     }
@@ -141,7 +159,8 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] += r[c].get(j);
           r[c].set(h[c]);
-          r[c].store(a.res_out, at + i);
+          if (a.large) r[c].store_nt(a.res_out, at + i);
+          else r[c].store(a.res_out, at + i);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] = r[c].get(j);
         }
@@ -236,7 +255,8 @@ __global__ __launch_bounds__(1024) void rms_norm_q8_1_long_kernel(NormArgs a, in
 template <int XT, int RT>
 static void launch_norm(NormArgs a, hipStream_t st) {
   // Threads per row, by K alone: eight values each up to 4096 (1 x 4096: 3.0 us; with sixteen 3.4, but 16384 x 4096
-  // 93 and 91 us), then sixteen (16384 x 8192: 186 us, with eight 191, with 32 229), and 32 where a workgroup is full.
+  // 93 and 91 us), then sixteen (16384 x 8192: 186 us, with eight 191, with 32 229; all with plain loads), and 32 where a
+  // workgroup is full.
   // Up to 2048 values a workgroup has several rows.
   const int chunks = a.K <= 4096 ? 1 : a.K <= 16384 ? 2 : 4;
   a.row_threads = a.K <= 512 ? 64 : a.K <= 1024 ? 128 : a.K <= 2048 ? 256
@@ -313,7 +333,10 @@ extern "C" int rms_norm_q8_1(const void* x, int x_type, const void* residual, vo
       !aligned16(y))
     return QMM_ERR_ALIGN;
   const NormArgs a{x, residual, residual_out, weight, static_cast<uint8_t*>(xq), y, w_type, y_type, weight_offset, eps,
-                   T, K, 0};
+                   T, K, 0,
+                   // its stores then leave the caches to the other data (4096 x 24576, bf16: 175 -> 143 us; 16384 x 8192:
+                   // 186 -> 181); a smaller one the next kernel finds there
+                   T * K >= (int64_t{128} << 20) / (res_type == QMM_F32 ? 4 : 2)};
   hipStream_t st = to_stream(stream);
   if (K > 32768)
     hipLaunchKernelGGL(rms_norm_q8_1_long_kernel, dim3(static_cast<unsigned>(std::min(T, kMaxGrid))), dim3(1024), 0, st,
