@@ -300,8 +300,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // with log2 e, exp2, a sum with chains of V + 4 <= 36, its terms' errors, the
 // division), and s * 2.5 |x - max| <= 1; sigmoid, 1/(1+e): s (1 - s) times e's
 // relative error (1.5 |x| + 2) * 2^-24, and 3 s * 2^-24 of sum and reciprocal,
-// with s (1 - s) |x| < 0.23.  So |error of c| <= (1 + kappa s + |c|) * 2^-24
-// with kappa 56 and 3.  Neighbours of the first top_k + 1 that are closer than
+// with s (1 - s) |x| < 0.23.  So |error of c| <= (1 + kappa + |c|) * 2^-24 with
+// kappa 56 times the largest probability, and 3.  Neighbours of the first top_k + 1 that are closer than
 // both errors, or groups at the border of the kept, make the token unsure.
 // The n best then get their exponentials in 64 bits and are ranked again; if
 // that leaves a doubt (the softmax's sum, still in 32 bits; the n-th, whose
@@ -383,7 +383,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
     for (int v = 0; v < V; ++v) c[v] = x[v];
   }
 
-  const float kappa = softmax ? 56.0f : 3.0f;
+  // no score is larger: 1/sum is the largest logit's
+  const float kappa = softmax ? 56.0f * inv : 3.0f;
   bool unsure = false;  // of the groups
   uint32_t inside = 0;  // bit v: expert v*16 + li is in a kept group
   if (a.groups > 1) {
@@ -435,7 +436,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
     }
     low = row_reduce_f(low, fmin2);
     high = row_reduce_f(high, fmax2);
-    // two scores' errors (s <= 1) and their sum's on either side; groups without unmasked experts tie exactly
+    // two scores' errors and their sum's on either side; groups without unmasked experts tie exactly
     if (scored && high > -INFINITY)
       unsure = !(low - high > 0x1p-23f * (2.0f + 2.0f * kappa + 2.0f * (fabsf(low) + fabsf(high))));
 #pragma unroll
@@ -481,8 +482,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   if (!__any(all > 16)) {
     int at = upto - count;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-    {
+    for (int v = 0; v < V; ++v) {
       const bool in = key[v] >= bound;
       cand[in ? at : 16] = make_int2(key[v], v * 16 + li);
       at += in ? 1 : 0;
@@ -528,17 +528,16 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
 
   rank = li;
   if (biased) {
-    const float now = key_value(my_key), b = a.bias[min(my_id, a.E - 1)], score = now - b;
-    const float next = row_shl1(now), next_s = row_shl1(score);
+    const float now = key_value(my_key), b = a.bias[min(my_id, a.E - 1)], next = row_shl1(now);
     const bool next_live = row_shl1(live ? 1.0f : 0.0f) > 0.0f;
-    const float margin = 0x1p-23f * (1.0f + kappa * fmaxf(score, next_s) + fmaxf(fabsf(now), fabsf(next)));
+    const float margin = 0x1p-23f * (1.0f + kappa + fmaxf(fabsf(now), fabsf(next)));
     const bool close = li < a.top_k && live && next_live && !(now - next > margin);
     const uint64_t closes = __ballot(close);
     if (closes) {  // any of the wave's tokens
       const bool token = (closes >> (lane & 48) & 0xffff) != 0;
       // The n best again, their exponentials in 64 bits; masked ones stay behind, in their order.  The softmax's sum keeps
-      // a relative error below kappa * 2^-24 =: r, which moves the difference of two values by r |s - s'|.
-      const double r = softmax ? 0x1p-24 * kappa : 0.0;
+      // a relative error below 56 * 2^-24 =: r, which moves the difference of two values by r |s - s'|.
+      const double r = softmax ? 0x1p-24 * 56.0 : 0.0;
       double score64 = 0.0, d = -1e300 * (li + 1) / 64;
       if (live) {
         score64 = softmax ? exp(static_cast<double>(mine_x) - static_cast<double>(ref)) / static_cast<double>(sum)
@@ -558,9 +557,9 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
       }
       // every expert that is not among the n has a 32-bit c of at most the n-th's
       const int last = (lane & 48) | (n - 1);
-      const float last_c = __shfl(now, last), last_s = __shfl(score, last);
+      const float last_c = __shfl(now, last);
       const bool last_live = __shfl(live ? 1 : 0, last) != 0;
-      const double above = static_cast<double>(last_c) + 0x1p-22 * (1.0 + kappa * fabs(last_s) + fabs(last_c));
+      const double above = static_cast<double>(last_c) + 0x1p-22 * (1.0 + kappa + fabs(last_c));
       const bool bad = token && live && place < a.top_k && (doubt || (last_live && !(d - r * score64 > above)));
       if (token) rank = place;
       unsure = unsure || (__ballot(bad) >> (lane & 48) & 0xffff) != 0;
@@ -612,7 +611,8 @@ extern "C" int moe_router(const void* logits, int type, int64_t T, int64_t E, in
   if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return QMM_ERR_ALIGN;
   const uint32_t per = static_cast<uint32_t>(E / n_groups);
   const RouterArgs a{logits, bias, ids, weights, T, type, static_cast<int>(E), static_cast<int>(top_k), scoring,
-                     static_cast<int>(n_groups), static_cast<int>(topk_groups), group_score, renormalize, scale, static_cast<uint32_t>(((1u << 20) + per - 1) / per)};
+                     static_cast<int>(n_groups), static_cast<int>(topk_groups), group_score, renormalize, scale,
+                     ((1u << 20) + per - 1) / per};
   hipStream_t st = to_stream(stream);
   const dim3 block(kRouterWaves * 64);
   if (top_k + (bias ? 2 : 0) > 16) {

@@ -124,6 +124,26 @@ def test_values_closer_than_fp32_resolves(E, groups, scoring):
         check(y, 2, scoring, None, groups, 1, "top2")
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_clusters_of_near_ties(scoring):
+    # a third of the experts within a few fp32 roundings of one value, from scores of all sizes
+    g = qmm_synth.rng(12)
+    E = 192
+    x = (g.standard_normal((24, E)) * 3).astype(np.float32)
+    x[1:] = x[0]
+    s = 1 / (1 + np.exp(-x[0].astype(np.float64)))
+    if scoring == "softmax":
+        s = np.exp(x[0].astype(np.float64))
+        s /= s.sum()
+    b = (g.standard_normal(E) * 0.1).astype(np.float32)
+    b[::3] = (1.25 - s[::3]).astype(np.float32)
+    for t in range(1, 24):                       # and the logits a few steps off
+        x[t, ::3] = (x[0, ::3].view(np.int32) + g.integers(-3, 4, size=E // 3).astype(np.int32)).view(np.float32)
+    for k in (1, 6, 14, 30):
+        check(x, k, scoring, b)
+        check(x, k, scoring, b, 8, 4, "top2", True)
+
+
 def test_masks():
     g = qmm_synth.rng(77)
     for E, groups, keep, k in [(128, 1, 1, 8), (64, 8, 3, 20), (10, 2, 1, 5), (512, 1, 1, 64), (300, 4, 2, 12)]:
