@@ -235,23 +235,20 @@ __global__ __launch_bounds__(1024) void mmvq_q4g_kernel(Q4gArgs a) {
     const auto load = [&](Batch<U, R>& B, int64_t tile, int it0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        {
-          const int j = (it0 + u) * L + li;
-          const int b = s0 + min(j, n - 1);
-          const int g = a.group_blk == 1 ? b : static_cast<int>(__umulhi(static_cast<uint32_t>(b), a.magic));
+        const int b = s0 + min((it0 + u) * L + li, n - 1);
+        const int g = a.group_blk == 1 ? b : static_cast<int>(__umulhi(static_cast<uint32_t>(b), a.magic));
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            // with L = 64 the row is the wave's: its addresses are scalar, the lane's part a 32-bit offset
-            const int64_t m = min(tile * kRows + r * kSub + (L == 64 ? 0 : sub), a.M - 1);
-            const uint8_t* row = a.w + m * a.nblk * 16;
-            const uint8_t* scales = static_cast<const uint8_t*>(a.scales) + m * a.groups * 2;
-            B.w[u][r] = ld16_nt(row + static_cast<uint32_t>(b * 16));
-            B.s[u][r] = *reinterpret_cast<const uint16_t*>(scales + static_cast<uint32_t>(g * 2));
-            if constexpr (ZEROS)
-              B.z[u][r] = static_cast<uint32_t>(a.zeros[m * zrow + static_cast<uint32_t>(g >> 1)]) >> (4 * (g & 1));
-            else
-              B.z[u][r] = 8u;
-          }
+        for (int r = 0; r < R; ++r) {
+          // with L = 64 the row is the wave's: its addresses are scalar, the lane's part a 32-bit offset
+          const int64_t m = min(tile * kRows + r * kSub + (L == 64 ? 0 : sub), a.M - 1);
+          const uint8_t* row = a.w + m * a.nblk * 16;
+          const uint8_t* scales = static_cast<const uint8_t*>(a.scales) + m * a.groups * 2;
+          B.w[u][r] = ld16_nt(row + static_cast<uint32_t>(b * 16));
+          B.s[u][r] = *reinterpret_cast<const uint16_t*>(scales + static_cast<uint32_t>(g * 2));
+          if constexpr (ZEROS)
+            B.z[u][r] = static_cast<uint32_t>(a.zeros[m * zrow + static_cast<uint32_t>(g >> 1)]) >> (4 * (g & 1));
+          else
+            B.z[u][r] = 8u;
         }
       }
     };

@@ -1,5 +1,5 @@
 // Values of 32 and 16 bits behind one type code (QMM_F32, QMM_F16, QMM_BF16):
-// widening loads and loads' inverse with one round-to-nearest-even.
+// widening loads, and stores rounded once to the nearest (ties to even).
 #pragma once
 
 #include "qmm_common.hpp"
@@ -35,12 +35,6 @@ __device__ __forceinline__ void store4(void* p, int64_t i, float4 v) {
   r.z = static_cast<one>(v.z);
   r.w = static_cast<one>(v.w);
   static_cast<typename Typed<TY>::four*>(p)[i] = r;
-}
-
-// v as it reads back after a store.
-template <int TY>
-__device__ __forceinline__ float rounded(float v) {
-  return static_cast<float>(static_cast<typename Typed<TY>::one>(v));
 }
 
 // The same with the type known only when the kernel runs (uniform over it).
