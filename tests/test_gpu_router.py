@@ -209,3 +209,42 @@ def test_buffers_and_refusals():
                 lambda: qmm.moe_router(torch.zeros(1, 513, device=DEV), 4)):
         with pytest.raises(qmm.QmmError):
             bad()
+
+
+def _near_equal_groups(g, T, groups, scoring):
+    """Probabilities or sigmoid scores [T, groups, 2] whose group sums are far apart but for groups 0 and 1 in the
+    middle, which are equal but for the logits' rounding; returned as float32 logits [T, 2 * groups]."""
+    want = np.empty((T, groups))
+    want[:, :2] = g.uniform(0.8, 1.2, size=(T, 1))
+    above = (groups - 2) // 2
+    want[:, 2:2 + above] = g.uniform(1.5, 1.8, size=(T, above))
+    want[:, 2 + above:] = g.uniform(0.1, 0.5, size=(T, groups - 2 - above))
+    first = want * g.uniform(0.45, 0.55, size=(T, groups))       # every score below 1
+    s = np.stack([first, want - first], -1)
+    if scoring == "softmax":
+        return np.log(s).reshape(T, -1).astype(np.float32)
+    return np.log(s / (1 - s)).reshape(T, -1).astype(np.float32)
+
+
+@pytest.mark.parametrize("B", [10.0, 30.0, 100.0, 1e3, 1e4])
+@pytest.mark.parametrize("groups", [2, 8])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_group_sums_of_biases_that_cancel(B, groups, scoring):
+    # a group's two terms c = s + B and s - B are rounded at the size of B, their sum is of the size of s
+    x = _near_equal_groups(qmm_synth.rng(int(B) + groups), 1500, groups, scoring)
+    b = np.zeros(2 * groups, np.float32)
+    b[0::4], b[1::4] = B, -B                             # every second group
+    check(x, 2, scoring, b, groups, groups // 2, "top2", True)
+    check(x, 1, scoring, -b, groups, groups // 2, "top2", dtype=torch.float32)
+
+
+def test_group_sums_past_fp32():
+    # two biases of the type's lowest value: their sum is below every fp32 value, but above a group that is masked
+    low = np.finfo(np.float32).min
+    x = np.array([[-np.inf, np.nan, 0.5, 0.25, -np.inf, -np.inf], [0.5, 0.25, 1.0, -1.0, 0.5, 0.5]], np.float32)
+    b = np.array([0, 0, low, low, 0, 0], np.float32)
+    for scoring in ("softmax", "sigmoid"):
+        for keep in (1, 2):
+            check(x, 2, scoring, b, 3, keep, "top2")
+            check(x, 2, scoring, -b, 3, keep, "top2", True)
+        check(x, 2, scoring, np.array([low, 0, low, low, 0, low], np.float32), 3, 1, "max")
