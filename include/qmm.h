@@ -267,7 +267,8 @@ int mmq_q6k_f32(const void* w, const float* x, float* y, int64_t M, int64_t K, i
  *          (QMM_GROUP_TOP2); the topk_groups best groups are kept
  *   ids    the top_k experts of the kept groups by c, in decreasing order
  *   weights s of the chosen (without the bias), divided by their sum if
- *          renormalize, times scale; fp32
+ *          renormalize, times scale; fp32.  The quotients are right for scores
+ *          below fp32's range too; where all are 0 in 64 bits they are 0
  * The order is that of c without rounding error (as in 64 bits; without a
  * bias the order of the logits), equal values in the order of the experts or
  * groups.  A logit of -inf (or NaN) masks its expert: score 0 and after all

@@ -94,6 +94,12 @@ __device__ __forceinline__ int64_t order_key(double c) {
   return k ^ ((k >> 63) & INT64_MAX);
 }
 
+// Sigmoid scores of logits below this are taken in 64 bits for their shares of
+// a sum: in fp32 they come near the subnormals (from -87.3), and from -88.7 on
+// exp(-x) is infinite and all of them 0.  route_token takes such tokens.
+constexpr float kSmallSigmoid = -80.0f;
+__device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-static_cast<double>(x))); }
+
 // One token by the whole wave, its order in 64 bits.  Lane l holds experts l*V
 // .. l*V + V - 1 (V = ceil(E/64)): the lowest lane of several with the same
 // value has the lowest expert.  s_pick: a double per expert.
@@ -123,7 +129,7 @@ __device__ __noinline__ void route_token(RouterArgs a, int64_t t, double* s_pick
     pick[v] = static_cast<double>(x[v]);
     if (v < V && scored) {
       pick[v] = softmax ? exp(static_cast<double>(x[v]) - static_cast<double>(ref))
-                        : 1.0 / (1.0 + exp(-static_cast<double>(x[v])));
+                        : sigmoid64(x[v]);
       sum += pick[v];
     }
   }
@@ -238,7 +244,12 @@ __device__ __noinline__ void route_token(RouterArgs a, int64_t t, double* s_pick
   } else if (live) {
     w = 1.0f / (1.0f + expf(-my_x));
   }
-  if (a.renorm) {
+  if (a.renorm && !softmax && __any(live && my_x < kSmallSigmoid)) {
+    const double s = live ? sigmoid64(my_x) : 0.0;
+    double z = s;
+    for (int d = 32; d; d >>= 1) z += __shfl_xor(z, d);
+    w = z > 0.0 ? static_cast<float>(s / z) : 0.0f;
+  } else if (a.renorm) {
     const float z = wave_sum(w);
     if (z > 0.0f) w /= z;
   }
@@ -552,7 +563,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
       double score64 = 0.0, d = -1e300 * (li + 1) / 64;
       if (live) {
         score64 = softmax ? exp(static_cast<double>(mine_x) - static_cast<double>(ref)) / static_cast<double>(sum)
-                          : 1.0 / (1.0 + exp(-static_cast<double>(mine_x)));
+                          : sigmoid64(mine_x);
         d = score64 + static_cast<double>(b);
       }
       if (li >= n) d = -DBL_MAX;
@@ -581,25 +592,27 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   const bool chosen = rank < a.top_k && li < n;
   live = live && chosen;
   float w = 0.0f;
+  bool again = unsure;
   if (softmax) {
     const float at = a.renorm ? row_reduce_f(live ? mine_x : -INFINITY, fmax2) : top;
     if (live) w = expf(mine_x - at);
     if (!a.renorm && live) w /= sum;
   } else if (live) {
     w = 1.0f / (1.0f + expf(-mine_x));
+    if (a.renorm && mine_x < kSmallSigmoid) again = true;
   }
   if (a.renorm) {
     const float z = row_reduce_f(w, add2);
     if (z > 0.0f) w /= z;
   }
-  if (chosen && t0 + tok < a.T && !unsure) {
+  const uint64_t redo = __ballot(again);
+  if (chosen && t0 + tok < a.T && !(redo >> (lane & 48) & 0xffff)) {
     a.ids[t * a.top_k + rank] = my_id;
     a.weights[t * a.top_k + rank] = w * a.scale;
   }
-  const uint64_t again = __ballot(unsure);
-  if (again) {
+  if (redo) {
     for (int i = 0; i < 4; ++i)
-      if ((again >> (16 * i) & 1) && t0 + i < a.T) route_token(a, t0 + i, s_pick);
+      if ((redo >> (16 * i) & 0xffff) && t0 + i < a.T) route_token(a, t0 + i, s_pick);
   }
 }
 

@@ -248,3 +248,29 @@ def test_group_sums_past_fp32():
             check(x, 2, scoring, b, 3, keep, "top2")
             check(x, 2, scoring, -b, 3, keep, "top2", True)
         check(x, 2, scoring, np.array([low, 0, low, low, 0, low], np.float32), 3, 1, "max")
+
+
+@pytest.mark.parametrize("top_k", [4, 20])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_sigmoid_shares_of_small_scores(top_k, with_bias):
+    # scores below fp32's range, or among its subnormals, still have shares of their sum
+    g = qmm_synth.rng(9)
+    E = 64
+    x = np.empty((14, E), np.float32)
+    for i, v in enumerate([-50.0, -79.9, -80.1, -86.0, -88.0, -89.0, -95.0, -100.0, -104.0, -200.0, -700.0]):
+        x[i] = v + 0.5 * g.standard_normal(E)
+    x[7] = -100.0                                        # all equal
+    x[11] = -200.0
+    x[11, 4] = 88.0
+    x[12] = np.where(np.arange(E) % 2 == 0, -60.0, -101.0)
+    x[13] = -100.0
+    x[13, 9:] = -np.inf                                  # fewer than top_k = 20 left
+    b = (0.1 * g.standard_normal(E)).astype(np.float32) if with_bias else None
+    _, w = check(x, top_k, "sigmoid", b, renormalize=True, scale=2.0)
+    assert np.allclose(w.sum(1), 2.0, rtol=1e-5)
+    check(x, top_k, "sigmoid", b, 4, 3, "top2", True)
+    # a token's weights do not depend on its neighbours in the batch
+    ids, w = qmm.moe_router(dev(x), top_k, scoring="sigmoid", renormalize=True)
+    for t in range(14):
+        i1, w1 = qmm.moe_router(dev(x[t:t + 1]), top_k, scoring="sigmoid", renormalize=True)
+        assert torch.equal(i1[0], ids[t]) and torch.equal(w1[0], w[t])
