@@ -122,8 +122,8 @@ int q8_1_dequantize(const void* xq, void* x, int x_type, int64_t T, int64_t K, v
  * both NULL (res_type is then ignored), and may be the same buffer: the
  * stream is then updated in place.  No other buffers may overlap.  A row's
  * result depends on that row, K and the types alone, not on T.
- * Input must be finite, mean(h^2) below the fp32 range and |n| <= 127 * 65504.
- * A row of zeros gives zeros, with eps == 0 too.
+ * Input and h must be finite and |n| <= 127 * 65504; the squares may leave the
+ * fp32 range at either end.  A row of zeros gives zeros, with eps == 0 too.
  * Requires 0 <= T < 2^31, 0 < K <= 2^30, K % 32 == 0, eps >= 0.  T == 0 is a
  * no-op.
  */

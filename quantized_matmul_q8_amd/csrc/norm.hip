@@ -3,6 +3,7 @@
 //
 //   h = x (+ r, rounded to r's type: the stored residual stream)
 //   n = h * rstd * (w + offset),  rstd = 1 / sqrt(mean(h^2) + eps)
+//       (by powers of two where squares would leave fp32)
 //   xq = Q8_1(n) with the steps of q8_1_quantize;  y = n rounded to y's type
 //
 // A row stays in registers between the sum of its squares and its output: 64
@@ -94,7 +95,7 @@ struct Raw8 {
   }
 };
 
-// 1 / sqrt(mean + eps); 0 for a row of zeros without an eps, whose values then stay 0.
+// 1 / sqrt(mean + eps); 0 where the mean is 0 and there is no eps, and where it is infinite.
 __device__ __forceinline__ float rms_scale(float sum, const NormArgs& a) {
   const float ms = sum / static_cast<float>(a.K) + a.eps;
   return ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms);
@@ -128,8 +129,78 @@ __device__ __forceinline__ void q8_1_block_4lanes(const float (&v)[8], int part,
     *reinterpret_cast<uint32_t*>(dst + (part ? 36 : 0)) = part ? static_cast<uint32_t>(s) : f2h_bits(d);
 }
 
+// Whether a row has to be done again with its values scaled: where its mean
+// square + eps is past fp32 (rstd 0 or NaN) or below 2^-96, where squares come
+// near the subnormals (above it those that vanish move it by less than 2^-50).
+__device__ __forceinline__ bool is_odd(float rstd) { return !(rstd > 0.0f && rstd <= 0x1p48f); }
+
+__device__ __forceinline__ void load8(int type, const void* p, int64_t i, float (&v)[8]) {
+  const float4 lo = load4(type, p, 2 * i), hi = load4(type, p, 2 * i + 1);
+  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+}
+
+// Such a row once more, from memory: each wave sums all of it and writes its
+// part.  `by` multiplies the values and `sq` these again for their squares alone:
+//   past fp32: values of at most 2^124 then, squares of up to 2^64, 1/rms above
+//     2^-126; a value that loses bits has a result below 2^-126
+//   below 2^-96: up to 2^30 values below 2^-33 give a sum below 2^126, the
+//     smallest subnormal a square of 2^-106.
+__device__ __forceinline__ void odd_row(const NormArgs& a, int type, const void* from, int64_t row, int tid, bool past) {
+  __asm__ volatile("" : "+v"(tid));  // no address from it is worked out before the usual rows
+  const int64_t n8 = a.K / 8, at = row * n8;
+  const float by = past ? 0x1p-4f : 0x1p96f, sq = past ? 0x1p-92f : 1.0f, f = by * sq;
+  float h[8], sum = 0.0f;
+  for (int64_t i = tid & 63; i < n8; i += 64) {
+    load8(type, from, at + i, h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[j] * f, h[j] * f, sum);
+  }
+  const float ms = wave_sum(sum) / static_cast<float>(a.K) + a.eps * f * f;
+  // a row of zeros without an eps stays zeros
+  const float rstd = ms == 0.0f ? 0.0f : 1.0f / sqrtf(ms) * sq;
+  for (int64_t i = tid; i < n8; i += a.row_threads) {
+    float w[8];
+    load8(type, from, at + i, h);
+    load8(a.w_type, a.w, i, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = h[j] * by * rstd * (w[j] + a.offset);
+    if (a.y) {
+      store4(a.y_type, a.y, 2 * (at + i), make_float4(h[0], h[1], h[2], h[3]));
+      store4(a.y_type, a.y, 2 * (at + i) + 1, make_float4(h[4], h[5], h[6], h[7]));
+    }
+    q8_1_block_4lanes(h, static_cast<int>(i & 3), a.xq + ((at + i) >> 2) * kQ8Bytes);
+  }
+}
+
+// The odd ones among a workgroup's rows, each wave its own, found by their sums,
+// which are added up as norm_rows does.  A row's waves have waited for each
+// other's stores of the stream at the barriers there.  Behind all rows, for
+// within their loop this costs registers (4096 x 11008, fp32: 72 us for 57).
+__device__ __forceinline__ void odd_rows(const NormArgs& a, int type, const void* from, int wave) {
+  const int64_t n8 = a.K / 8;
+  const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), thread = wave * 64 + lane;
+  const int tid = thread % a.row_threads, rows = blockDim.x / a.row_threads;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + thread / a.row_threads; row < a.T;
+       row += static_cast<int64_t>(gridDim.x) * rows) {
+    float all = 0.0f;
+    for (int k = 0; k < a.row_threads; k += 64) {
+      float h[8], sum = 0.0f;
+      for (int64_t i = k + lane; i < n8; i += a.row_threads) {
+        load8(type, from, row * n8 + i, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[j], h[j], sum);
+      }
+      all += wave_sum(sum);
+    }
+    const float rstd = rms_scale(all, a);
+    if (is_odd(rstd)) odd_row(a, type, from, row, tid, !(all / static_cast<float>(a.K) + a.eps < INFINITY));
+  }
+}
+
+// True where a row of the wave is odd.
 template <int XT, int RT, int WT, int C, bool LATE>
-__device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
+__device__ __forceinline__ bool norm_rows(const NormArgs& a, float* s_sum) {
+  bool odd = false;
   const int64_t n8 = a.K / 8;
   const int tid = threadIdx.x % a.row_threads;
   const int rows = blockDim.x / a.row_threads;  // of the workgroup; above one where a wave has a row
@@ -204,7 +275,9 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
         q8_1_block_4lanes(n, i & 3, a.xq + ((at + i) >> 2) * kQ8Bytes);
       }
     }
+    odd = odd || (on && is_odd(rstd));
   }
+  return odd;
 }
 
 // LATE: the weights are read after the sum, for fewer registers and so two
@@ -213,13 +286,33 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, float* s_sum) {
 template <int XT, int RT, int C, bool LATE>
 __global__ __launch_bounds__(1024) void rms_norm_q8_1_kernel(NormArgs a) {
   __shared__ float s_sum[16];
-  if (a.w_type == QMM_F32) norm_rows<XT, RT, QMM_F32, C, LATE>(a, s_sum);
-  else if (a.w_type == QMM_F16) norm_rows<XT, RT, QMM_F16, C, LATE>(a, s_sum);
-  else norm_rows<XT, RT, QMM_BF16, C, LATE>(a, s_sum);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // not from the thread's number, a register more
+  const bool odd = a.w_type == QMM_F32   ? norm_rows<XT, RT, QMM_F32, C, LATE>(a, s_sum)
+                   : a.w_type == QMM_F16 ? norm_rows<XT, RT, QMM_F16, C, LATE>(a, s_sum)
+                                         : norm_rows<XT, RT, QMM_BF16, C, LATE>(a, s_sum);
+  if (odd) odd_rows(a, RT == kNoType ? XT : RT, RT == kNoType ? a.x : a.res_out, wave);
 }
 
-// Rows of more than 32768 values: read again after the sum.
-__global__ __launch_bounds__(1024) void rms_norm_q8_1_long_kernel(NormArgs a, int x_type, int res_type) {
+// One chunk per lane: up to 64 vector registers, so eight waves per SIMD if a
+// wave has at most 80 scalar ones (16384 x 4096, bf16: 85 us, 91 with more).
+// The same body, and no function for both, with which 16384 x 8192 took 186 us
+// for 183.
+template <int XT, int RT>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_num_sgpr(80))) void rms_norm_q8_1_short_kernel(NormArgs a) {
+  constexpr int C = 1;
+  constexpr bool LATE = false;
+  __shared__ float s_sum[16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // not from the thread's number, a register more
+  const bool odd = a.w_type == QMM_F32   ? norm_rows<XT, RT, QMM_F32, C, LATE>(a, s_sum)
+                   : a.w_type == QMM_F16 ? norm_rows<XT, RT, QMM_F16, C, LATE>(a, s_sum)
+                                         : norm_rows<XT, RT, QMM_BF16, C, LATE>(a, s_sum);
+  if (odd) odd_rows(a, RT == kNoType ? XT : RT, RT == kNoType ? a.x : a.res_out, wave);
+}
+
+// Rows of more than 32768 values: read again after the sum.  Scalar registers
+// as above (300 x 65536, bf16: 64 us, 101 with more than 80).
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_num_sgpr(80)))
+void rms_norm_q8_1_long_kernel(NormArgs a, int x_type, int res_type) {
   __shared__ float s_sum[16];
   const int64_t n4 = a.K / 4;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -249,6 +342,11 @@ __global__ __launch_bounds__(1024) void rms_norm_q8_1_long_kernel(NormArgs a, in
       if (a.y) store4(a.y_type, a.y, row4 + i, n);
       q8_1_block_8lanes(n, static_cast<int>(i & 7), a.xq + ((row4 + i) >> 3) * kQ8Bytes, true);
     }
+    if (is_odd(rstd)) {
+      __syncthreads();  // other threads wrote what this one writes again
+      odd_row(a, a.res ? res_type : x_type, a.res ? a.res_out : a.x, row, threadIdx.x,
+              !(sum / static_cast<float>(a.K) + a.eps < INFINITY));
+    }
   }
 }
 
@@ -264,7 +362,7 @@ static void launch_norm(NormArgs a, hipStream_t st) {
   const int threads = std::max(256, a.row_threads), rows = a.K <= 2048 ? 256 / a.row_threads : 1;
   a.row_threads = a.K <= 2048 ? a.row_threads : threads;
   const dim3 g(static_cast<unsigned>(std::min((a.T + rows - 1) / rows, kMaxGrid))), b(threads);
-  if (chunks == 1) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 1, false>), g, b, 0, st, a);
+  if (chunks == 1) hipLaunchKernelGGL((rms_norm_q8_1_short_kernel<XT, RT>), g, b, 0, st, a);
   else if (chunks == 2 && threads <= 512) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 2, false>), g, b, 0, st, a);
   else if (chunks == 2) hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 2, true>), g, b, 0, st, a);
   else hipLaunchKernelGGL((rms_norm_q8_1_kernel<XT, RT, 4, true>), g, b, 0, st, a);
@@ -333,7 +431,7 @@ extern "C" int rms_norm_q8_1(const void* x, int x_type, const void* residual, vo
       !aligned16(y))
     return QMM_ERR_ALIGN;
   const NormArgs a{x, residual, residual_out, weight, static_cast<uint8_t*>(xq), y, w_type, y_type, weight_offset, eps,
-                   T, K, 0,
+                   T, K, 1024,  // set by launch_norm for rows that stay in registers
                    // its stores then leave the caches to the other data (4096 x 24576, bf16: 175 -> 143 us; 16384 x 8192:
                    // 186 -> 181); a smaller one the next kernel finds there
                    T * K >= (int64_t{128} << 20) / (res_type == QMM_F32 ? 4 : 2)};

@@ -211,3 +211,37 @@ def test_dequantize_buffers_and_refusals():
         qmm.q8_1_dequantize(xq[..., :36].contiguous())
     with pytest.raises(TypeError):
         qmm.q8_1_dequantize(xq, torch.float64)
+
+
+@pytest.mark.parametrize("K", [64, 512, 768, 1024, 2048, 4096, 8192, 11008, 20000, 40960])
+@pytest.mark.parametrize("rt", [None, F32, BF16])
+def test_rows_whose_squares_leave_fp32(K, rt):
+    """Finite rows whose squares, or their sum, are above or below what fp32 holds, between ordinary rows."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(11, K, generator=g)
+    x[1] *= 2.0**60                       # from K = 512: the sum is past fp32, the mean is not
+    x[2] *= 2.0**63
+    x[4] *= 2.0**120                      # the mean is past fp32
+    x[5] = x[5].clamp(-1, 1) * 3e38
+    x[5, ::7] *= 2.0**-140                # and values far smaller in the same row
+    x[2, ::5] *= 2.0**-100
+    x[8, ::5] *= 2.0**-30
+    x[7] *= 2.0**-50
+    x[8] *= 2.0**-66                      # subnormal squares
+    x[9] *= 2.0**-75                      # squares below every fp32 value
+    x[10] = x[10].sign() * 2.0**(-133 if rt == BF16 else -149)       # the type's smallest
+    assert torch.all(x[10] != 0)
+    r = None if rt is None else torch.zeros(11, K, dtype=rt)
+    w = 1 + 0.2 * torch.randn(K, generator=g)
+    for eps in (0.0, 1e-38, 1e-6):
+        say("rms_norm_q8_1", f"K={K} residual={rt} eps={eps}")
+        xq, ro, y = qmm.rms_norm_q8_1(x.to(DEV), w.to(DEV), eps, residual=None if r is None else r.to(DEV), y_dtype=F32)
+        h = x if rt is None else ro.cpu()
+        assert rt is None or torch.equal(h, x.to(rt))
+        n = oracle.rms_norm(h.double().numpy(), w.double().numpy(), float(np.float32(eps)))
+        yh = host(y)
+        assert np.all(np.isfinite(n)) and np.all(np.abs(yh - n) <= tolerance(K) * np.abs(n) + 2.0**-126), eps
+        assert np.array_equal(host(xq), oracle.quantize_q8_1(yh))
+        for i in (0, 1, 3, 6, 9):         # an ordinary row's neighbours change nothing in it
+            a, _, b = qmm.rms_norm_q8_1(h[i:i + 1].to(DEV), w.to(DEV), eps, y_dtype=F32)
+            assert torch.equal(a[0], xq[i]) and torch.equal(b[0], y[i])
