@@ -120,3 +120,49 @@ def test_refusals():
         qmm.mmvq_q4g(w, s, xq.repeat(9, 1, 1))
     with pytest.raises(qmm.QmmError):
         qmm.mmvq_q4g(w, s, xq[:0])
+
+
+def check_tall(M, K, group, T, zeros, dtype=torch.float16):
+    """Many rows: copies of 67 different ones in a random order, so that the oracle works out 67."""
+    g = qmm_synth.rng(M + K + T)
+    w, s, z = qmm_synth.q4g_weights(g, 67, K, group, zeros)
+    pick = g.integers(0, 67, size=M)
+    xq = oracle.quantize_q8_1(qmm_synth.activations(g, T, K, 0.01))
+    say("mmvq_q4g", f"M={M} K={K} group={group} T={T} zeros={zeros} {dtype}")
+    at = dev(pick)
+    out = torch.full((T * M + 64,), 7.0, device=DEV)
+    y = qmm.mmvq_q4g(dev(w)[at], dev(s).to(dtype)[at], dev(xq), zeros=None if z is None else dev(z)[at],
+                     out=out[:T * M].view(T, M))
+    W, X = oracle.q4g_dequant(w, s, z), oracle.q8_1_dequant(xq)
+    ref, bound = oracle.dense(W, X)[:, pick], oracle.abs_bound(W, X)[:, pick]
+    assert np.all(np.abs(host(y) - ref) <= (K / 512 + 18) * 2.0**-24 * bound)
+    assert torch.all(out[T * M:] == 7)
+
+
+# two rows per lane: 64 lanes a row from 8192 rows on, 16 from 32768 (of 256 CUs); the last tile is not full
+@pytest.mark.parametrize("T", [2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("M,K,group", [(8195, 2048, 128), (32771, 256, 64), (32773, 1056, 32)])
+def test_two_rows_per_lane(T, M, K, group):
+    check_tall(M, K, group, T, zeros=T % 2 == 0, dtype=torch.bfloat16 if T == 3 else torch.float16)
+
+
+# activations in segments, and as many rows as leave each wave a whole one: the sums live over the segments
+@pytest.mark.parametrize("M,K,group,T", [(2100, 28672, 128, 8), (4099, 20000, 32, 8), (8195, 20000, 160, 8), (4097, 24576, 64, 6),
+                                         (2049, 114688, 128, 1), (32771, 16416, 32, 8)])
+def test_many_rows_over_segments(M, K, group, T):
+    check_tall(M, K, group, T, zeros=M % 2 == 1)
+
+
+@pytest.mark.parametrize("M,K", [(300, 4096), (8195, 2048), (37, 28672)])
+def test_a_token_alone(M, K):
+    # other variants than with eight, so within both calls' roundings
+    g = qmm_synth.rng(M)
+    w, s, z = qmm_synth.q4g_weights(g, 67, K, 128, True)
+    at = dev(g.integers(0, 67, size=M))
+    wd, sd, zd = dev(w)[at], dev(s).half()[at], dev(z)[at]
+    xq = oracle.quantize_q8_1(qmm_synth.activations(g, 8, K))
+    y = host(qmm.mmvq_q4g(wd, sd, dev(xq), zeros=zd))
+    bound = oracle.abs_bound(oracle.q4g_dequant(w, s, z), oracle.q8_1_dequant(xq))[:, host(at)]
+    for t in range(8):
+        one = host(qmm.mmvq_q4g(wd, sd, dev(xq[t:t + 1]), zeros=zd))
+        assert np.all(np.abs(one[0] - y[t]) <= 2 * (K / 512 + 18) * 2.0**-24 * bound[t])
