@@ -245,3 +245,39 @@ def test_rows_whose_squares_leave_fp32(K, rt):
         for i in (0, 1, 3, 6, 9):         # an ordinary row's neighbours change nothing in it
             a, _, b = qmm.rms_norm_q8_1(h[i:i + 1].to(DEV), w.to(DEV), eps, y_dtype=F32)
             assert torch.equal(a[0], xq[i]) and torch.equal(b[0], y[i])
+
+
+@pytest.mark.parametrize("K", [64, 768, 2080, 4096, 11008, 20000, 40960])
+@pytest.mark.parametrize("rt", [F32, F16, BF16])
+def test_stream_updated_in_place(K, rt):
+    x, r, w = (t.to(DEV) for t in inputs(7, K, F32, rt, F32, K))
+    x[2], r[2] = 2.0**-70 * x[2], 0      # with eps = 0 rows that are read again from the updated stream
+    if rt != F16:
+        x[5], r[5] = 2.0**100 * x[5], 0
+    for eps in (1e-6, 0.0):
+        say("rms_norm_q8_1", f"in place K={K} residual={rt} eps={eps}")
+        xq, ro, y = qmm.rms_norm_q8_1(x, w, eps, residual=r, y_dtype=F32)
+        stream = r.clone()
+        a, b, c = qmm.rms_norm_q8_1(x, w, eps, residual=stream, residual_out=stream, y_dtype=F32)
+        assert b.data_ptr() == stream.data_ptr()
+        assert torch.equal(ro, (x + r.float()).to(rt)) and torch.equal(stream, ro)
+        assert torch.equal(a, xq) and torch.equal(c, y)
+
+
+# streams of 128 MB and more are stored past the caches; rows of such a call are those of smaller ones
+@pytest.mark.parametrize("T,K,rt", [(8195, 4096, F32), (16389, 4096, BF16), (8197, 8192, F16), (2051, 16416, F32)])
+def test_large_streams(T, K, rt):
+    g = torch.Generator(DEV).manual_seed(K)
+    x = torch.randn(T, K, device=DEV, generator=g).to(rt)
+    r = (2 * torch.randn(T, K, device=DEV, generator=g)).to(rt)
+    w = 1 + 0.2 * torch.randn(K, device=DEV, generator=g)
+    assert T * K * r.element_size() >= 1 << 27
+    say("rms_norm_q8_1", f"large T={T} K={K} {rt}")
+    xq, ro, _ = qmm.rms_norm_q8_1(x, w, residual=r)
+    assert torch.equal(ro, (x.float() + r.float()).to(rt))
+    for i in range(0, T, 1000):
+        a, b, _ = qmm.rms_norm_q8_1(x[i:i + 1000], w, residual=r[i:i + 1000])
+        assert torch.equal(a, xq[i:i + 1000]) and torch.equal(b, ro[i:i + 1000])
+    stream = r.clone()
+    a, b, _ = qmm.rms_norm_q8_1(x, w, residual=stream, residual_out=stream)
+    assert torch.equal(a, xq) and torch.equal(stream, ro)
