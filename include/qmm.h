@@ -278,8 +278,9 @@ int mmq_q6k_f32(const void* w, const float* x, float* y, int64_t M, int64_t K, i
  * the largest finite fp32 value.
  * Requires 0 <= T <= 2^25, 1 <= E <= 512, 1 <= n_groups <= 64, E % n_groups
  * == 0, 1 <= topk_groups <= n_groups, 1 <= top_k <= min(64, topk_groups * E /
- * n_groups); 16-byte aligned pointers.  bias must be finite.  T == 0 is a
- * no-op; n_groups == 1 ignores group_score.
+ * n_groups); 16-byte aligned pointers.  bias must be finite (with any
+ * other the ids are in range and differ, in an order that is not specified).
+ * T == 0 is a no-op; n_groups == 1 ignores group_score.
  */
 int moe_router(const void* logits, int type, int64_t T, int64_t E, int64_t top_k, int scoring, const float* bias,
                int64_t n_groups, int64_t topk_groups, int group_score, int renormalize, float scale, int32_t* ids,

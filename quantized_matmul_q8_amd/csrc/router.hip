@@ -582,7 +582,9 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
       const float last_c = __shfl(now, last);
       const bool last_live = __shfl(live ? 1 : 0, last) != 0;
       const double above = static_cast<double>(last_c) + 0x1p-22 * (1.0 + kappa + fabs(last_c));
-      const bool bad = token && live && place < a.top_k && (doubt || (last_live && !(d - r * score64 > above)));
+      // a bias that is not finite has no place among the others
+      const bool bad = token && live && (!(fabs(d) < DBL_MAX) ||
+                                         (place < a.top_k && (doubt || (last_live && !(d - r * score64 > above)))));
       if (token) rank = place;
       unsure = unsure || (__ballot(bad) >> (lane & 48) & 0xffff) != 0;
     }
@@ -592,7 +594,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
   const bool chosen = rank < a.top_k && li < n;
   live = live && chosen;
   float w = 0.0f;
-  bool again = unsure;
+  // NaNs of some bits have the key of what is taken
+  bool again = unsure || (li < a.top_k && my_key == kTaken);
   if (softmax) {
     const float at = a.renorm ? row_reduce_f(live ? mine_x : -INFINITY, fmax2) : top;
     if (live) w = expf(mine_x - at);

@@ -274,3 +274,25 @@ def test_sigmoid_shares_of_small_scores(top_k, with_bias):
     for t in range(14):
         i1, w1 = qmm.moe_router(dev(x[t:t + 1]), top_k, scoring="sigmoid", renormalize=True)
         assert torch.equal(i1[0], ids[t]) and torch.equal(w1[0], w[t])
+
+
+@pytest.mark.parametrize("E,groups,keep,top_k", [(8, 1, 1, 8), (8, 1, 1, 6), (6, 2, 1, 3), (64, 1, 1, 6), (96, 8, 2, 14), (512, 4, 3, 9), (100, 1, 1, 40)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_ids_stay_in_range_whatever_the_bias(E, groups, keep, top_k, scoring):
+    # ids go on to calls that cannot check them
+    g = qmm_synth.rng(E)
+    x = dev((g.standard_normal((21, E)) * 2).astype(np.float32))
+    x[3, ::2] = -np.inf
+    bits = np.array([0x7FC00000, 0xFFC00000, 0xFFFFFFFF, 0xFFFFFE00, 0x7F800001, 0x7F800000, 0xFF800000], np.uint32).view(np.float32)
+    for share in (0.1, 0.5, 1.0):
+        for one in (None, *range(len(bits))):
+            b = (0.1 * g.standard_normal(E)).astype(np.float32)
+            odd = g.random(E) < share
+            b[odd] = bits[g.integers(0, len(bits), size=odd.sum()) if one is None else one]
+            say("moe_router", f"E={E} groups={groups}/{keep} top_k={top_k} {scoring} odd biases {odd.sum()} kind {one}")
+            for score in ("max", "top2"):
+                ids = torch.full((21, top_k), 1 << 30, dtype=torch.int32, device=DEV)
+                qmm.moe_router(x, top_k, scoring=scoring, bias=dev(b), n_groups=groups, topk_groups=keep, group_score=score,
+                               renormalize=True, ids=ids)
+                ids = host(ids)
+                assert ids.min() >= 0 and ids.max() < E and all(len(set(r)) == top_k for r in ids.tolist())
