@@ -16,14 +16,14 @@
 // with 16 waves.  With few rows `split` waves share a tile by parts of K.
 //
 // Bound by HBM at one token, 28672 x 8192, groups of 32: 24 us, 5.5 TB/s (a
-// copy of 1 GiB reaches 5.1); 4096 x 11008, groups of 128 with zero points: 7.0
-// us, 3.4 TB/s (start-up and the activations' copy are about 3 us of it).
-// Every further token adds 13 VALU instructions per 2048 weights, 85 in all at
-// five tokens: 28672 x 8192 takes 26, 28, 33 and 46 us at 2, 3, 5 and 8 tokens,
-// where the instructions take 17 and 24 us of the last two.  The weights are
-// read past the caches' usual order: 26.7 us otherwise at one token, where
-// they do not fit the last-level cache (32000 x 4096, which does three times:
-// 13.5 us, and 14.6 this way).
+// copy of 1 GiB reaches 5.1); 4096 x 11008, groups of 128 with zero points: 6.9
+// us, 3.4 TB/s (the start and the end of a launch that short; mmvq_q4k reads a
+// tenth more in 6.2).  28672 x 8192 takes 25, 28, 34 and 48 us at 2, 3, 5 and 8
+// tokens; 57, 74, 108 and 156 VALU instructions per 2048 weights (all of the
+// kernel's, counted) are 12, 15, 22 and 32 us of them.  The weights are read
+// past the caches' usual order: 26.7 us otherwise at one token, where they do
+// not fit the last-level cache (32000 x 4096, which does three times: 13.5 us,
+// and 14.4 this way).
 //
 // Measured and not kept: the products on the matrix cores (16 x 16 x 64 with
 // four blocks kept apart by zeros, or 4 x 4 x 4 with the weights transposed

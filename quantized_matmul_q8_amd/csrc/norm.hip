@@ -12,10 +12,11 @@
 // depends on K alone, so its result does not depend on T.
 //
 // Bound by HBM: 16384 x 8192, bf16 with a bf16 residual, 7.25 bytes a value:
-// 179 us, 5.4 TB/s (a copy of 1 GiB reaches 5.1); reading the row again after
+// 180 us, 5.4 TB/s (a copy of 1 GiB reaches 5.1); reading the row again after
 // the sum took 306 us.  A few rows are bound by the launch and three round
 // trips (1 x 4096: 3.0 us).  Reading 8192 x 11008 back to bf16: 44.5 us, 6.6
-// TB/s (part of it from the last-level cache), to fp32 81 us, 5.9 TB/s.
+// TB/s, to fp32 82 us, 5.7 TB/s (asked of the memory side, where the last-level
+// cache serves a part that the counters do not tell apart).
 #include "typed.hpp"
 
 #include <algorithm>

@@ -8,11 +8,12 @@
 //
 // Its bytes are few: latency bounds it up to some thousand tokens (1 x 128:
 // 3.3 us, 512 x 128: 4.4, most of it the launch; 4099 x 256 with a bias and
-// groups 13.2), then the instructions: 16384 x 256, eight of them, no bias: 10.1
-// us, 1.8 TB/s; 32768 x 384 with a bias: 21.9 us, 2.4 TB/s.  One token per wave
-// in 64 bits throughout took 9.5, 43 and 88 us for 1 x 128, 16384 x 256 and
-// 32768 x 384; taking the best out one after the other instead of the
-// candidates' ranks 12.0 and 35.8 for the latter two.
+// groups 13.0), then the instructions: 16384 x 256, eight of them, no bias: 10.3
+// us, 1.7 TB/s, 5.9 us of VALU time; 32768 x 384 with a bias: 22.1 us, 2.3 TB/s,
+// 17.8 us of VALU time.  One token per wave in 64 bits throughout took 9.5, 43
+// and 88 us for 1 x 128, 16384 x 256 and 32768 x 384; taking the best out one
+// after the other instead of the candidates' ranks 12.0 and 35.8 for the latter
+// two.
 #include "typed.hpp"
 
 #include <float.h>
@@ -643,7 +644,7 @@ extern "C" int moe_router(const void* logits, int type, int64_t T, int64_t E, in
   hipStream_t st = to_stream(stream);
   const dim3 block(kRouterWaves * 64);
   if (top_k + (bias ? 2 : 0) > 16) {
-    // more picks than a token's 16 lanes hold: one token per wave (16384 x 256, 32 of them: 103 us)
+    // more picks than a token's 16 lanes hold: one token per wave (16384 x 256, 32 of them: 103 us, bound by its 3600 VALU instructions a token)
     hipLaunchKernelGGL(moe_router_wide_kernel, dim3(static_cast<unsigned>((T + kRouterWaves - 1) / kRouterWaves)), block,
                        0, st, a);
     return launch_status();
