@@ -323,8 +323,7 @@ template <int V>
 __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArgs a) {
   // with groups, per wave a float per token and expert, or route_token's double per expert
   extern __shared__ double s_values[];
-  __shared__ float s_group[kRouterWaves][4][kRouterMaxGroups];
-  __shared__ float s_size[kRouterWaves][4][kRouterMaxGroups];  // the magnitudes of a group's terms, added
+  __shared__ float s_group[kRouterWaves][4][2][kRouterMaxGroups];  // a group's value, and its terms' magnitudes added
   __shared__ int2 s_cand[kRouterWaves][2][4][17];  // the 17th takes what is no candidate
   const int lane = threadIdx.x & 63, li = lane & 15, tok = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -430,38 +429,36 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(RouterArg
       }
       if (g < a.groups) {
         const float second = a.group_score != QMM_GROUP_MAX && b1 > -INFINITY ? b1 : 0.0f;
-        s_group[wave][tok][g] = b0 + second;
-        s_size[wave][tok][g] = b0 > -INFINITY ? fabsf(b0) + fabsf(second) : 0.0f;
+        s_group[wave][tok][0][g] = b0 + second;
+        s_group[wave][tok][1][g] = b0 > -INFINITY ? fabsf(b0) + fabsf(second) : 0.0f;
       }
     }
     wave_fence();
     // Of the kept the least that one can be, of the others the most.  A group's error is that of its terms, which its sum
     // may be far smaller than: 2 (1 + kappa) * 2^-24, and twice their magnitudes for theirs and the sum's rounding (taken
-    // twice, for the roundings here).  Terms that add up past fp32 leave the token unsure; a group without unmasked
-    // experts has no error.
+    // twice, for the roundings here).  Terms that add up past fp32 can be anything; groups without unmasked experts are
+    // all the same.
     float low = INFINITY, high = -INFINITY;
-    bool past = false;
     uint64_t kept = 0;  // bit g: group g of the token
     for (int g0 = 0; g0 < a.groups; g0 += 16) {
       const int g = g0 + li;
-      const float mine = s_group[wave][tok][min(g, a.groups - 1)], size = s_size[wave][tok][min(g, a.groups - 1)];
-      const float err = 0x1p-23f * (1.0f + kappa) + 0x1p-22f * size;
-      past = past || !(size < INFINITY);
+      const float mine = s_group[wave][tok][0][min(g, a.groups - 1)], size = s_group[wave][tok][1][min(g, a.groups - 1)];
+      const float err = 0x1p-23f * (1.0f + kappa) + 0x1p-22f * size, from = size < INFINITY ? mine : 0.0f;
       int rank = 0;
 #pragma unroll 8
       for (int j = 0; j < a.groups; ++j) {
-        const float o = s_group[wave][tok][j];
+        const float o = s_group[wave][tok][0][j];
         rank += o > mine || (o == mine && j < g) ? 1 : 0;
       }
       const bool in = g < a.groups && rank < a.keep;
       kept |= (__ballot(in) >> (lane & 48) & 0xffff) << g0;
-      if (in) low = fminf(low, mine - err);
-      else if (g < a.groups) high = fmaxf(high, mine + err);
+      if (in) low = fminf(low, from - err);
+      else if (g < a.groups) high = fmaxf(high, from + err);
     }
     low = row_reduce_f(low, fmin2);
     high = row_reduce_f(high, fmax2);
     // where all others are masked, the kept are right; scores by the logits have no error
-    if (scored) unsure = (__ballot(past) >> (lane & 48) & 0xffff) != 0 || (high > -INFINITY && !(low > high));
+    if (scored) unsure = high > -INFINITY && !(low > high);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       // e / per: exact, for e times the multiplier's error is below 2^9 * 2^9
