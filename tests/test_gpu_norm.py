@@ -281,3 +281,19 @@ def test_large_streams(T, K, rt):
     stream = r.clone()
     a, b, _ = qmm.rms_norm_q8_1(x, w, residual=stream, residual_out=stream)
     assert torch.equal(a, xq) and torch.equal(stream, ro)
+
+
+def test_scaled_rows_past_the_first_workgroups():
+    T = (1 << 22) + 5                     # four rows to a workgroup, and one row more than all of them have at first
+    x = torch.randn(T, 32, device=DEV, generator=torch.Generator(DEV).manual_seed(4)).bfloat16()
+    for i in (0, 1, 77, (1 << 22) - 1, 1 << 22, T - 1):
+        x[i] = x[i] * 2.0**-100
+    x[2], x[T - 2] = x[2] * 2.0**100, x[T - 2] * 2.0**100
+    w = torch.ones(32, device=DEV)
+    xq, _, y = qmm.rms_norm_q8_1(x, w, 0.0, y_dtype=F32)
+    assert torch.all(y.abs().amax(1) > 0.5)
+    for rows in (slice(0, 100), slice((1 << 22) - 50, T)):
+        n = oracle.rms_norm(x[rows].double().cpu().numpy(), np.ones(32), 0.0)
+        assert np.all(np.abs(host(y[rows]) - n) <= tolerance(32) * np.abs(n))
+        a, _, b = qmm.rms_norm_q8_1(x[rows].contiguous(), w, 0.0, y_dtype=F32)
+        assert torch.equal(a, xq[rows]) and torch.equal(b, y[rows])
