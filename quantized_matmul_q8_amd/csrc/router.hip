@@ -641,7 +641,8 @@ extern "C" int moe_router(const void* logits, int type, int64_t T, int64_t E, in
   hipStream_t st = to_stream(stream);
   const dim3 block(kRouterWaves * 64);
   if (top_k + (bias ? 2 : 0) > 16) {
-    // more picks than a token's 16 lanes hold: one token per wave (16384 x 256, 32 of them: 103 us, bound by its 3600 VALU instructions a token)
+    // more picks than a token's 16 lanes hold: one token per wave (16384 x 256, 32 of them: 103 us, bound by its 3600
+    // VALU instructions a token)
     hipLaunchKernelGGL(moe_router_wide_kernel, dim3(static_cast<unsigned>((T + kRouterWaves - 1) / kRouterWaves)), block,
                        0, st, a);
     return launch_status();
