@@ -404,6 +404,152 @@ int moe_slot_mmvq(int fmt, const void* w, int64_t E, int64_t M, int64_t K, int64
  */
 int swiglu_q8_1(const float* g_u, void* hq, int64_t R, int64_t F, void* stream);
 
+/*
+ * Attention of a decoder layer: what stands between the stacked q, k, v
+ * product and the output product.  Heads of D values; Hq query heads share Hk
+ * key heads, query head h reading key head h / (Hq / Hk).  q, k and v are rows
+ * [T][stride] with a token's heads next to each other from its first value
+ * on; a stride is a count of values, at least heads * D and a multiple of 8,
+ * so that slices of the stacked product's rows are taken as they are (each
+ * pointer 16-byte aligned).  Other buffers have no gaps.
+ *
+ * Rotation tables are fp32 [P][rot]: row p holds rot/2 cosines, then rot/2
+ * sines, of the angles at position p.  Pair i of a head, at angle i, is values
+ * i and i + rot/2, or with `interleaved` values 2i and 2i + 1; (a, b) turns to
+ * (a c - b s, b c + a s), and values from rot on pass.  rot % 16 == 0 and
+ * rot <= D.  positions int32 [T] are expected in [0, P); others count as the
+ * nearest of these.
+ */
+
+/*
+ * qk_norm_rope -- norm of each query and key head and rotation, in one pass:
+ *   n = x * rstd * (weight + weight_offset), rstd = 1/sqrt(mean(x^2) + eps)
+ *   out = n turned by its token's position, rounded once to out_type
+ * q, k of `type`, weights [D] of w_type; all three types may be QMM_F32,
+ * QMM_F16 or QMM_BF16.  A NULL weight leaves that side unnormed (n = x), a
+ * NULL rope (with rot == 0) unturned.  k may be NULL (Hk is then ignored).
+ * q_out and k_out have strides of their own; q_out == q is allowed where type
+ * and stride are the same, and so for k; no other buffers may overlap.
+ * Squares may leave the fp32 range at either end; a head of zeros gives zeros.
+ * Requires 0 <= T < 2^31, 1 <= Hq, Hk <= 1024, D % 32 == 0, 32 <= D <= 512,
+ * eps >= 0, 1 <= P < 2^31.  T == 0 is a no-op.
+ */
+int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int type, const void* q_weight,
+                 const void* k_weight, int w_type, float weight_offset, float eps, const float* rope, int64_t P,
+                 int64_t rot, int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
+                 void* k_out, int64_t k_out_stride, int out_type, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                 void* stream);
+
+/*
+ * The paged 4-bit cache of keys and values: uint8 [pages][Hk][page/16][20 D].
+ * A page holds `page` tokens (a multiple of 16); slot s is token s % page of
+ * page s / page.  A cell of 20 D bytes holds 16 tokens t of one head, with
+ * B = D/32 blocks of 32 values:
+ *   at 0      key codes    [B][16 t][16 bytes]; byte 4j + i of a block has in
+ *             its low and high half codes 8j + {0, 4, 1, 5}[i] and the code
+ *             two further
+ *   at 8 D    key scales   [B][16 t] pairs of f16 (d, m)
+ *   at 10 D   value codes  [4 quads of t][16 c][B][4 bytes]; byte i has codes
+ *             32 b + c (low) and 32 b + 16 + c (high) of token
+ *             {0, 2, 1, 3}[i] of the quad
+ *   at 18 D   value scales [4 quads][B] of four f16 d and four f16 m
+ * A code n of 0..15 stands for the f16 number n * d + m, rounded once: five
+ * bits a value.  The order is that in which attn_q4's loads are the operands
+ * of its matrix instructions.
+ */
+
+/*
+ * kv_append_q4 -- T tokens' keys and values into the cache, the keys turned on
+ * the way.  k, v rows of Hk heads, each QMM_F32, QMM_F16 or QMM_BF16;
+ * slots int64 [T], a token whose slot is outside [0, pages * page) is left
+ * out (padding); no other slot may come twice.  Per block of 32 values x (fp32
+ * after the turn, every product and sum rounded; NaN counts as 0 and values
+ * beyond +-32768 as that):
+ *   d = f16((max - min) / 15), m = f16(min),
+ *   n = clamp(rint((x - m) * (1/d)), 0, 15), 0 where d == 0
+ * in IEEE fp32 without contraction: the bytes are defined to the bit, and
+ * every value that the cache holds is finite.  A NULL rope (with rot == 0)
+ * stores the keys unturned and takes no positions.
+ * Requires T >= 0, 1 <= Hk <= 1024, D one of 64, 96, 128, 192, 256, page % 16
+ * == 0 and 16 <= page <= 2^20, 1 <= pages < 2^31, T * Hk < 2^31.  T == 0 is a
+ * no-op.
+ */
+int kv_append_q4(const void* k, int64_t k_stride, int k_type, const void* v, int64_t v_stride, int v_type,
+                 const float* rope, int64_t P, int64_t rot, int interleaved, const int32_t* positions,
+                 const int64_t* slots, void* cache, int64_t pages, int64_t page, int64_t T, int64_t Hk, int64_t D,
+                 void* stream);
+
+/*
+ * kv_read_q4 -- the keys and values [T][Hk][D] that the slots of the cache
+ * stand for, in `type`: exact in QMM_F32 and QMM_F16, rounded once in
+ * QMM_BF16.  For consumers that are not quantized, such as attn_prompt over a
+ * context in the cache.  A slot outside [0, pages * page) gives zeros; a slot
+ * may come twice.  Limits as kv_append_q4.
+ */
+int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* slots, void* k, void* v, int type,
+               int64_t T, int64_t Hk, int64_t D, void* stream);
+
+/* Largest count of new tokens per sequence of attn_q4. */
+#define QMM_ATTN_MAX_N 8
+
+/*
+ * attn_q4 -- attention of the last n tokens of each of B sequences over the
+ * cache (which holds their keys already): decoding, and drafted tokens.
+ *   q      [B * n][q_stride], Hq heads, QMM_F16 or QMM_BF16 (`type`)
+ *   table  int32 [B][W]: page number w of sequence b
+ *   lens   int32 [B]: tokens of sequence b, the n new ones among them
+ *   y      [B * n][Hq * D] of y_type (any type)
+ * Query i of n stands at len - n + i; it sees the keys up to its own place,
+ * and with window > 0 of these the last `window`.  y = sum softmax(scale *
+ * q . k) v over these.  A query that sees no key (len 0, or i < n - len) gives
+ * zeros.  lens above W * page count as that, negative ones as 0; keys of a
+ * page number outside [0, pages) are not seen; nothing of a page behind a
+ * sequence's end is used, whatever it holds.
+ * Scores, softmax statistics and sums are fp32; the softmax's terms are
+ * rounded to f16 (relative 2^-12) where they meet the values.
+ * ws: attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page) bytes of scratch, no
+ * initialisation needed; may be NULL where that is 0.  Calls that share it
+ * must be ordered on one stream.  Equal calls give equal bits.
+ * Requires B >= 0, 1 <= n <= QMM_ATTN_MAX_N, Hq % Hk == 0, Hq <= 1024, D one
+ * of 64, 96, 128, 192, 256, scale finite, 0 <= window < 2^31, W >= 1, W * page
+ * <= 2^30, B * n * Hq < 2^26, pages as kv_append_q4.  B == 0 is a no-op.
+ */
+int attn_q4(const void* q, int64_t q_stride, int type, const void* cache, int64_t pages, int64_t page,
+            const int32_t* table, int64_t W, const int32_t* lens, float scale, int64_t window, void* y, int y_type,
+            int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of attn_q4 for sequences of at most max_len (= W * page)
+ * tokens; 0 where none is needed, and for sizes that attn_q4 refuses. */
+size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len);
+
+/*
+ * attn_prompt -- attention over whole prompts, B sequences packed one behind
+ * the other.
+ *   q      [Tq][q_stride], Hq heads;  k, v [Tk][..stride], Hk heads; all of
+ *          `type`, QMM_F16 or QMM_BF16
+ *   cu_q   int32 [B + 1]: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 of q
+ *   cu_k   the same for k and v (cu_q again where both are the same tokens)
+ *   y      [Tq][Hq * D] of y_type (any type)
+ * Query i of a sequence of nq queries and nk keys stands at key nk - nq + i
+ * (its context comes first); with `causal` it sees the keys up to that place,
+ * and with window > 0 (causal only) of these the last `window`; without, all.
+ * y = sum softmax(scale * q . k) v; a query that sees no key gives zeros, and
+ * so does one whose every score is -inf.  What stands at keys that a query
+ * does not see has no influence on it, NaN and infinities neither.  Rows of y
+ * outside [cu_q[0], cu_q[B]) are left as they were.  The entries of cu_q and
+ * cu_k are expected in order and within [0, Tq] and [0, Tk]; rows beyond these
+ * are never touched.
+ * Scores, softmax statistics and sums are fp32; the softmax's terms are
+ * rounded to `type` (relative 2^-12 or 2^-9) where they meet the values.
+ * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
+ * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, and (Tq/64 + B) * Hq <
+ * 2^31.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.
+ */
+int attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                int type, const int32_t* cu_q, const int32_t* cu_k, int64_t B, float scale, int causal,
+                int64_t window, void* y, int y_type, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
+                void* stream);
+
 /* Bytes of workspace needed by `op` (QMM_OP_MMQ, QMM_OP_MOE or
  * QMM_OP_MOE_SLOTS) for the given sizes; unused sizes may be 0.  Returns 0
  * for an unknown op.  The workspace is the scratch the caller allocates

@@ -49,3 +49,6 @@ from .matmul import (  # noqa: F401
 from .moe import route_buckets, grouped, grouped_blocks, combine, swiglu  # noqa: F401
 from .norm import rms_norm  # noqa: F401
 from .routing import route  # noqa: F401
+from .attention import (  # noqa: F401
+    rope_table, turn, head_norm, q4_blocks, q4_values, cache_store, cache_load, attention, visible,
+)

@@ -11,6 +11,7 @@ Tensor layouts (uint8 unless stated):
   Q8_1 blocks   [rows, K/32, 40]     outputs       float32 [T, M]
   MoE experts   [E, M, K/256, bytes] (contiguous; the expert stride is taken
                 from the tensor)
+  4-bit key-value cache  [pages, Hk, page/16, 20 D]
 """
 from __future__ import annotations
 
@@ -24,7 +25,8 @@ from ._lib import (  # noqa: F401
 )
 
 __all__ = [
-    "q8_1_quantize", "q8_1_dequantize", "rms_norm_q8_1", "moe_router", "mmvq_q4g", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
+    "q8_1_quantize", "q8_1_dequantize", "rms_norm_q8_1", "moe_router", "mmvq_q4g", "qk_norm_rope", "kv_cache_q4", "kv_append_q4", "kv_read_q4", "attn_q4",
+    "attn_q4_workspace_bytes", "attn_prompt", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
     "mmq_q6k_f32",
     "moe_grouped_mmq", "moe_grouped_swiglu", "moe_ffn", "moe_slot_mmvq",
     "swiglu_q8_1", "workspace", "workspace_bytes", "debug_subdots", "probe_read", "probe_read_geom",
@@ -292,6 +294,286 @@ def mmvq_q4g(w: torch.Tensor, scales: torch.Tensor, xq: torch.Tensor, *, zeros: 
     out = _out(out, (T, M), torch.float32, w.device)
     _enqueue(index, _lib.LIB.mmvq_q4g, w.data_ptr(), scales.data_ptr(), st, None if zeros is None else zeros.data_ptr(),
              xq.data_ptr(), out.data_ptr(), M, K, K // groups, T)
+    return out
+
+
+def _heads(t: torch.Tensor, name: str, H: int | None = None, D: int | None = None):
+    """Checks rows of heads ``[T, H, D]`` (a token's heads next to each other, the tokens any multiple of 8
+    values apart); returns (type code, values from token to token)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a HIP device")
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (D is not None and t.shape[2] != D):
+        raise ValueError(f"{name} must be [T, {'heads' if H is None else H}, {'D' if D is None else D}], got "
+                         f"{tuple(t.shape)}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: a token's heads must stand next to each other, got strides {t.stride()}")
+    if T <= 1:
+        st = H * D
+    elif st < H * D or st % 8:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 values apart and must not overlap, got strides "
+                         f"{t.stride()}")
+    return code, st
+
+
+def _rope_args(rope, positions, T: int, D: int, index: int):
+    """(table pointer, P, rot, positions pointer) of an optional rotation table."""
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions need a rope table")
+        return None, 0, 0, None
+    _need(rope, torch.float32, "rope", 2)
+    if positions is None:
+        raise ValueError("a rope table needs positions")
+    _need(positions, torch.int32, "positions", 1)
+    if positions.shape[0] != T:
+        raise ValueError(f"positions must have shape ({T},), got {tuple(positions.shape)}")
+    P, rot = rope.shape
+    if P < 1 or rot < 16 or rot % 16 or rot > D:
+        raise ValueError(f"rope must be [positions, rot] with rot a multiple of 16 up to D = {D}, got {tuple(rope.shape)}")
+    _on(index, rope=rope, positions=positions)
+    return rope.data_ptr(), P, rot, positions.data_ptr()
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, *, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                 interleaved: bool = False, dtype: torch.dtype | None = None, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None):
+    """RMS norm of every head of ``q[T, Hq, D]`` and ``k[T, Hk, D]`` and the position rotation, in one pass.
+
+    ``q`` and ``k`` may be slices of the rows of a stacked product (heads next
+    to each other, any token stride that is a multiple of 8).  ``q_weight`` and
+    ``k_weight`` [D] norm a side (None: not normed), times weight +
+    ``weight_offset``.  ``rope`` fp32 [P, rot]: a position's rot/2 cosines, then
+    its sines; ``positions`` int32 [T].  Pairs are values i and i + rot/2, or 2i
+    and 2i + 1 if ``interleaved``; values from rot on pass.  Returns ``(q_out,
+    k_out)`` in ``dtype`` (default: that of q); ``q_out=q`` works in place.
+    """
+    code, qs = _heads(q, "q")
+    T, Hq, D = q.shape
+    index, dev = q.get_device(), q.device
+    if D % 32 or not 32 <= D <= 512:
+        raise ValueError(f"q: D = {D} must be a multiple of 32 up to 512")
+    if not eps >= 0.0:
+        raise ValueError(f"eps must be at least 0, got {eps}")
+    Hk = ks = wt = 0
+    if k is not None:
+        kc, ks = _heads(k, "k", None, D)
+        if kc != code:
+            raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+        if k.shape[0] != T:
+            raise ValueError(f"k must be of {T} tokens, got {tuple(k.shape)}")
+        Hk = k.shape[1]
+        _on(index, k=k)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            c = _typed(w, name, 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must have shape ({D},), got {tuple(w.shape)}")
+            if q_weight is not None and w.dtype != q_weight.dtype:
+                raise TypeError("q_weight and k_weight must have one dtype")
+            wt = c
+    _on(index, q_weight=q_weight, k_weight=k_weight)
+    rp, P, rot, pp = _rope_args(rope, positions, T, D, index)
+
+    def output(out, like, H, name):
+        t = dtype or (like.dtype if out is None else out.dtype)
+        if t not in _TYPES:
+            raise TypeError(f"dtype must be float32, float16 or bfloat16, got {t}")
+        if out is None:
+            out = torch.empty((T, H, D), dtype=t, device=dev)
+        c, s = _heads(out, name, H, D)
+        if out.dtype != t:
+            raise TypeError(f"{name} must be {t}, got {out.dtype}")
+        if out.shape[0] != T:
+            raise ValueError(f"{name} must be of {T} tokens, got {tuple(out.shape)}")
+        _on(index, **{name: out})
+        if out.data_ptr() == like.data_ptr() and T > 0 and (out.dtype != like.dtype or (T > 1 and out.stride() != like.stride())):
+            raise ValueError(f"{name}: in place needs the dtype and strides of the input")
+        return out, c, s
+
+    q_out, oc, qos = output(q_out, q, Hq, "q_out")
+    kos = 0
+    if k is not None:
+        k_out, kc, kos = output(k_out, k, Hk, "k_out")
+        if kc != oc:
+            raise TypeError("q_out and k_out must have one dtype")
+    _enqueue(index, _lib.LIB.qk_norm_rope, q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, code,
+             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), wt,
+             weight_offset, eps, rp, P, rot, int(bool(interleaved)), pp, q_out.data_ptr(), qos,
+             None if k is None else k_out.data_ptr(), kos, oc, T, Hq, Hk, D)
+    return q_out, k_out
+
+
+def kv_cache_q4(pages: int, page: int, Hk: int, D: int, device) -> torch.Tensor:
+    """A zeroed paged 4-bit cache of keys and values, uint8 ``[pages, Hk, page/16, 20 D]`` (see include/qmm.h)."""
+    if page < 16 or page % 16 or D not in (64, 96, 128, 192, 256) or pages < 1 or Hk < 1:
+        raise ValueError("page must be a multiple of 16, D one of 64, 96, 128, 192, 256, pages and Hk at least 1")
+    return torch.zeros((pages, Hk, page // 16, 20 * D), dtype=torch.uint8, device=device)
+
+
+def _kv_cache(cache: torch.Tensor):
+    """(pages, page, Hk, D) of a cache."""
+    _need(cache, torch.uint8, "cache", 4)
+    pages, Hk, cells, size = cache.shape
+    if pages < 1 or Hk < 1 or cells < 1 or size not in (1280, 1920, 2560, 3840, 5120):
+        raise ValueError(f"cache must be [pages, Hk, page/16, 20 D] with D one of 64, 96, 128, 192, 256, got "
+                         f"{tuple(cache.shape)}")
+    return pages, 16 * cells, Hk, size // 20
+
+
+def _slots(slots: torch.Tensor, index: int, T: int | None = None) -> int:
+    _need(slots, torch.int64, "slots", 1)
+    if T is not None and slots.shape[0] != T:
+        raise ValueError(f"slots must have shape ({T},), got {tuple(slots.shape)}")
+    _on(index, slots=slots)
+    return slots.shape[0]
+
+
+def kv_append_q4(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *,
+                 rope: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                 interleaved: bool = False) -> torch.Tensor:
+    """Stores ``k[T, Hk, D]`` and ``v[T, Hk, D]`` (rows as :func:`qk_norm_rope` takes them) into the slots (page
+    number * page + place, int64 ``[T]``) of ``cache``, in 4 bits a value; k is turned by ``rope`` first if given.
+    k and v may be float32, float16 or bfloat16 each on its own.
+
+    A slot outside the cache (such as -1) leaves its token out; no other may
+    come twice.  Values beyond +-32768 count as that, NaN as 0.  Returns ``cache``.
+    """
+    pages, page, Hk, D = _kv_cache(cache)
+    index = cache.get_device()
+    code, ks = _heads(k, "k", Hk, D)
+    vc, vs = _heads(v, "v", Hk, D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"v must be of {T} tokens, got {tuple(v.shape)}")
+    _slots(slots, index, T)
+    _on(index, k=k, v=v)
+    rp, P, rot, pp = _rope_args(rope, positions, T, D, index)
+    _enqueue(index, _lib.LIB.kv_append_q4, k.data_ptr(), ks, code, v.data_ptr(), vs, vc, rp, P, rot,
+             int(bool(interleaved)), pp, slots.data_ptr(), cache.data_ptr(), pages, page, T, Hk, D)
+    return cache
+
+
+def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.float16, *,
+               k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+    """The keys and values ``[T, Hk, D]`` that the slots (int64 ``[T]``) of ``cache`` stand for, in ``dtype``
+    (float32, float16: exact; bfloat16: rounded once).  A slot outside the cache gives zeros."""
+    pages, page, Hk, D = _kv_cache(cache)
+    index, dev = cache.get_device(), cache.device
+    T = _slots(slots, index)
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    k = _out(k, (T, Hk, D), dtype, dev, "k")
+    v = _out(v, (T, Hk, D), dtype, dev, "v")
+    _enqueue(index, _lib.LIB.kv_read_q4, cache.data_ptr(), pages, page, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+             _TYPES[dtype], T, Hk, D)
+    return k, v
+
+
+def attn_q4_workspace_bytes(B: int, n: int, Hq: int, Hk: int, D: int, max_len: int) -> int:
+    """Bytes of workspace of :func:`attn_q4`; max_len is the table's width times the page size."""
+    return int(_lib.LIB.attn_q4_workspace_bytes(B, n, Hq, Hk, D, max_len))
+
+
+def _half(code: int, t: torch.Tensor, name: str) -> None:
+    if code == _lib.QMM_F32:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, *,
+            scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the last n <= 8 tokens of each sequence over the 4-bit ``cache`` that holds them already.
+
+    ``q`` float16 or bfloat16 [B, n, Hq, D], or [B, Hq, D] for n = 1; ``table``
+    int32 [B, W] the pages of each sequence, ``lens`` int32 [B] its tokens.
+    Query i sees the keys up to place len - n + i, and with ``window`` of these
+    the last so many; one that sees none gives zeros.  ``scale`` defaults to
+    1/sqrt(D).  Returns q's shape in ``out_dtype`` (default: q's).
+    """
+    pages, page, Hk, D = _kv_cache(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be [B, n, Hq, D] or [B, Hq, D]")
+    B, n = q.shape[0], q.shape[1] if q.dim() == 4 else 1
+    rows = q
+    if q.dim() == 4:
+        if B > 1 and n > 1 and q.stride(0) != n * q.stride(1):
+            raise ValueError(f"q: the tokens must be the same distance apart over all sequences, got strides {q.stride()}")
+        rows = q.flatten(0, 1)
+    code, qs = _heads(rows, "q", None, D)
+    _half(code, q, "q")
+    Hq = rows.shape[1]
+    if Hq % Hk or not Hq:
+        raise ValueError(f"q: {Hq} heads are no multiple of the cache's {Hk}")
+    _need(table, torch.int32, "table", 2)
+    _need(lens, torch.int32, "lens", 1)
+    if table.shape[0] != B or lens.shape[0] != B or table.shape[1] < 1:
+        raise ValueError(f"table must be [{B}, W] and lens [{B}], got {tuple(table.shape)} and {tuple(lens.shape)}")
+    index = cache.get_device()
+    _on(index, q=q, table=table, lens=lens)
+    out = _out(out, tuple(q.shape), out_dtype or (q.dtype if out is None else out.dtype), q.device)
+    yt = _typed(out, "out", q.dim())
+    W = table.shape[1]
+    need = _lib.LIB.attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    else:
+        _need(ws, torch.uint8, "ws", 1)
+        _on(index, ws=ws)
+    _enqueue(index, _lib.LIB.attn_q4, q.data_ptr(), qs, code, cache.data_ptr(), pages, page, table.data_ptr(), W,
+             lens.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(), yt, B, n, Hq, Hk, D,
+             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    return out
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor | None = None,
+                *, causal: bool = True, window: int = 0, scale: float | None = None, out: torch.Tensor | None = None,
+                out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Attention over whole prompts, packed one behind the other.
+
+    ``q`` [Tq, Hq, D], ``k`` and ``v`` [Tk, Hk, D], float16 or bfloat16, rows as
+    :func:`qk_norm_rope` takes them; ``cu_q`` and ``cu_k`` int32 [B + 1], the
+    sequences' first rows and the end (``cu_k`` None: as cu_q).  A sequence's
+    last query stands at its last key; with ``causal`` a query sees the keys up
+    to its own place, and with ``window`` of these the last so many.  A query
+    that sees no key gives zeros; rows of ``out`` outside the sequences are left
+    as they were.  Returns [Tq, Hq, D] in ``out_dtype`` (default: q's).
+    """
+    code, qs = _heads(q, "q")
+    _half(code, q, "q")
+    Tq, Hq, D = q.shape
+    kc, ks = _heads(k, "k", None, D)
+    Tk, Hk = k.shape[:2]
+    vc, vs = _heads(v, "v", Hk, D)
+    if kc != code or vc != code:
+        raise TypeError(f"k and v must be {q.dtype}, got {k.dtype} and {v.dtype}")
+    if v.shape[0] != Tk:
+        raise ValueError(f"k and v must be of as many tokens, got {tuple(k.shape)} and {tuple(v.shape)}")
+    if not Hk or not Hq or Hq % Hk:
+        raise ValueError(f"q: {Hq} heads are no multiple of the {Hk} of k")
+    cu_k = cu_q if cu_k is None else cu_k
+    _need(cu_q, torch.int32, "cu_q", 1)
+    _need(cu_k, torch.int32, "cu_k", 1)
+    B = cu_q.shape[0] - 1
+    if B < 0 or cu_k.shape[0] != B + 1:
+        raise ValueError(f"cu_q and cu_k must have the same shape [B + 1], got {tuple(cu_q.shape)} and {tuple(cu_k.shape)}")
+    index = q.get_device()
+    _on(index, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
+    out = _out(out, (Tq, Hq, D), out_dtype or (q.dtype if out is None else out.dtype), q.device)
+    yt = _typed(out, "out", 3)
+    _enqueue(index, _lib.LIB.attn_prompt, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, cu_q.data_ptr(),
+             cu_k.data_ptr(), B, D ** -0.5 if scale is None else scale, int(bool(causal)), window, out.data_ptr(), yt, Tq,
+             Tk, Hq, Hk, D)
     return out
 
 

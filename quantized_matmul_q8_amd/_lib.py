@@ -38,6 +38,7 @@ QMM_SCORE_SOFTMAX = 0
 QMM_SCORE_SIGMOID = 1
 QMM_GROUP_MAX = 0
 QMM_GROUP_TOP2 = 1
+QMM_ATTN_MAX_N = 8
 
 _vp, _i64, _sz, _i, _f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
@@ -48,6 +49,16 @@ SIGNATURES = {
     "rms_norm_q8_1": (_i, [_vp, _i, _vp, _vp, _i, _vp, _i, _f, _f, _vp, _vp, _i, _i64, _i64, _vp]),
     "mmvq_q4g": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
     "moe_router": (_i, [_vp, _i, _i64, _i64, _i64, _i, _vp, _i64, _i64, _i, _i, _f, _vp, _vp, _vp]),
+    "qk_norm_rope": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _vp, _i, _f, _f, _vp, _i64, _i64, _i, _vp, _vp, _i64, _vp, _i64,
+                          _i, _i64, _i64, _i64, _i64, _vp]),
+    "kv_append_q4": (_i, [_vp, _i64, _i, _vp, _i64, _i, _vp, _i64, _i64, _i, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
+                          _vp]),
+    "kv_read_q4": (_i, [_vp, _i64, _i64, _vp, _vp, _vp, _i, _i64, _i64, _i64, _vp]),
+    "attn_q4": (_i, [_vp, _i64, _i, _vp, _i64, _i64, _vp, _i64, _vp, _f, _i64, _vp, _i, _i64, _i64, _i64, _i64, _i64,
+                     _vp, _sz, _vp]),
+    "attn_q4_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "attn_prompt": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _vp, _i64, _f, _i, _i64, _vp, _i, _i64, _i64, _i64,
+                         _i64, _i64, _vp]),
     "mmvq_q4k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q5k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q6k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),

@@ -40,62 +40,6 @@ struct NormArgs {
   bool large;       // the stream is larger than what the last-level cache (256 MB) would keep of it
 };
 
-// Eight values 8i .. 8i + 7 as they are stored.
-template <int TY>
-struct Raw8 {
-  static constexpr int kWords = TY == QMM_F32 ? 2 : 1;
-  uint4 v[kWords];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) v[k] = static_cast<const uint4*>(p)[i * kWords + k];
-  }
-  // Data that is read once.  Only 16-bit values: the two loads of eight fp32 ones touch the same lines, and the second
-  // would miss (16384 x 4096, bf16: 93 -> 87 us; 4096 x 11008, fp32: 57 -> 64).
-  __device__ __forceinline__ void load_once(const void* p, int64_t i) {
-    if constexpr (kWords == 1) v[0] = ld16_nt(static_cast<const uint4*>(p) + i);
-    else load(p, i);
-  }
-  __device__ __forceinline__ void store_nt(void* p, int64_t i) const {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      v4u t;
-      t.x = v[k].x;
-      t.y = v[k].y;
-      t.z = v[k].z;
-      t.w = v[k].w;
-      __builtin_nontemporal_store(t, static_cast<v4u*>(p) + i * kWords + k);
-    }
-  }
-  __device__ __forceinline__ void store(void* p, int64_t i) const {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) static_cast<uint4*>(p)[i * kWords + k] = v[k];
-  }
-  __device__ __forceinline__ float get(int j) const {
-    if constexpr (TY == QMM_F32) {
-      const uint4& q = v[j >> 2];
-      return __builtin_bit_cast(float, (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w);
-    } else {
-      const uint32_t d = (j >> 1) == 0 ? v[0].x : (j >> 1) == 1 ? v[0].y : (j >> 1) == 2 ? v[0].z : v[0].w;
-      if constexpr (TY == QMM_F16) return h2f(j & 1 ? d >> 16 : d & 0xffffu);
-      return __builtin_bit_cast(float, j & 1 ? d & 0xffff0000u : d << 16);
-    }
-  }
-  // values f rounded to the type, to the nearest (ties to even)
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    uint32_t d[4 * kWords];
-#pragma unroll
-    for (int j = 0; j < 4 * kWords; ++j) {
-      if constexpr (TY == QMM_F32) d[j] = __builtin_bit_cast(uint32_t, f[j]);
-      else if constexpr (TY == QMM_F16) d[j] = f2h_bits(f[2 * j]) | f2h_bits(f[2 * j + 1]) << 16;
-      else
-        d[j] = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * j]))) |
-               static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * j + 1]))) << 16;
-    }
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) v[k] = make_uint4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
-  }
-};
-
 // 1 / sqrt(mean + eps); 0 where the mean is 0 and there is no eps, and where it is infinite.
 __device__ __forceinline__ float rms_scale(float sum, const NormArgs& a) {
   const float ms = sum / static_cast<float>(a.K) + a.eps;
@@ -134,11 +78,6 @@ __device__ __forceinline__ void q8_1_block_4lanes(const float (&v)[8], int part,
 // square + eps is past fp32 (rstd 0 or NaN) or below 2^-96, where squares come
 // near the subnormals (above it those that vanish move it by less than 2^-50).
 __device__ __forceinline__ bool is_odd(float rstd) { return !(rstd > 0.0f && rstd <= 0x1p48f); }
-
-__device__ __forceinline__ void load8(int type, const void* p, int64_t i, float (&v)[8]) {
-  const float4 lo = load4(type, p, 2 * i), hi = load4(type, p, 2 * i + 1);
-  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-}
 
 // Such a row once more, from memory: each wave sums all of it and writes its
 // part.  `by` multiplies the values and `sq` these again for their squares alone:
