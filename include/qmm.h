@@ -506,7 +506,7 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * page number outside [0, pages) are not seen; nothing of a page behind a
  * sequence's end is used, whatever it holds.
  * Scores, softmax statistics and sums are fp32; the softmax's terms are
- * rounded to f16 (relative 2^-12) where they meet the values.
+ * rounded to f16 (half a step, 2^-11 relative) where they meet the values.
  * ws: attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page) bytes of scratch, no
  * initialisation needed; may be NULL where that is 0.  Calls that share it
  * must be ordered on one stream.  Equal calls give equal bits.
@@ -540,7 +540,8 @@ size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
  * cu_k are expected in order and within [0, Tq] and [0, Tk]; rows beyond these
  * are never touched.
  * Scores, softmax statistics and sums are fp32; the softmax's terms are
- * rounded to `type` (relative 2^-12 or 2^-9) where they meet the values.
+ * rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
+ * values.
  * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
  * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, and (Tq/64 + B) * Hq <
  * 2^31.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.

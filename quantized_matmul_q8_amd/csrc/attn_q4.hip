@@ -1,7 +1,22 @@
 // Attention of a sequence's last tokens over the paged 4-bit cache.
 //
-// One wave per query row: scores key by key, with the running maximum and sum
-// of the softmax.
+//   S^T = K Q^T,  p = 2^(c s - m),  O^T = V^T P^T,  y = O / sum p
+//
+// The query rows of one key head (new tokens x heads of the group) are the
+// columns of 16 x 16 tiles.  A wave takes 32 tokens, two cells of the cache, at
+// a time.  The cache's order gives each lane the codes that its place in the
+// operands of v_mfma_f32_16x16x32_f16 needs, with whole loads: for K a lane has
+// one key and one block (or a part of one), so one scale pair; for V one dim
+// and a quad of tokens of each cell, whose scales come from a load of the whole
+// cell's by row broadcasts.  The tile of S^T leaves in each lane the terms of
+// one query and the same quads of tokens, which is the operand that O^T takes:
+// nothing goes through LDS between the products.  Codes become f16 numbers by
+// their bits (0x6400 | n = 1024 + n, 0x5400 | n << 4 = 64 + n), a subtraction
+// that is exact, and one fma: the numbers that the format stands for.
+//
+// A sequence is cut into chunks of tokens, one per workgroup, so that a few
+// long sequences fill the chip; partial results go to the workspace and a
+// second kernel joins them.
 #include "kv_q4.hpp"
 
 #include <algorithm>
@@ -9,68 +24,415 @@
 
 namespace qmm {
 
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kStep = 32;    // tokens of a step: two cells
+constexpr int kWaves = 4;    // of a workgroup
+constexpr float kLift = 15.0f;  // terms are 2^15 at most: f16 then keeps those down to 2^-39 of the largest
+
 struct AttnQ4Args {
   const void* q;
   const uint8_t* cache;
   const int32_t* table;
   const int32_t* lens;
   void* y;
-  int64_t q_stride, pages, page, W, window;
+  float* part;  // [B * Hq * n rows][chunks][D], then [rows][chunks] pairs (m, l)
+  int64_t q_stride, pages, W;
+  int64_t max_len;
   float scale;
-  int B, n, Hq, Hk, D, type, y_type;
+  int window, B, n, Hq, Hk, group, rows, row_blocks, chunks, chunk, cells, cell_shift;
+  bool bf16;
+  int y_type;
 };
 
-__device__ __forceinline__ float load1(int type, const void* p, int64_t i) {
-  if (type == QMM_F32) return static_cast<const float*>(p)[i];
-  if (type == QMM_F16) return static_cast<float>(static_cast<const _Float16*>(p)[i]);
-  return static_cast<float>(static_cast<const __bf16*>(p)[i]);
-}
-__device__ __forceinline__ void store1(int type, void* p, int64_t i, float v) {
-  if (type == QMM_F32) static_cast<float*>(p)[i] = v;
-  else if (type == QMM_F16) static_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
-  else static_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
+__device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
+
+// Eight codes of a dword -> the f16 numbers of pairs (0, 4), (1, 5), (2, 6), (3, 7), less the bits' offsets.
+__device__ __forceinline__ void codes(uint32_t w, h2 (&x)[4]) {
+  const h2 big = {static_cast<_Float16>(1024.0f), static_cast<_Float16>(1024.0f)};
+  const h2 small = {static_cast<_Float16>(64.0f), static_cast<_Float16>(64.0f)};
+  const uint32_t u = w >> 8;
+  x[0] = as_h2((w & 0x000f000fu) | 0x64006400u) - big;
+  x[1] = as_h2((w & 0x00f000f0u) | 0x54005400u) - small;
+  x[2] = as_h2((u & 0x000f000fu) | 0x64006400u) - big;
+  x[3] = as_h2((u & 0x00f000f0u) | 0x54005400u) - small;
 }
 
-__global__ __launch_bounds__(64) void attn_q4_kernel(AttnQ4Args a) {
-  const int lane = threadIdx.x;
-  const int h = blockIdx.x % a.Hq, row = blockIdx.x / a.Hq, b = row / a.n, i = row % a.n, kh = h / (a.Hq / a.Hk);
-  const int64_t len = max(int64_t{0}, min(a.W * a.page, static_cast<int64_t>(a.lens[b])));
-  const int64_t at = len - a.n + i, first = a.window > 0 ? max(int64_t{0}, at - a.window + 1) : 0;
-  const int nb = a.D / 32;
-  float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = -INFINITY, sum = 0.0f;
-  for (int r = 0; r < 4; ++r) {
-    const int d = lane + 64 * r;
-    q[r] = d < a.D ? load1(a.type, a.q, row * a.q_stride + h * a.D + d) * a.scale : 0.0f;
-  }
-  for (int64_t j = first; j <= at; ++j) {
-    const int64_t pg = a.table[b * a.W + j / a.page];
-    if (pg < 0 || pg >= a.pages) continue;
-    const uint8_t* cell = a.cache + kv_cell(pg * a.page + j % a.page, a.page, kh, a.Hk, a.D);
-    const int t = static_cast<int>(j % kCellTokens), quad = t >> 2;
-    float s = 0.0f, v[4];
-    for (int r = 0; r < 4; ++r) {
-      const int d = lane + 64 * r, blk = d >> 5, e = d & 7;
-      v[r] = 0.0f;
-      if (d >= a.D) continue;
-      const uint32_t kb = cell[(blk * 16 + t) * 16 + (d & 31) / 8 * 4 + (e & 1) * 2 + (e >> 2)];
-      const uint16_t* ks = reinterpret_cast<const uint16_t*>(cell + 8 * a.D + (blk * 16 + t) * 4);
-      const float d16 = h2f(ks[0]), m16 = h2f(ks[1]);
-      s += q[r] * h2f(f2h_bits(__builtin_fmaf(static_cast<float>((e & 2) ? kb >> 4 : kb & 15u), d16, m16)));
-      const uint32_t vb = cell[10 * a.D + ((quad * 16 + (d & 15)) * nb + blk) * 4 + kv_quad_byte(t & 3)];
-      const uint16_t* vs = reinterpret_cast<const uint16_t*>(cell + 18 * a.D + (quad * nb + blk) * 16) + (t & 3);
-      v[r] = h2f(f2h_bits(__builtin_fmaf(static_cast<float>((d & 16) ? vb >> 4 : vb & 15u), h2f(vs[0]), h2f(vs[4]))));
+__device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
+  return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Over the four rows of 16 lanes, in all of them.
+template <typename F>
+__device__ __forceinline__ float rows_join(float v, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t w = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, static_cast<uint32_t>(a[0])),
+                                                    __builtin_bit_cast(float, static_cast<uint32_t>(a[1]))));
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return f(__builtin_bit_cast(float, static_cast<uint32_t>(b[0])), __builtin_bit_cast(float, static_cast<uint32_t>(b[1])));
+}
+__device__ __forceinline__ float rows_max(float v) {
+  return rows_join(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  return rows_join(v, [](float a, float b) { return a + b; });
+}
+
+template <int K>
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x150 + K, 0xf, 0xf, false));
+}
+
+// How a head's NB blocks are dealt out: runs of four blocks (a lane has one), of two (half of one), single ones (a quarter).
+template <int NB>
+struct Runs {
+  static constexpr int kQuads = NB / 4, kPair = (NB % 4) / 2, kOne = NB % 2, kScales = kQuads + kPair + kOne;
+};
+
+// One cell as loaded: this lane's key codes, their scales, the value codes, and its part of the values' scales.
+template <int NB>
+struct Cell {
+  static constexpr int kVs = (4 * NB + 15) / 16;
+  uint32_t k[NB], ks[Runs<NB>::kScales], v[NB], vs[kVs];
+
+  __device__ __forceinline__ void load(const uint8_t* cell, int lane) {
+    constexpr int D = 32 * NB;
+    const int key = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int r = 0; r < Runs<NB>::kQuads; ++r) {
+      const uint4 x = ld16_a16(cell + r * 1024 + lane * 16);
+      k[4 * r] = x.x, k[4 * r + 1] = x.y, k[4 * r + 2] = x.z, k[4 * r + 3] = x.w;
+      ks[r] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + r * 256 + lane * 4);
     }
-    s = wave_sum(s);
-    const float up = fmaxf(top, s), keep = expf(top - up), p = expf(s - up);
-    sum = sum * keep + p;
-    for (int r = 0; r < 4; ++r) o[r] = o[r] * keep + p * v[r];
-    top = up;
+    constexpr int kAt = 4 * Runs<NB>::kQuads;
+    if constexpr (Runs<NB>::kPair) {
+      const uint2 x = *reinterpret_cast<const uint2*>(cell + ((kAt + (c >> 1)) * 16 + key) * 16 + (c & 1) * 8);
+      k[kAt] = x.x, k[kAt + 1] = x.y;
+      ks[Runs<NB>::kQuads] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + ((kAt + (c >> 1)) * 16 + key) * 4);
+    }
+    if constexpr (Runs<NB>::kOne) {
+      k[NB - 1] = *reinterpret_cast<const uint32_t*>(cell + ((NB - 1) * 16 + key) * 16 + c * 4);
+      ks[Runs<NB>::kScales - 1] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + ((NB - 1) * 16 + key) * 4);
+    }
+    struct __attribute__((aligned(NB % 4 == 0 ? 16 : NB % 2 == 0 ? 8 : 4))) Words { uint32_t w[NB]; };
+    const Words x = *reinterpret_cast<const Words*>(cell + 10 * D + lane * (4 * NB));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) v[b] = x.w[b];
+#pragma unroll
+    for (int r = 0; r < kVs; ++r) {
+      const int at = min(r * 16 + key, 4 * NB - 1);
+      vs[r] = *reinterpret_cast<const uint32_t*>(cell + 18 * D + (c * (4 * NB) + at) * 4);
+    }
   }
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  for (int r = 0; r < 4; ++r) {
-    const int d = lane + 64 * r;
-    if (d < a.D) store1(a.y_type, a.y, (static_cast<int64_t>(row) * a.Hq + h) * a.D + d, o[r] * inv);
+
+  // The values' scales of tokens outside [lo, hi) of the cell as zeros: they may hold anything.
+  __device__ __forceinline__ void clear_scales(int lane, int lo, int hi) {
+#pragma unroll
+    for (int r = 0; r < kVs; ++r) {
+      const int t = 4 * (lane >> 4) + (lane & 1) * 2;
+      vs[r] &= (t >= lo && t < hi ? 0xffffu : 0u) | (t + 1 >= lo && t + 1 < hi ? 0xffff0000u : 0u);
+    }
   }
+
+  // A operand of the products with the queries, number j.
+  __device__ __forceinline__ h8 key_operand(int j) const {
+    h2 x[4];
+    codes(k[j], x);
+    const int s = j < 4 * Runs<NB>::kQuads ? j / 4 : (Runs<NB>::kPair && j < 4 * Runs<NB>::kQuads + 2) ? Runs<NB>::kQuads
+                                                                                                    : Runs<NB>::kScales - 1;
+    const h2 dm = as_h2(ks[s]), d = {dm.x, dm.x}, m = {dm.y, dm.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __builtin_elementwise_fma(x[i], d, m);
+    return join(x[0], x[1], x[2], x[3]);
+  }
+
+  // This cell's half of the A operands of block b's two tiles: dims c and c + 16, four tokens each.
+  template <int b>
+  __device__ __forceinline__ void value_operands(h2 (&low)[2], h2 (&high)[2]) const {
+    h2 x[4];
+    codes(v[b], x);
+    const uint32_t s = vs[b / 4];
+    const h2 d01 = as_h2(row_bcast<b % 4 * 4>(s)), d23 = as_h2(row_bcast<b % 4 * 4 + 1>(s));
+    const h2 m01 = as_h2(row_bcast<b % 4 * 4 + 2>(s)), m23 = as_h2(row_bcast<b % 4 * 4 + 3>(s));
+    low[0] = __builtin_elementwise_fma(x[0], d01, m01);
+    low[1] = __builtin_elementwise_fma(x[2], d23, m23);
+    high[0] = __builtin_elementwise_fma(x[1], d01, m01);
+    high[1] = __builtin_elementwise_fma(x[3], d23, m23);
+  }
+};
+
+// The dim at which the eight values of operand j begin in lane group c.
+template <int NB>
+__device__ __forceinline__ int operand_dim(int j, int c) {
+  constexpr int kAt = 4 * Runs<NB>::kQuads;
+  if (j < kAt) return (j / 4 * 4 + c) * 32 + j % 4 * 8;
+  if (Runs<NB>::kPair && j < kAt + 2) return (kAt + (c >> 1)) * 32 + (c & 1) * 16 + (j - kAt) * 8;
+  return (NB - 1) * 32 + c * 8;
+}
+
+template <int NB, int RT, int b = 0>
+__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (&p)[RT], v4f (&o)[RT][2 * NB]) {
+  h2 l0[2], u0[2], l1[2], u1[2];
+  cell[0].template value_operands<b>(l0, u0);
+  cell[1].template value_operands<b>(l1, u1);
+  const h8 low = join(l0[0], l0[1], l1[0], l1[1]), high = join(u0[0], u0[1], u1[0], u1[1]);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    o[r][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(low, p[r], o[r][2 * b], 0, 0, 0);
+    o[r][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(high, p[r], o[r][2 * b + 1], 0, 0, 0);
+  }
+  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, p, o);
+}
+
+template <int NB, int RT>
+__global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
+  constexpr int D = 32 * NB, kRow = D + 4;
+  __shared__ float s_o[kWaves][16][kRow];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, c = lane >> 4;
+  // chunks of a sequence and head next to each other
+  int id = blockIdx.x;
+  const int chunk = id % a.chunks;
+  id /= a.chunks;
+  const int row_block = id % a.row_blocks;
+  id /= a.row_blocks;
+  const int kh = id % a.Hk, seq = id / a.Hk;
+  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(a.lens[seq]))));
+  // the first key that any query sees, in whole steps
+  const int floor_at = a.window > 0 ? max(0, len - a.n - a.window + 1) : 0;
+  const int first = floor_at / kStep * kStep;
+  const int begin = first + chunk * a.chunk, end = min(len, begin + a.chunk);
+  const bool split = len - first > a.chunk;
+  if (chunk > 0 && begin >= len) return;
+
+  // queries: this lane's row of each tile, its place, and what a product is multiplied with
+  h8 q[RT][NB];
+  float mul[RT];
+  int at[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = (row_block * RT + r) * 16 + col;
+    const bool on = row < a.rows;
+    const int i = on ? row / a.group : a.n - 1, h = kh * a.group + (on ? row % a.group : 0);
+    at[r] = len - a.n + i;
+    const int64_t base = (static_cast<int64_t>(seq) * a.n + i) * a.q_stride + static_cast<int64_t>(h) * D;
+    mul[r] = a.scale * 1.44269504088896340736f;
+    if (!a.bf16) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        q[r][j] = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(a.q) + base + operand_dim<NB>(j, c));
+    } else {
+      // a power of two for the row brings its largest value to 2^13: exact but for what lies 2^-27 below that
+      float f[NB][8], top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        Raw8<QMM_BF16> x;
+        x.load(a.q, (base + operand_dim<NB>(j, c)) / 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[j][k] = x.get(k), top = fmaxf(top, fabsf(f[j][k]));
+      }
+      top = rows_max(top);
+      const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 14 : 0;
+      mul[r] = __builtin_amdgcn_ldexpf(mul[r], e);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(f[j][k], -e));
+    }
+  }
+
+  v4f o[RT][2 * NB];
+  float top[RT], sum[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    top[r] = -INFINITY, sum[r] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const int32_t* pages = a.table + static_cast<int64_t>(seq) * a.W;
+  const int64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
+  const uint8_t* head = a.cache + kh * head_bytes;
+  const int last_cell = (len - 1) / kCellTokens;  // nothing behind it is looked up
+  const auto page_of = [&](int cell) { return a.cell_shift >= 0 ? cell >> a.cell_shift : cell / a.cells; };
+  const auto page_at = [&](int token) { return pages[page_of(min(token / kCellTokens, last_cell))]; };
+  const auto cell_at = [&](int token, int page) {
+    const int cell = min(token / kCellTokens, last_cell);
+    const int64_t pg = page >= 0 && page < a.pages ? page : 0;
+    return head + pg * page_bytes + (cell - page_of(cell) * a.cells) * cell_bytes;
+  };
+
+  const int stride = kWaves * kStep;
+  int t = begin + wave * kStep;
+  if (t < end) {
+    Cell<NB> cell[2];
+    int pg[2] = {page_at(t), page_at(t + kCellTokens)};
+    cell[0].load(cell_at(t, pg[0]), lane);
+    cell[1].load(cell_at(t + kCellTokens, pg[1]), lane);
+    int next_pg[2] = {page_at(t + stride), page_at(t + stride + kCellTokens)};
+    for (;;) {
+      const bool more = t + stride < end;
+      Cell<NB> next[2];
+      if (more) {
+        next[0].load(cell_at(t + stride, next_pg[0]), lane);
+        next[1].load(cell_at(t + stride + kCellTokens, next_pg[1]), lane);
+      }
+      const int ahead[2] = {page_at(t + 2 * stride), page_at(t + 2 * stride + kCellTokens)};
+      const bool there0 = pg[0] >= 0 && pg[0] < a.pages, there1 = pg[1] >= 0 && pg[1] < a.pages;
+      // whether every query sees the whole step
+      const bool whole = t + kStep <= len - a.n + 1 && t >= (a.window > 0 ? len - a.window : 0) && there0 && there1;
+
+      h8 p[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) p[r] = h8{};
+      v4f s[RT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const h8 k = cell[u].key_operand(j);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
+        }
+      if (!whole) {
+        const int lo = floor_at - t, hi = len - t;
+        cell[0].clear_scales(lane, there0 ? lo : 16, hi);
+        cell[1].clear_scales(lane, there1 ? lo - 16 : 16, hi - 16);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x[8], most = top[r];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = s[r][k >> 2][k & 3] * mul[r];
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int j = t + (k >> 2) * kCellTokens + 4 * c + (k & 3);
+            const bool seen = j <= at[r] && (a.window == 0 || j > at[r] - a.window) && (k < 4 ? there0 : there1);
+            x[k] = seen ? x[k] : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, x[k]);
+        most = rows_max(most);
+        if (__builtin_amdgcn_ballot_w64(most > top[r])) {
+          const float keep = __builtin_amdgcn_exp2f(top[r] - (most == -INFINITY ? 0.0f : most));
+          sum[r] *= keep;
+#pragma unroll
+          for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
+          top[r] = most;
+        }
+        const float base = kLift - (most == -INFINITY ? 0.0f : most);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float e = __builtin_amdgcn_exp2f(x[k] + base);
+          sum[r] += e;
+          p[r][k] = static_cast<_Float16>(e);
+        }
+      }
+      add_values<NB, RT>(cell, p, o);
+      if (!more) break;
+      t += stride;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) cell[u] = next[u], pg[u] = next_pg[u], next_pg[u] = ahead[u];
+    }
+  }
+
+  // join the waves, tile by tile, and write
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float l = rows_sum(sum[r]);
+    if (c == 0) s_m[wave][col] = top[r], s_l[wave][col] = l;
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&s_o[wave][col][b * 16 + 4 * c]) = o[r][b];
+    __syncthreads();
+    const int row0 = (row_block * RT + r) * 16, rows = min(16, a.rows - row0);
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 256) {
+      const int row = x / (D / 4), d = x % (D / 4) * 4;
+      float m = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][row]);
+      const float base = m == -INFINITY ? 0.0f : m;
+      float total = 0.0f;
+      v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_m[w][row] - base);
+        total += s_l[w][row] * f;
+        y += *reinterpret_cast<const v4f*>(&s_o[w][row][d]) * f;
+      }
+      const int i = (row0 + row) / a.group, h = kh * a.group + (row0 + row) % a.group;
+      const int64_t out = (static_cast<int64_t>(seq) * a.n + i) * a.Hq + h;
+      if (split) {
+        *reinterpret_cast<v4f*>(a.part + (out * a.chunks + chunk) * D + d) = y;
+        if (d == 0) {
+          float* ml = a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D + (out * a.chunks + chunk) * 2;
+          ml[0] = m, ml[1] = total;
+        }
+      } else {
+        y *= total == 0.0f ? 0.0f : 1.0f / total;
+        store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the chunks of one row; sequences of one chunk have been written.
+__global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
+  const int64_t out = blockIdx.x;
+  const int seq = static_cast<int>(out / (static_cast<int64_t>(a.n) * a.Hq));
+  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(a.lens[seq]))));
+  const int first = a.window > 0 ? max(0, len - a.n - a.window + 1) / kStep * kStep : 0;
+  if (len - first <= a.chunk) return;
+  const int count = (len - first + a.chunk - 1) / a.chunk, lane = threadIdx.x;
+  const float* part = a.part + out * a.chunks * D;
+  const float* ml = a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D + out * a.chunks * 2;
+  float m = -INFINITY;
+  for (int k = 0; k < count; ++k) m = fmaxf(m, ml[2 * k]);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float total = 0.0f;
+  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int d = lane * 4;
+  for (int k = 0; k < count; ++k) {
+    const float f = __builtin_amdgcn_exp2f(ml[2 * k] - base);
+    total += ml[2 * k + 1] * f;
+    if (d < D) y += *reinterpret_cast<const v4f*>(part + static_cast<int64_t>(k) * D + d) * f;
+  }
+  y *= total == 0.0f ? 0.0f : 1.0f / total;
+  if (d < D) store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+}
+
+// How a call is cut: row tiles per workgroup and tokens per chunk, from the sizes that the host knows.
+struct AttnQ4Plan {
+  int tiles, row_blocks, chunk, chunks;
+};
+
+static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
+  AttnQ4Plan p;
+  const int64_t rows = n * (Hq / Hk), most = D > 128 ? 2 : 4;
+  p.tiles = static_cast<int>(rows <= 16 ? 1 : rows <= 32 ? 2 : most);
+  p.row_blocks = static_cast<int>((rows + 16 * p.tiles - 1) / (16 * p.tiles));
+  const int64_t groups = std::max<int64_t>(1, B * Hk * p.row_blocks), want = (4096 + groups - 1) / groups;
+  int64_t chunk = (max_len + want - 1) / want;
+  chunk = std::max<int64_t>(256, std::min<int64_t>(2048, chunk));
+  chunk = std::max(chunk, (max_len + std::max<int64_t>(64, want) - 1) / std::max<int64_t>(64, want));
+  p.chunk = static_cast<int>((chunk + 127) / 128 * 128);
+  p.chunks = static_cast<int>((max_len + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+template <int NB>
+static void launch_attn_q4(const AttnQ4Args& a, int tiles, dim3 g, hipStream_t st) {
+  if (tiles == 1) hipLaunchKernelGGL((attn_q4_kernel<NB, 1>), g, dim3(256), 0, st, a);
+  else if (tiles == 2 || NB > 4) hipLaunchKernelGGL((attn_q4_kernel<NB, 2>), g, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((attn_q4_kernel<NB, NB <= 4 ? 4 : 2>), g, dim3(256), 0, st, a);
 }
 
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
@@ -84,7 +446,8 @@ using namespace qmm;
 
 extern "C" size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   if (!attn_q4_shape(B, n, Hq, Hk, D, max_len)) return 0;
-  return 0;
+  const int64_t chunks = attn_q4_plan(B, n, Hq, Hk, D, max_len).chunks;
+  return chunks == 1 ? 0 : static_cast<size_t>(B * n * Hq * chunks * (D + 2) * 4 + 15) / 16 * 16;
 }
 
 extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* cache, int64_t pages, int64_t page,
@@ -101,9 +464,28 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
   if (!aligned16(q) || !aligned16(cache) || !aligned16(table) || !aligned16(lens) || !aligned16(y) || !aligned16(ws))
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
-  const AttnQ4Args a{q, static_cast<const uint8_t*>(cache), table, lens, y, q_stride, pages, page, W, window, scale,
-                     static_cast<int>(B), static_cast<int>(n), static_cast<int>(Hq), static_cast<int>(Hk),
-                     static_cast<int>(D), type, y_type};
-  hipLaunchKernelGGL(attn_q4_kernel, dim3(static_cast<unsigned>(B * n * Hq)), dim3(64), 0, to_stream(stream), a);
+  const AttnQ4Plan p = attn_q4_plan(B, n, Hq, Hk, D, W * page);
+  const int64_t grid = B * Hk * p.row_blocks * p.chunks;
+  if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
+  const int cells = static_cast<int>(page / kCellTokens);
+  int shift = 0;
+  while ((1 << shift) < cells) ++shift;
+  const AttnQ4Args a{q, static_cast<const uint8_t*>(cache), table, lens, y, static_cast<float*>(ws), q_stride, pages, W,
+                     W * page, scale, static_cast<int>(window), static_cast<int>(B), static_cast<int>(n),
+                     static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk),
+                     static_cast<int>(n * (Hq / Hk)), p.row_blocks, p.chunks, p.chunk, cells,
+                     (1 << shift) == cells ? shift : -1, type == QMM_BF16, y_type};
+  const dim3 g(static_cast<unsigned>(grid));
+  hipStream_t st = to_stream(stream);
+  switch (D) {
+    case 64: launch_attn_q4<2>(a, p.tiles, g, st); break;
+    case 96: launch_attn_q4<3>(a, p.tiles, g, st); break;
+    case 128: launch_attn_q4<4>(a, p.tiles, g, st); break;
+    case 192: launch_attn_q4<6>(a, p.tiles, g, st); break;
+    default: launch_attn_q4<8>(a, p.tiles, g, st); break;
+  }
+  if (p.chunks > 1)
+    hipLaunchKernelGGL(attn_q4_join_kernel, dim3(static_cast<unsigned>(B * n * Hq)), dim3(64), 0, st, a,
+                       static_cast<int>(D));
   return launch_status();
 }

@@ -5,8 +5,8 @@ at most D + 8 roundings of 2^-24 of sum |q||k| scale, with those of the scale's
 product and of the exponent's argument.  The exponential itself is right to
 2^-21 relative (two units of its last place and its argument's).  So a term of
 the softmax is off by its score's error and that, the term meets the values
-rounded to 16 bits (2^-12 relative in f16, 2^-9 in bf16, or below 2^-30 of the
-largest), and the sums over n keys add at most n + 64 roundings.  Terms and
+rounded to 16 bits (half a step: 2^-11 relative in f16, with 10 bits of fraction,
+2^-8 in bf16, with 7; or below 2^-30 of the largest), and the sums over n keys add at most n + 64 roundings.  Terms and
 their sum are off alike, so twice; the error of y is that times sum p |v|.
 """
 import numpy as np

@@ -13,7 +13,7 @@ import quantized_matmul_q8_amd as qmm
 pytestmark = pytest.mark.gpu
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
-TERM = {F16: 2.0**-12, BF16: 2.0**-9}
+TERM = {F16: 2.0**-11, BF16: 2.0**-8}
 
 
 def cu(lens, start=0):
