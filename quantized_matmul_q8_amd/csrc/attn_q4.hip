@@ -42,22 +42,41 @@ struct AttnQ4Args {
   int64_t q_stride, pages, W;
   int64_t max_len;
   float scale;
-  int window, B, n, Hq, Hk, group, rows, row_blocks, chunks, chunk, cells, cell_shift;
+  int window, B, n, Hq, Hk, group, rows, row_blocks, chunks, chunk, cells;
+  // a cell's page is cell * page_mul >> page_shift: right for cells below 2^31
+  uint32_t page_mul, page_shift;
   bool bf16;
   int y_type;
 };
 
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
 
-// Eight codes of a dword -> the f16 numbers of pairs (0, 4), (1, 5), (2, 6), (3, 7), less the bits' offsets.
-__device__ __forceinline__ void codes(uint32_t w, h2 (&x)[4]) {
+// The constants of a code's unpacking, in vector registers that the compiler
+// cannot see through: an instruction has room for one literal, so with these an
+// and and an or are one (v_bfi), not two.
+struct Magic {
+  uint32_t low = 0x000f000fu, high = 0x00f000f0u, big = 0x64006400u, small = 0x54005400u;
+  __device__ __forceinline__ Magic() {
+    __asm__ volatile("" : "+v"(big), "+v"(small));
+    __asm__ volatile("" : "+s"(low), "+s"(high));
+  }
+};
+
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  __asm__("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(bits));
+  return r;
+}
+
+// Eight codes of a dword -> the f16 numbers of pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ void codes(uint32_t w, const Magic& k, h2 (&x)[4]) {
   const h2 big = {static_cast<_Float16>(1024.0f), static_cast<_Float16>(1024.0f)};
   const h2 small = {static_cast<_Float16>(64.0f), static_cast<_Float16>(64.0f)};
   const uint32_t u = w >> 8;
-  x[0] = as_h2((w & 0x000f000fu) | 0x64006400u) - big;
-  x[1] = as_h2((w & 0x00f000f0u) | 0x54005400u) - small;
-  x[2] = as_h2((u & 0x000f000fu) | 0x64006400u) - big;
-  x[3] = as_h2((u & 0x00f000f0u) | 0x54005400u) - small;
+  x[0] = as_h2(and_or(w, k.low, k.big)) - big;
+  x[1] = as_h2(and_or(w, k.high, k.small)) - small;
+  x[2] = as_h2(and_or(u, k.low, k.big)) - big;
+  x[3] = as_h2(and_or(u, k.high, k.small)) - small;
 }
 
 __device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
@@ -138,9 +157,9 @@ struct Cell {
   }
 
   // A operand of the products with the queries, number j.
-  __device__ __forceinline__ h8 key_operand(int j) const {
+  __device__ __forceinline__ h8 key_operand(int j, const Magic& magic) const {
     h2 x[4];
-    codes(k[j], x);
+    codes(k[j], magic, x);
     const int s = j < 4 * Runs<NB>::kQuads ? j / 4 : (Runs<NB>::kPair && j < 4 * Runs<NB>::kQuads + 2) ? Runs<NB>::kQuads
                                                                                                     : Runs<NB>::kScales - 1;
     const h2 dm = as_h2(ks[s]), d = {dm.x, dm.x}, m = {dm.y, dm.y};
@@ -151,9 +170,9 @@ struct Cell {
 
   // This cell's half of the A operands of block b's two tiles: dims c and c + 16, four tokens each.
   template <int b>
-  __device__ __forceinline__ void value_operands(h2 (&low)[2], h2 (&high)[2]) const {
+  __device__ __forceinline__ void value_operands(const Magic& magic, h2 (&low)[2], h2 (&high)[2]) const {
     h2 x[4];
-    codes(v[b], x);
+    codes(v[b], magic, x);
     const uint32_t s = vs[b / 4];
     const h2 d01 = as_h2(row_bcast<b % 4 * 4>(s)), d23 = as_h2(row_bcast<b % 4 * 4 + 1>(s));
     const h2 m01 = as_h2(row_bcast<b % 4 * 4 + 2>(s)), m23 = as_h2(row_bcast<b % 4 * 4 + 3>(s));
@@ -174,17 +193,18 @@ __device__ __forceinline__ int operand_dim(int j, int c) {
 }
 
 template <int NB, int RT, int b = 0>
-__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (&p)[RT], v4f (&o)[RT][2 * NB]) {
+__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const Magic& magic, const h8 (&p)[RT],
+                                           v4f (&o)[RT][2 * NB]) {
   h2 l0[2], u0[2], l1[2], u1[2];
-  cell[0].template value_operands<b>(l0, u0);
-  cell[1].template value_operands<b>(l1, u1);
+  cell[0].template value_operands<b>(magic, l0, u0);
+  cell[1].template value_operands<b>(magic, l1, u1);
   const h8 low = join(l0[0], l0[1], l1[0], l1[1]), high = join(u0[0], u0[1], u1[0], u1[1]);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     o[r][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(low, p[r], o[r][2 * b], 0, 0, 0);
     o[r][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(high, p[r], o[r][2 * b + 1], 0, 0, 0);
   }
-  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, p, o);
+  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, magic, p, o);
 }
 
 template <int NB, int RT>
@@ -201,7 +221,7 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
   const int row_block = id % a.row_blocks;
   id /= a.row_blocks;
   const int kh = id % a.Hk, seq = id / a.Hk;
-  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(a.lens[seq]))));
+  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(as_scalar(a.lens)[seq]))));
   // the first key that any query sees, in whole steps
   const int floor_at = a.window > 0 ? max(0, len - a.n - a.window + 1) : 0;
   const int first = floor_at / kStep * kStep;
@@ -220,7 +240,7 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
     const int i = on ? row / a.group : a.n - 1, h = kh * a.group + (on ? row % a.group : 0);
     at[r] = len - a.n + i;
     const int64_t base = (static_cast<int64_t>(seq) * a.n + i) * a.q_stride + static_cast<int64_t>(h) * D;
-    mul[r] = a.scale * 1.44269504088896340736f;
+    mul[r] = fabsf(a.scale) * 1.44269504088896340736f;
     if (!a.bf16) {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
@@ -243,112 +263,135 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(f[j][k], -e));
     }
+    // a factor above zero, so that the largest product is the largest score
+    const _Float16 sign = static_cast<_Float16>(mul[r] == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) q[r][j] *= sign;
+    mul[r] = mul[r] == 0.0f ? 1.0f : mul[r];
   }
 
   v4f o[RT][2 * NB];
-  float top[RT], sum[RT];
+  // the largest product so far, what is added to a product's exponent for it, and this lane's part of the sum
+  float top[RT], base[RT], sum[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    top[r] = -INFINITY, sum[r] = 0.0f;
+    top[r] = -INFINITY, base[r] = kLift, sum[r] = 0.0f;
 #pragma unroll
     for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const int32_t* pages = a.table + static_cast<int64_t>(seq) * a.W;
-  const int64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
+  const scalar_ints pages = as_scalar(a.table + static_cast<int64_t>(seq) * a.W);
+  const uint64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
   const uint8_t* head = a.cache + kh * head_bytes;
-  const int last_cell = (len - 1) / kCellTokens;  // nothing behind it is looked up
-  const auto page_of = [&](int cell) { return a.cell_shift >= 0 ? cell >> a.cell_shift : cell / a.cells; };
-  const auto page_at = [&](int token) { return pages[page_of(min(token / kCellTokens, last_cell))]; };
-  const auto cell_at = [&](int token, int page) {
-    const int cell = min(token / kCellTokens, last_cell);
-    const int64_t pg = page >= 0 && page < a.pages ? page : 0;
-    return head + pg * page_bytes + (cell - page_of(cell) * a.cells) * cell_bytes;
+  const uint32_t last_cell = static_cast<uint32_t>(max(0, len - 1)) / kCellTokens;  // nothing behind it is looked up or loaded
+  const auto page_of = [&](uint32_t cell) {
+    return static_cast<uint32_t>(static_cast<uint64_t>(cell) * a.page_mul >> a.page_shift);
+  };
+  const auto there = [&](int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages); };
+  const Magic magic;
+
+  // one step's two cells and their page numbers
+  struct Step {
+    Cell<NB> cell[2];
+    int page[2];
+  };
+  const auto look_up = [&](int t, int (&page)[2]) {
+#pragma unroll
+    for (uint32_t u = 0; u < 2; ++u) page[u] = pages[page_of(min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell))];
+  };
+  const auto load = [&](Step& s, int t, const int (&page)[2]) {
+#pragma unroll
+    for (uint32_t u = 0; u < 2; ++u) {
+      const uint32_t cell = min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell);
+      const uint32_t pg = there(page[u]) ? page[u] : 0;
+      s.cell[u].load(head + pg * page_bytes + (cell - page_of(cell) * a.cells) * static_cast<uint32_t>(cell_bytes), lane);
+      s.page[u] = page[u];
+    }
+  };
+  const auto work = [&](Step& st, int t) {
+    const bool there0 = there(st.page[0]), there1 = there(st.page[1]);
+    // whether every query sees the whole step
+    const bool whole = t + kStep <= len - a.n + 1 && t >= (a.window > 0 ? len - a.window : 0) && there0 && there1;
+    v4f s[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const h8 k = st.cell[u].key_operand(j, magic);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
+      }
+    if (!whole) {
+      const int lo = floor_at - t, hi = len - t;
+      st.cell[0].clear_scales(lane, there0 ? lo : 16, hi);
+      st.cell[1].clear_scales(lane, there1 ? lo - 16 : 16, hi - 16);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int j = t + (k >> 2) * kCellTokens + 4 * c + (k & 3);
+          const bool seen = j <= at[r] && (a.window == 0 || j > at[r] - a.window) && (k < 4 ? there0 : there1);
+          s[r][k >> 2][k & 3] = seen ? s[r][k >> 2][k & 3] : -INFINITY;
+        }
+    }
+    h8 p[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float most = top[r];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = fmaxf(most, s[r][k >> 2][k & 3]);
+      most = rows_max(most);
+      if (__builtin_amdgcn_ballot_w64(most > top[r])) {
+        const float keep = __builtin_amdgcn_exp2f((top[r] - (most == -INFINITY ? 0.0f : most)) * mul[r]);
+        sum[r] *= keep;
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
+        top[r] = most;
+        base[r] = kLift - (most == -INFINITY ? 0.0f : most) * mul[r];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3], mul[r], base[r]));
+        sum[r] += e;
+        p[r][k] = static_cast<_Float16>(e);
+      }
+    }
+    add_values<NB, RT>(st.cell, magic, p, o);
   };
 
+  // Loads run one step ahead in the other buffer and look-ups two; behind the
+  // end they repeat the last cell, so that every step waits for the same loads.
   const int stride = kWaves * kStep;
   int t = begin + wave * kStep;
   if (t < end) {
-    Cell<NB> cell[2];
-    int pg[2] = {page_at(t), page_at(t + kCellTokens)};
-    cell[0].load(cell_at(t, pg[0]), lane);
-    cell[1].load(cell_at(t + kCellTokens, pg[1]), lane);
-    int next_pg[2] = {page_at(t + stride), page_at(t + stride + kCellTokens)};
-    for (;;) {
-      const bool more = t + stride < end;
-      Cell<NB> next[2];
-      if (more) {
-        next[0].load(cell_at(t + stride, next_pg[0]), lane);
-        next[1].load(cell_at(t + stride + kCellTokens, next_pg[1]), lane);
-      }
-      const int ahead[2] = {page_at(t + 2 * stride), page_at(t + 2 * stride + kCellTokens)};
-      const bool there0 = pg[0] >= 0 && pg[0] < a.pages, there1 = pg[1] >= 0 && pg[1] < a.pages;
-      // whether every query sees the whole step
-      const bool whole = t + kStep <= len - a.n + 1 && t >= (a.window > 0 ? len - a.window : 0) && there0 && there1;
-
-      h8 p[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) p[r] = h8{};
-      v4f s[RT][2];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const h8 k = cell[u].key_operand(j);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
-        }
-      if (!whole) {
-        const int lo = floor_at - t, hi = len - t;
-        cell[0].clear_scales(lane, there0 ? lo : 16, hi);
-        cell[1].clear_scales(lane, there1 ? lo - 16 : 16, hi - 16);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float x[8], most = top[r];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = s[r][k >> 2][k & 3] * mul[r];
-        if (!whole) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = t + (k >> 2) * kCellTokens + 4 * c + (k & 3);
-            const bool seen = j <= at[r] && (a.window == 0 || j > at[r] - a.window) && (k < 4 ? there0 : there1);
-            x[k] = seen ? x[k] : -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) most = fmaxf(most, x[k]);
-        most = rows_max(most);
-        if (__builtin_amdgcn_ballot_w64(most > top[r])) {
-          const float keep = __builtin_amdgcn_exp2f(top[r] - (most == -INFINITY ? 0.0f : most));
-          sum[r] *= keep;
-#pragma unroll
-          for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
-          top[r] = most;
-        }
-        const float base = kLift - (most == -INFINITY ? 0.0f : most);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float e = __builtin_amdgcn_exp2f(x[k] + base);
-          sum[r] += e;
-          p[r][k] = static_cast<_Float16>(e);
-        }
-      }
-      add_values<NB, RT>(cell, p, o);
-      if (!more) break;
-      t += stride;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) cell[u] = next[u], pg[u] = next_pg[u], next_pg[u] = ahead[u];
+    Step x, y;
+    int page[2], ahead[2];
+    look_up(t, page);
+    look_up(t + stride, ahead);
+    load(x, t, page);
+    // in pairs, with no way out between the two: each step then waits for its own loads alone
+    const int steps = (end - t + stride - 1) / stride;
+    for (int k = 1; k < steps; k += 2) {
+      load(y, t + stride, ahead);
+      look_up(t + 2 * stride, ahead);
+      __builtin_amdgcn_sched_barrier(0);  // all of these before the work, not sunk to their use
+      work(x, t);
+      load(x, t + 2 * stride, ahead);
+      look_up(t + 3 * stride, ahead);
+      __builtin_amdgcn_sched_barrier(0);
+      work(y, t + stride);
+      t += 2 * stride;
     }
+    if (steps & 1) work(x, t);
   }
 
   // join the waves, tile by tile, and write
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const float l = rows_sum(sum[r]);
-    if (c == 0) s_m[wave][col] = top[r], s_l[wave][col] = l;
+    if (c == 0) s_m[wave][col] = top[r] * mul[r], s_l[wave][col] = l;
 #pragma unroll
     for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&s_o[wave][col][b * 16 + 4 * c]) = o[r][b];
     __syncthreads();
@@ -384,29 +427,43 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
   }
 }
 
-// Joins the chunks of one row; sequences of one chunk have been written.
+// Joins the chunks of one row; sequences of one chunk have been written.  A
+// wave per row: the chunks' maxima and sums by its lanes, 64 at a time, then
+// the chunks in order, four loads in flight.
 __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   const int64_t out = blockIdx.x;
   const int seq = static_cast<int>(out / (static_cast<int64_t>(a.n) * a.Hq));
-  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(a.lens[seq]))));
+  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(as_scalar(a.lens)[seq]))));
   const int first = a.window > 0 ? max(0, len - a.n - a.window + 1) / kStep * kStep : 0;
   if (len - first <= a.chunk) return;
   const int count = (len - first + a.chunk - 1) / a.chunk, lane = threadIdx.x;
   const float* part = a.part + out * a.chunks * D;
-  const float* ml = a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D + out * a.chunks * 2;
-  float m = -INFINITY;
-  for (int k = 0; k < count; ++k) m = fmaxf(m, ml[2 * k]);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float total = 0.0f;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D) +
+                     out * a.chunks;
+  const int d = min(lane * 4, D - 4);
+  float m = -INFINITY, total = 0.0f;
   v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int d = lane * 4;
-  for (int k = 0; k < count; ++k) {
-    const float f = __builtin_amdgcn_exp2f(ml[2 * k] - base);
-    total += ml[2 * k + 1] * f;
-    if (d < D) y += *reinterpret_cast<const v4f*>(part + static_cast<int64_t>(k) * D + d) * f;
+  for (int k0 = 0; k0 < count; k0 += 64) {
+    const int here = min(64, count - k0);
+    const float2 own = lane < here ? ml[k0 + lane] : make_float2(-INFINITY, 0.0f);
+    float most = fmaxf(m, rows_max(own.x));
+#pragma unroll
+    for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
+    const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
+    const float f = __builtin_amdgcn_exp2f(own.x - base);
+    total = total * keep + wave_sum(own.y * f);
+    y *= keep;
+    m = most;
+    for (int k = 0; k < here; k += 4) {
+      v4f x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + static_cast<int64_t>(k0 + min(k + i, here - 1)) * D + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y += x[i] * (k + i < here ? __shfl(f, k + i) : 0.0f);
+    }
   }
   y *= total == 0.0f ? 0.0f : 1.0f / total;
-  if (d < D) store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+  if (lane * 4 < D) store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
 
 // How a call is cut: row tiles per workgroup and tokens per chunk, from the sizes that the host knows.
@@ -468,13 +525,13 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
   const int64_t grid = B * Hk * p.row_blocks * p.chunks;
   if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const int cells = static_cast<int>(page / kCellTokens);
-  int shift = 0;
-  while ((1 << shift) < cells) ++shift;
+  uint32_t shift = 31;
+  while ((int64_t{1} << (shift - 31)) < cells) ++shift;
   const AttnQ4Args a{q, static_cast<const uint8_t*>(cache), table, lens, y, static_cast<float*>(ws), q_stride, pages, W,
                      W * page, scale, static_cast<int>(window), static_cast<int>(B), static_cast<int>(n),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk),
                      static_cast<int>(n * (Hq / Hk)), p.row_blocks, p.chunks, p.chunk, cells,
-                     (1 << shift) == cells ? shift : -1, type == QMM_BF16, y_type};
+                     static_cast<uint32_t>(((uint64_t{1} << shift) + cells - 1) / cells), shift, type == QMM_BF16, y_type};
   const dim3 g(static_cast<unsigned>(grid));
   hipStream_t st = to_stream(stream);
   switch (D) {

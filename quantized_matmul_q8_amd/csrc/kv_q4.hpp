@@ -20,6 +20,13 @@ __device__ __forceinline__ int64_t kv_cell(int64_t slot, int64_t page, int h, in
   return ((p * Hk + h) * (page / kCellTokens) + (slot - p * page) / kCellTokens) * (20 * D);
 }
 
+// Memory that nothing writes while the kernel runs, read at addresses that are
+// the same for the whole wave: through the scalar cache.
+typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
+__device__ __forceinline__ scalar_ints as_scalar(const int32_t* p) {
+  return reinterpret_cast<scalar_ints>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Where byte i of a quad's four value codes stands: tokens 0, 2, 1, 3.
 __device__ __forceinline__ int kv_quad_byte(int t) { return (t & 1) * 2 + (t >> 1); }
 
