@@ -214,13 +214,16 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
-  // chunks of a sequence and head next to each other
-  int id = blockIdx.x;
-  const int chunk = id % a.chunks;
-  id /= a.chunks;
-  const int row_block = id % a.row_blocks;
-  id /= a.row_blocks;
-  const int kh = id % a.Hk, seq = id / a.Hk;
+  // Workgroups go to the eight dies in turn.  The chunk varies slowest, so that
+  // every die has as many of the later ones, which short sequences lack (with it
+  // fastest, 64 x 8192 of ragged lengths took 109 us); the row blocks of one
+  // chunk, which read the same tokens, are eight apart, so on one die.
+  const int span = kXcds * a.row_blocks, row_block = blockIdx.x % span / kXcds;
+  int id = blockIdx.x / span * kXcds + blockIdx.x % kXcds;
+  const int kh = id % a.Hk;
+  id /= a.Hk;
+  const int seq = id % a.B, chunk = id / a.B;
+  if (chunk >= a.chunks) return;
   const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(as_scalar(a.lens)[seq]))));
   // the first key that any query sees, in whole steps
   const int floor_at = a.window > 0 ? max(0, len - a.n - a.window + 1) : 0;
@@ -522,7 +525,7 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
   const AttnQ4Plan p = attn_q4_plan(B, n, Hq, Hk, D, W * page);
-  const int64_t grid = B * Hk * p.row_blocks * p.chunks;
+  const int64_t grid = (B * Hk * p.chunks + kXcds - 1) / kXcds * kXcds * p.row_blocks;
   if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const int cells = static_cast<int>(page / kCellTokens);
   uint32_t shift = 31;
