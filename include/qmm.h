@@ -409,9 +409,9 @@ int swiglu_q8_1(const float* g_u, void* hq, int64_t R, int64_t F, void* stream);
  * product and the output product.  Heads of D values; Hq query heads share Hk
  * key heads, query head h reading key head h / (Hq / Hk).  q, k and v are rows
  * [T][stride] with a token's heads next to each other from its first value
- * on; a stride is a count of values, at least heads * D and a multiple of 8,
- * so that slices of the stacked product's rows are taken as they are (each
- * pointer 16-byte aligned).  Other buffers have no gaps.
+ * on; a stride is a count of values, at least heads * D, a multiple of 8 and
+ * below 2^24, so that slices of the stacked product's rows are taken as they
+ * are (each pointer 16-byte aligned).  Other buffers have no gaps.
  *
  * Rotation tables are fp32 [P][rot]: row p holds rot/2 cosines, then rot/2
  * sines, of the angles at position p.  Pair i of a head, at angle i, is values
@@ -543,13 +543,20 @@ size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
  * rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
  * values.
  * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
- * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, and (Tq/64 + B) * Hq <
- * 2^31.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.
+ * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, Tq * Hq and B * Hq
+ * below 2^30.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.
+ * ws: attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D) bytes of scratch, no
+ * initialisation needed; may be NULL where that is 0.  Calls that share it
+ * must be ordered on one stream.
  */
 int attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                 int type, const int32_t* cu_q, const int32_t* cu_k, int64_t B, float scale, int causal,
                 int64_t window, void* y, int y_type, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
-                void* stream);
+                void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of attn_prompt: 0 but for few rows of q against many
+ * keys, and for sizes that attn_prompt refuses. */
+size_t attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
 
 /* Bytes of workspace needed by `op` (QMM_OP_MMQ, QMM_OP_MOE or
  * QMM_OP_MOE_SLOTS) for the given sizes; unused sizes may be 0.  Returns 0

@@ -26,7 +26,7 @@ from ._lib import (  # noqa: F401
 
 __all__ = [
     "q8_1_quantize", "q8_1_dequantize", "rms_norm_q8_1", "moe_router", "mmvq_q4g", "qk_norm_rope", "kv_cache_q4", "kv_append_q4", "kv_read_q4", "attn_q4",
-    "attn_q4_workspace_bytes", "attn_prompt", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
+    "attn_q4_workspace_bytes", "attn_prompt", "attn_prompt_workspace_bytes", "mmvq_q4k", "mmvq_q5k", "mmvq_q6k", "mmvq_pair", "mmq_q4k", "mmq_q5k", "mmq_q6k", "mmq_q4k_f32", "mmq_q5k_f32",
     "mmq_q6k_f32",
     "moe_grouped_mmq", "moe_grouped_swiglu", "moe_ffn", "moe_slot_mmvq",
     "swiglu_q8_1", "workspace", "workspace_bytes", "debug_subdots", "probe_read", "probe_read_geom",
@@ -536,9 +536,14 @@ def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     return out
 
 
+def attn_prompt_workspace_bytes(B: int, Tq: int, Tk: int, Hq: int, Hk: int, D: int) -> int:
+    """Bytes of workspace of :func:`attn_prompt`."""
+    return int(_lib.LIB.attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D))
+
+
 def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor | None = None,
                 *, causal: bool = True, window: int = 0, scale: float | None = None, out: torch.Tensor | None = None,
-                out_dtype: torch.dtype | None = None) -> torch.Tensor:
+                out_dtype: torch.dtype | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Attention over whole prompts, packed one behind the other.
 
     ``q`` [Tq, Hq, D], ``k`` and ``v`` [Tk, Hk, D], float16 or bfloat16, rows as
@@ -571,9 +576,15 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     _on(index, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
     out = _out(out, (Tq, Hq, D), out_dtype or (q.dtype if out is None else out.dtype), q.device)
     yt = _typed(out, "out", 3)
+    need = _lib.LIB.attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    else:
+        _need(ws, torch.uint8, "ws", 1)
+        _on(index, ws=ws)
     _enqueue(index, _lib.LIB.attn_prompt, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, cu_q.data_ptr(),
              cu_k.data_ptr(), B, D ** -0.5 if scale is None else scale, int(bool(causal)), window, out.data_ptr(), yt, Tq,
-             Tk, Hq, Hk, D)
+             Tk, Hq, Hk, D, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out
 
 

@@ -58,7 +58,8 @@ SIGNATURES = {
                      _vp, _sz, _vp]),
     "attn_q4_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
     "attn_prompt": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _vp, _i64, _f, _i, _i64, _vp, _i, _i64, _i64, _i64,
-                         _i64, _i64, _vp]),
+                         _i64, _i64, _vp, _sz, _vp]),
+    "attn_prompt_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
     "mmvq_q4k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q5k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "mmvq_q6k": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),

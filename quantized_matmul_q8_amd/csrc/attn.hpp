@@ -1,0 +1,71 @@
+// Shared by the attention kernels: the running maximum and sum of a softmax
+// over lanes, and the joining of partial results.
+#pragma once
+
+#include "typed.hpp"
+
+namespace qmm {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+inline bool attn_head_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
+
+// Over lanes l and l ^ 32, in both: one exchange of the wave's halves.
+template <typename F>
+__device__ __forceinline__ float halves_join(float v, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return f(__builtin_bit_cast(float, static_cast<uint32_t>(b[0])), __builtin_bit_cast(float, static_cast<uint32_t>(b[1])));
+}
+// Over the four rows of 16 lanes, in all of them.
+template <typename F>
+__device__ __forceinline__ float rows_join(float v, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return halves_join(f(__builtin_bit_cast(float, static_cast<uint32_t>(a[0])),
+                       __builtin_bit_cast(float, static_cast<uint32_t>(a[1]))), f);
+}
+__device__ __forceinline__ float rows_max(float v) {
+  return rows_join(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  return rows_join(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float halves_max(float v) {
+  return halves_join(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  return halves_join(v, [](float a, float b) { return a + b; });
+}
+
+// One row of four dims per lane from `count` partial results: part + k * step
+// holds number k's sums of terms times values, ml[k * ml_step] its maximum and
+// sum of terms.  The maxima and sums by the lanes, 64 at a time, then the
+// partial results in order, four loads in flight.  Zeros if all sums are 0.
+__device__ __forceinline__ v4f join_parts(const float* part, int64_t step, const float2* ml, int64_t ml_step, int count,
+                                          int lane) {
+  float m = -INFINITY, total = 0.0f;
+  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = 0; k0 < count; k0 += 64) {
+    const int here = min(64, count - k0);
+    const float2 own = lane < here ? ml[(k0 + lane) * ml_step] : make_float2(-INFINITY, 0.0f);
+    float most = fmaxf(m, rows_max(own.x));
+#pragma unroll
+    for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
+    const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
+    const float f = __builtin_amdgcn_exp2f(own.x - base);
+    total = total * keep + wave_sum(own.y * f);
+    y *= keep;
+    m = most;
+    for (int k = 0; k < here; k += 4) {
+      v4f x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + (k0 + min(k + i, here - 1)) * step);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y += x[i] * (k + i < here ? __shfl(f, k + i) : 0.0f);
+    }
+  }
+  return y * (total == 0.0f ? 0.0f : 1.0f / total);
+}
+
+}  // namespace qmm

@@ -1,14 +1,31 @@
 // Attention over whole prompts, packed sequences.
 //
-// One wave per query row and head: scores key by key, with the running maximum
-// and sum of the softmax.
-#include "typed.hpp"
+//   S^T = K Q^T,  p = 2^(c s - m),  O^T = V^T P^T,  y = O / sum p
+//
+// The rows of one key head (tokens x heads of the group) are the columns of
+// 32 x 32 tiles; a wave has 32 of them, a workgroup 128, which share tiles of K
+// and V in LDS, copied there by the loads themselves one tile ahead.  S^T's
+// layout leaves in each lane the terms of one query and eight keys of every
+// sixteen, which is the operand that O^T takes: the terms stay in registers.
+// V comes out of its rows transposed by the LDS's transposing reads.  Chunks of
+// 16 bytes stand permuted within a tile's rows so that neither the reads of 32
+// rows of K nor those of four rows of V meet in the LDS's banks.
+//
+// With the heads of a group in one tile a tile of 128 rows spans few tokens, so
+// little of it lies behind the causal border, and K and V are read once for the
+// group.
+#include "attn.hpp"
 
+#include <algorithm>
 #include <math.h>
 
 namespace qmm {
 
-inline bool prompt_head_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRows = 128;  // of a workgroup's tile: four waves of 32
 
 struct PromptArgs {
   const void* q;
@@ -17,82 +34,434 @@ struct PromptArgs {
   const int32_t* cu_q;
   const int32_t* cu_k;
   void* y;
-  int64_t q_stride, k_stride, v_stride, window, Tq, Tk;
+  float* part;  // [tiles][Hk][splits][128][D], then as many pairs (m, l) of rows
+  int64_t q_stride, k_stride, v_stride;
   float scale;
-  int B, Hq, Hk, D, type, y_type;
+  int window, Tq, Tk, B, Hq, Hk, group, splits, tiles, y_type;
   bool causal;
 };
 
-__device__ __forceinline__ float prompt_load(int type, const void* p, int64_t i) {
-  if (type == QMM_F16) return static_cast<float>(static_cast<const _Float16*>(p)[i]);
-  return static_cast<float>(static_cast<const __bf16*>(p)[i]);
+// An operand of eight 16-bit values, four dwords.
+__device__ __forceinline__ v4u op4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return v4u{a, b, c, d}; }
+template <bool BF16>
+__device__ __forceinline__ v16f mfma32(v4u x, v4u y, v16f c) {
+  if constexpr (BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
 }
 
-__global__ __launch_bounds__(64) void attn_prompt_kernel(PromptArgs a) {
-  const int lane = threadIdx.x;
-  const int64_t row = blockIdx.x / a.Hq;
-  const int h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hk);
-  int b = 0;
-  while (b < a.B && row >= a.cu_q[b + 1]) ++b;
-  if (b == a.B || row < a.cu_q[b]) return;
-  const auto within = [](int64_t x, int64_t lo, int64_t hi) { return max(lo, min(hi, x)); };
-  const int64_t q0 = within(a.cu_q[b], 0, a.Tq), q1 = within(a.cu_q[b + 1], q0, a.Tq);
-  const int64_t k0 = within(a.cu_k[b], 0, a.Tk), k1 = within(a.cu_k[b + 1], k0, a.Tk);
-  const int64_t nk = k1 - k0, at = nk - (q1 - q0) + (row - q0);
-  const int64_t first = a.window > 0 ? max(int64_t{0}, at - a.window + 1) : 0, last = a.causal ? at : nk - 1;
-  float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = -INFINITY, sum = 0.0f;
-  for (int r = 0; r < 4; ++r) {
-    const int d = lane + 64 * r;
-    q[r] = d < a.D ? prompt_load(a.type, a.q, row * a.q_stride + h * a.D + d) * a.scale : 0.0f;
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, b2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+  } else {
+    typedef _Float16 f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, f2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
   }
-  for (int64_t j = first; j <= last; ++j) {
-    float s = 0.0f, v[4];
-    for (int r = 0; r < 4; ++r) {
-      const int d = lane + 64 * r;
-      v[r] = 0.0f;
-      if (d >= a.D) continue;
-      s += q[r] * prompt_load(a.type, a.k, (k0 + j) * a.k_stride + kh * a.D + d);
-      v[r] = prompt_load(a.type, a.v, (k0 + j) * a.v_stride + kh * a.D + d);
+}
+
+// 16 bytes per lane from base + off into LDS at lds + 16 * lane; see dma16.
+__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                   : "=&s"(saved)
+                   : "v"(off), "s"(base), "s"(lds)
+                   : "memory");
+}
+
+constexpr int gcd16(int c) { return c % 16 == 0 ? 16 : c % 8 == 0 ? 8 : c % 4 == 0 ? 4 : c % 2 == 0 ? 2 : 1; }
+
+// Which sequence a tile belongs to, by the waves' lanes: 64 sequences at a time.
+struct Place {
+  int q0, nq, k0, nk, tile;  // the sequence's first rows and counts, and the tile's number in it
+  bool found;
+};
+__device__ __forceinline__ Place find_place(const PromptArgs& a, int n, int lane) {
+  Place p{0, 0, 0, 0, 0, false};
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int b = min(b0 + lane, a.B - 1);
+    const int q0 = max(0, min(a.Tq, a.cu_q[b])), q1 = max(q0, min(a.Tq, a.cu_q[b + 1]));
+    const int mine = b0 + lane < a.B ? ((q1 - q0) * a.group + kRows - 1) / kRows : 0;
+    int upto = mine;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+      const int o = __shfl_up(upto, k);
+      upto += lane >= k ? o : 0;
     }
-    s = wave_sum(s);
-    if (s == -INFINITY) continue;
-    const float up = fmaxf(top, s), keep = expf(top - up), p = expf(s - up);
-    sum = sum * keep + p;
-    for (int r = 0; r < 4; ++r) o[r] = o[r] * keep + p * v[r];
-    top = up;
+    const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > n);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      p.q0 = __builtin_amdgcn_readlane(q0, at);
+      p.nq = __builtin_amdgcn_readlane(q1, at) - p.q0;
+      // a sequence's last tiles, which see the most keys, first
+      p.tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - n;
+      const int k0 = max(0, min(a.Tk, a.cu_k[b0 + at])), k1 = max(k0, min(a.Tk, a.cu_k[b0 + at + 1]));
+      p.k0 = __builtin_amdgcn_readfirstlane(k0);
+      p.nk = __builtin_amdgcn_readfirstlane(k1 - k0);
+      p.found = true;
+      return p;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  for (int r = 0; r < 4; ++r) {
-    const int d = lane + 64 * r;
-    const int64_t i = (row * a.Hq + h) * a.D + d;
-    if (d >= a.D) continue;
-    if (a.y_type == QMM_F32) static_cast<float*>(a.y)[i] = o[r] * inv;
-    else if (a.y_type == QMM_F16) static_cast<_Float16*>(a.y)[i] = static_cast<_Float16>(o[r] * inv);
-    else static_cast<__bf16*>(a.y)[i] = static_cast<__bf16>(o[r] * inv);
+  return p;
+}
+
+template <int D, int BN, bool BF16>
+__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
+  constexpr int C = D / 8, kRowBytes = 2 * D, kTile = BN * kRowBytes;  // chunks of a row
+  constexpr int G = gcd16(C), kPeriod = 16 / G;                        // K: chunk ^ (row / kPeriod) % G
+  constexpr int kVShift = C % 16 == 0 ? 0 : 1, kVMask = C % 16 == 0 ? 3 : C % 8 == 0 ? 1 : 0;  // V: chunk ^ 4 * ...
+  constexpr int kCopies = BN * C / 256;                                // a wave's copies of a tile
+  constexpr int kSteps = D / 16, kBlocks = D / 32, kKeys = BN / 32;
+  constexpr float kLift = BF16 ? 0.0f : 7.0f;  // terms of up to 2^(8 + kLift): f16 holds them, and those down to 2^-31
+  constexpr float kSlack = 8.0f;               // a maximum is followed when it is passed by 2^8
+  __shared__ __attribute__((aligned(1024))) uint8_t s_k[2][kTile], s_v[2][kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, h = lane >> 5;
+
+  int id = blockIdx.x;
+  const int kh = id % a.Hk;
+  id /= a.Hk;
+  const int split = id % a.splits, n = id / a.splits;
+  const Place pl = find_place(a, n, lane);
+  if (!pl.found) return;
+  const int rows = pl.nq * a.group, row0 = pl.tile * kRows + wave * 32, before = pl.nk - pl.nq;
+
+  // this lane's query, and the keys it sees: lo .. at
+  const int row = min(row0 + col, rows - 1), tok = row / a.group, head = kh * a.group + row % a.group;
+  const int at = a.causal ? before + tok : pl.nk - 1, lo = a.window > 0 ? max(0, at - a.window + 1) : 0;
+  float mul = fabsf(a.scale) * 1.44269504088896340736f;
+  v4u q[kSteps];
+  {
+    // the scale's sign into the query, so that the largest product is the largest score
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(pl.q0 + tok) * a.q_stride + head * D;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = mul == 0.0f ? 0u : ~0u;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      q[s] = *reinterpret_cast<const v4u*>(src + s * 16 + h * 8);
+      q[s].x = (q[s].x ^ flip) & keep, q[s].y = (q[s].y ^ flip) & keep;
+      q[s].z = (q[s].z ^ flip) & keep, q[s].w = (q[s].w ^ flip) & keep;
+    }
+    mul = mul == 0.0f ? 1.0f : mul;
   }
+  const float slack = kSlack / mul;
+
+  // the bounds of the wave's rows and of the workgroup's, the same for all lanes
+  const bool active = row0 < rows;
+  const int wave_first = min(row0, rows - 1) / a.group, wave_last = min(row0 + 31, rows - 1) / a.group;
+  const int wave_at0 = a.causal ? before + wave_first : pl.nk - 1, wave_at1 = a.causal ? before + wave_last : pl.nk - 1;
+  const int wave_lo0 = a.window > 0 ? max(0, wave_at0 - a.window + 1) : 0;
+  const int wave_lo1 = a.window > 0 ? max(0, wave_at1 - a.window + 1) : 0;
+  const int first_tok = pl.tile * kRows / a.group, last_tok = min(pl.tile * kRows + kRows - 1, rows - 1) / a.group;
+  const int all_end = max(0, (a.causal ? before + last_tok : pl.nk - 1) + 1);
+  const int all_first = a.window > 0 ? max(0, before + first_tok - a.window + 1) / BN : 0;
+  const int count = max(0, (all_end + BN - 1) / BN - all_first), per = (count + a.splits - 1) / a.splits;
+  const int tile0 = all_first + min(count, split * per), tile1 = all_first + min(count, (split + 1) * per);
+
+  // copies: where each of this lane's chunks stands in a tile of the rows
+  const uint32_t k_bytes = static_cast<uint32_t>(a.k_stride) * 2, v_bytes = static_cast<uint32_t>(a.v_stride) * 2;
+  const auto offsets = [&](int i, int left, uint32_t& k_off, uint32_t& v_off) {
+    const int at16 = (wave * kCopies + i) * 64 + lane, r = at16 / C, c = at16 % C;
+    const uint32_t from = static_cast<uint32_t>(min(r, left));  // rows behind the sequence's last repeat it
+    k_off = from * k_bytes + static_cast<uint32_t>((c ^ ((r / kPeriod) & (G - 1))) * 16);
+    v_off = from * v_bytes + static_cast<uint32_t>((c ^ (4 * ((r >> kVShift) & kVMask))) * 16);
+  };
+  uint32_t k_off[kCopies], v_off[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) offsets(i, BN, k_off[i], v_off[i]);
+  const uint8_t* k_base = static_cast<const uint8_t*>(a.k) + (static_cast<int64_t>(pl.k0) * a.k_stride + kh * D) * 2;
+  const uint8_t* v_base = static_cast<const uint8_t*>(a.v) + (static_cast<int64_t>(pl.k0) * a.v_stride + kh * D) * 2;
+  const uint32_t k_lds = lds_addr(&s_k[0][0]) + wave * (kCopies * 1024), v_lds = lds_addr(&s_v[0][0]) + wave * (kCopies * 1024);
+  const auto copy = [&](int t, int buf) {
+    const uint8_t* kb = k_base + static_cast<int64_t>(t) * BN * k_bytes;
+    const uint8_t* vb = v_base + static_cast<int64_t>(t) * BN * v_bytes;
+    const int left = pl.nk - 1 - t * BN;
+    const uint32_t k_to = k_lds + buf * kTile, v_to = v_lds + buf * kTile;
+    if (left >= BN - 1) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        dma16_at(kb, k_off[i], k_to + i * 1024);
+        dma16_at(vb, v_off[i], v_to + i * 1024);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kCopies; ++i) {
+        uint32_t ko, vo;
+        offsets(i, left, ko, vo);
+        dma16_at(kb, ko, k_to + i * 1024);
+        dma16_at(vb, vo, v_to + i * 1024);
+      }
+    }
+  };
+
+  // LDS addresses of this lane's operands in the first buffer.  The permutations touch bits that are clear in a row's
+  // address, so an operand further on is an exclusive or away, or a sum.
+  const int k_swz = (col / kPeriod) & (G - 1), i16 = lane & 15, v_row = 4 * h + (i16 >> 2);
+  const uint32_t k_at = lds_addr(&s_k[0][0]) + col * kRowBytes + (h ^ k_swz) * 16;
+  const uint32_t v_at = lds_addr(&s_v[0][0]) + v_row * kRowBytes + ((v_row >> kVShift) & kVMask) * 64 +
+                        ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
+  typedef const __attribute__((address_space(3))) v4u* lds_v4u;
+  typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+  const auto k_operand = [&](uint32_t at, int kb, int s) {
+    constexpr int kLow = G / 2;  // steps within which the permutation stays
+    return *reinterpret_cast<lds_v4u>((at ^ (s % kLow * 32)) + (s / kLow * kLow * 32 + kb * 32 * kRowBytes));
+  };
+  const auto v_operand = [&](uint32_t at, int kk, int b) {
+    const uint32_t off = (at ^ ((b & kVMask) * 64)) + ((b & ~kVMask) * 64 + kk * 16 * kRowBytes);
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4>(off));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4>(off + 8 * kRowBytes));
+    const uint2 u = __builtin_bit_cast(uint2, x), w = __builtin_bit_cast(uint2, y);
+    return op4(u.x, u.y, w.x, w.y);
+  };
+  // the key of register i of block kb, counted within a tile from 4 h on
+  const auto key_of = [](int kb, int i) { return kb * 32 + 8 * (i >> 2) + (i & 3); };
+
+  v16f o[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) o[b] = v16f{};
+  float top = -INFINITY, base = kLift, sum = 0.0f;
+
+  if (tile0 < tile1) copy(tile0, 0);
+  for (int t = tile0; t < tile1; ++t) {
+    const int buf = (t - tile0) & 1, key0 = t * BN;
+    wait_vmcnt<0>();
+    __syncthreads();  // every wave's copies of this tile are there, and the other buffer has been read
+    if (t + 1 < tile1) copy(t + 1, buf ^ 1);
+    if (!active || key0 > wave_at1 || key0 + BN - 1 < wave_lo0) continue;
+
+    const uint32_t k_here = k_at + buf * kTile, v_here = v_at + buf * kTile;
+    v16f s[kKeys];
+#pragma unroll
+    for (int kb = 0; kb < kKeys; ++kb) s[kb] = v16f{};
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int kb = 0; kb < kKeys; ++kb) s[kb] = mfma32<BF16>(k_operand(k_here, kb, st), q[st], s[kb]);
+    const bool whole = key0 + BN - 1 <= wave_at0 && key0 >= wave_lo1;
+    const int at_here = at - key0 - 4 * h, lo_here = lo - key0 - 4 * h;
+    if (!whole) {
+#pragma unroll
+      for (int kb = 0; kb < kKeys; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kb][i] = key_of(kb, i) <= at_here && key_of(kb, i) >= lo_here ? s[kb][i] : -INFINITY;
+    }
+    float most = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < kKeys; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) most = fmaxf(most, s[kb][i]);
+    most = halves_max(most);
+    if (__builtin_amdgcn_ballot_w64(most > top + slack)) {
+      most = fmaxf(most, top);
+      const float keep = __builtin_amdgcn_exp2f((top - (most == -INFINITY ? 0.0f : most)) * mul);
+      sum *= keep;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
+      top = most;
+      base = kLift - (most == -INFINITY ? 0.0f : most) * mul;
+    }
+    v4u p[BN / 16];
+#pragma unroll
+    for (int kb = 0; kb < kKeys; ++kb) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], mul, base));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + 1], mul, base));
+        sum += e0;
+        sum += e1;
+        w[i / 2] = pack2<BF16>(e0, e1);
+      }
+      p[2 * kb] = op4(w[0], w[1], w[2], w[3]);
+      p[2 * kb + 1] = op4(w[4], w[5], w[6], w[7]);
+    }
+
+    // Where keys of the tile are not seen, a term of 0 times a value that is
+    // not finite would be NaN.  Products with zeros tell whether there are any.
+    bool odd = false;
+    if (!whole) {
+      v16f z = {};
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) z = mfma32<BF16>(v_operand(v_here, kk, b), op4(0u, 0u, 0u, 0u), z);
+      float any = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) any += z[i];
+      odd = __builtin_amdgcn_ballot_w64(any != any) != 0;
+    }
+    if (!odd) {
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) o[b] = mfma32<BF16>(v_operand(v_here, kk, b), p[kk], o[b]);
+    } else {
+      // The finite values as above; then, in loops that are not unrolled, how
+      // many of the others each query sees: +inf counts 1, -inf 128, NaN 16384
+      // (at most 64 of each).
+      constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u, kOne = BF16 ? 0x3f80u : 0x3c00u;
+      const auto bad = [](uint32_t x) { return (x & kInf) == kInf; };
+      const auto clean = [&](uint32_t x) { return x & ((bad(x) ? 0u : 0xffffu) | (bad(x >> 16) ? 0u : 0xffff0000u)); };
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          const v4u v = v_operand(v_here, kk, b);
+          o[b] = mfma32<BF16>(op4(clean(v.x), clean(v.y), clean(v.z), clean(v.w)), p[kk], o[b]);
+        }
+      int at_odd = at_here, lo_odd = lo_here;
+      uint32_t v_odd = v_here;
+      __asm__ volatile("" : "+v"(at_odd), "+v"(lo_odd), "+v"(v_odd));  // nothing of this is worked out before
+#pragma unroll 1
+      for (int b = 0; b < kBlocks; ++b) {
+        v16f found = {};
+#pragma unroll 1
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          const v4u v = v_operand(v_odd, kk, b);
+          const auto kind = [&](uint32_t x) {
+            x &= 0xffffu;
+            return !bad(x) ? 0u : x == kInf ? kOne : x == (kInf | 0x8000u) ? (BF16 ? 0x4300u : 0x5800u) : BF16 ? 0x4680u : 0x7400u;
+          };
+          const auto see = [&](int i) {
+            const int j = kk * 16 + 8 * (i >> 2) + (i & 3);
+            return j <= at_odd && j >= lo_odd ? kOne : 0u;
+          };
+          found = mfma32<BF16>(op4(kind(v.x) | kind(v.x >> 16) << 16, kind(v.y) | kind(v.y >> 16) << 16,
+                                          kind(v.z) | kind(v.z >> 16) << 16, kind(v.w) | kind(v.w >> 16) << 16),
+                               op4(see(0) | see(1) << 16, see(2) | see(3) << 16, see(4) | see(5) << 16,
+                                          see(6) | see(7) << 16),
+                               found);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = static_cast<int>(found[i]);
+          const bool pos = (c & 127) != 0, neg = (c >> 7 & 127) != 0, nan = c >= 16384 || (pos && neg);
+          found[i] = nan ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+          if (u == b) o[u] += found;
+      }
+    }
+  }
+  wait_vmcnt<0>();
+
+  if (!active) return;
+  sum = halves_sum(sum);
+  const bool mine = row0 + col < rows;
+  if (a.splits > 1) {
+    const int64_t slot = ((static_cast<int64_t>(n) * a.Hk + kh) * a.splits + split) * kRows + wave * 32 + col;
+    float* part = a.part + slot * D;
+    if (mine) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<v4f*>(part + b * 32 + 2 * i + 4 * h) = v4f{o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
+      if (h == 0)
+        reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.tiles) * a.Hk * a.splits * kRows * D)[slot] =
+            make_float2(top * mul, sum);
+    }
+  } else if (mine) {
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t out = (static_cast<int64_t>(pl.q0 + tok) * a.Hq + head) * D;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        store4(a.y_type, a.y, (out + b * 32 + 2 * i + 4 * h) / 4,
+               make_float4(o[b][i] * f, o[b][i + 1] * f, o[b][i + 2] * f, o[b][i + 3] * f));
+  }
+}
+
+// Joins the splits of a tile's rows, a wave per row.
+__global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int D) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int part = blockIdx.x % (kRows / 4), kh = blockIdx.x / (kRows / 4) % a.Hk, n = blockIdx.x / (kRows / 4) / a.Hk;
+  const Place pl = find_place(a, n, lane);
+  const int in_tile = part * 4 + wave, row = pl.tile * kRows + in_tile;
+  if (!pl.found || row >= pl.nq * a.group) return;
+  const int64_t slot = (static_cast<int64_t>(n) * a.Hk + kh) * a.splits * kRows + in_tile;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.tiles) * a.Hk * a.splits * kRows * D);
+  const v4f y = join_parts(a.part + slot * D + min(lane * 4, D - 4), kRows * D, ml + slot, kRows, a.splits, lane);
+  const int64_t out = (static_cast<int64_t>(pl.q0 + row / a.group) * a.Hq + kh * a.group + row % a.group) * D;
+  if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
+}
+
+// The most tiles that sequences of Tq tokens in all may have, and how many ways
+// their keys are split: so many that about two workgroups per CU come to be,
+// none below 256 keys of an average sequence.
+struct PromptPlan {
+  int64_t tiles, splits;
+};
+static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk) {
+  PromptPlan p;
+  const int64_t rows = Tq * (Hq / Hk);
+  p.tiles = std::min(rows, (rows + kRows - 1) / kRows + B);
+  const int64_t groups = std::max<int64_t>(1, p.tiles * Hk), keys = B > 0 ? Tk / B : 0;
+  p.splits = std::max<int64_t>(1, std::min<int64_t>({512 / groups, keys / 256, 64}));
+  return p;
+}
+
+static bool prompt_shape(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
+  constexpr int64_t kMost = int64_t{1} << 30;
+  return B >= 0 && Tq >= 0 && Tk >= 0 && Tq < kMost && Tk < kMost && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
+         attn_head_dim(D) && Tq < kMost / Hq && B < kMost / Hq;
+}
+
+template <int D, int BN>
+static void launch_prompt(const PromptArgs& a, bool bf16, dim3 g, hipStream_t st) {
+  if (bf16) hipLaunchKernelGGL((attn_prompt_kernel<D, BN, true>), g, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((attn_prompt_kernel<D, BN, false>), g, dim3(256), 0, st, a);
 }
 
 }  // namespace qmm
 
 using namespace qmm;
 
+extern "C" size_t attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
+  if (!prompt_shape(B, Tq, Tk, Hq, Hk, D)) return 0;
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk);
+  return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles * Hk * p.splits * kRows * (D + 2) * 4);
+}
+
 extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                            int64_t v_stride, int type, const int32_t* cu_q, const int32_t* cu_k, int64_t B, float scale,
                            int causal, int64_t window, void* y, int y_type, int64_t Tq, int64_t Tk, int64_t Hq,
-                           int64_t Hk, int64_t D, void* stream) {
+                           int64_t Hk, int64_t D, void* ws, size_t ws_bytes, void* stream) {
   if ((type != QMM_F16 && type != QMM_BF16) || !known_type(y_type) || (window > 0 && !causal)) return QMM_ERR_UNSUPPORTED;
-  if (B < 0 || Tq < 0 || Tk < 0 || Tq >= (int64_t{1} << 30) || Tk >= (int64_t{1} << 30)) return QMM_ERR_SHAPE;
-  if (Hk < 1 || Hq < Hk || Hq > 1024 || Hq % Hk != 0 || !prompt_head_dim(D)) return QMM_ERR_SHAPE;
-  if (B > 0x7fffffff || (Tq / 64 + B) * Hq > 0x7fffffff) return QMM_ERR_SHAPE;
+  if (!prompt_shape(B, Tq, Tk, Hq, Hk, D)) return QMM_ERR_SHAPE;
   if (!strided_rows(q_stride, Hq, D) || !strided_rows(k_stride, Hk, D) || !strided_rows(v_stride, Hk, D))
     return QMM_ERR_SHAPE;
   if (!isfinite(scale) || window < 0 || window > 0x7fffffff) return QMM_ERR_SHAPE;
   if (B == 0 || Tq == 0) return QMM_OK;
-  if (!q || !cu_q || !cu_k || !y || (Tk > 0 && (!k || !v))) return QMM_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cu_q) || !aligned16(cu_k) || !aligned16(y))
+  const size_t need = attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D);
+  if (!q || !cu_q || !cu_k || !y || (Tk > 0 && (!k || !v)) || (need > 0 && !ws)) return QMM_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cu_q) || !aligned16(cu_k) || !aligned16(y) ||
+      !aligned16(ws))
     return QMM_ERR_ALIGN;
-  const PromptArgs a{q, k, v, cu_q, cu_k, y, q_stride, k_stride, v_stride, window, Tq, Tk, scale, static_cast<int>(B),
-                     static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(D), type, y_type, causal != 0};
-  hipLaunchKernelGGL(attn_prompt_kernel, dim3(static_cast<unsigned>(Tq * Hq)), dim3(64), 0, to_stream(stream), a);
+  if (ws_bytes < need) return QMM_ERR_WORKSPACE;
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk);
+  const int64_t grid = p.tiles * Hk * p.splits;
+  if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
+  const PromptArgs a{q, k, v, cu_q, cu_k, y, static_cast<float*>(ws), q_stride, k_stride, v_stride, scale,
+                     static_cast<int>(window), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(B),
+                     static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk), static_cast<int>(p.splits),
+                     static_cast<int>(p.tiles), y_type, causal != 0};
+  const dim3 g(static_cast<unsigned>(grid));
+  hipStream_t st = to_stream(stream);
+  switch (D) {
+    case 64: launch_prompt<64, 64>(a, type == QMM_BF16, g, st); break;
+    case 96: launch_prompt<96, 64>(a, type == QMM_BF16, g, st); break;
+    case 128: launch_prompt<128, 64>(a, type == QMM_BF16, g, st); break;
+    case 192: launch_prompt<192, 32>(a, type == QMM_BF16, g, st); break;
+    default: launch_prompt<256, 32>(a, type == QMM_BF16, g, st); break;
+  }
+  if (p.splits > 1)
+    hipLaunchKernelGGL(attn_prompt_join_kernel, dim3(static_cast<unsigned>(p.tiles * Hk * (kRows / 4))), dim3(256), 0, st,
+                       a, static_cast<int>(D));
   return launch_status();
 }

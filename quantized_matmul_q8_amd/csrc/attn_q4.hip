@@ -17,6 +17,7 @@
 // A sequence is cut into chunks of tokens, one per workgroup, so that a few
 // long sequences fill the chip; partial results go to the workspace and a
 // second kernel joins them.
+#include "attn.hpp"
 #include "kv_q4.hpp"
 
 #include <algorithm>
@@ -26,7 +27,6 @@ namespace qmm {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 32;    // tokens of a step: two cells
 constexpr int kWaves = 4;    // of a workgroup
@@ -81,23 +81,6 @@ __device__ __forceinline__ void codes(uint32_t w, const Magic& k, h2 (&x)[4]) {
 
 __device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
   return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// Over the four rows of 16 lanes, in all of them.
-template <typename F>
-__device__ __forceinline__ float rows_join(float v, F f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t w = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, static_cast<uint32_t>(a[0])),
-                                                    __builtin_bit_cast(float, static_cast<uint32_t>(a[1]))));
-  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  return f(__builtin_bit_cast(float, static_cast<uint32_t>(b[0])), __builtin_bit_cast(float, static_cast<uint32_t>(b[1])));
-}
-__device__ __forceinline__ float rows_max(float v) {
-  return rows_join(v, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ float rows_sum(float v) {
-  return rows_join(v, [](float a, float b) { return a + b; });
 }
 
 template <int K>
@@ -430,9 +413,7 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
   }
 }
 
-// Joins the chunks of one row; sequences of one chunk have been written.  A
-// wave per row: the chunks' maxima and sums by its lanes, 64 at a time, then
-// the chunks in order, four loads in flight.
+// Joins the chunks of one row, a wave each; sequences of one chunk have been written.
 __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   const int64_t out = blockIdx.x;
   const int seq = static_cast<int>(out / (static_cast<int64_t>(a.n) * a.Hq));
@@ -440,33 +421,9 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   const int first = a.window > 0 ? max(0, len - a.n - a.window + 1) / kStep * kStep : 0;
   if (len - first <= a.chunk) return;
   const int count = (len - first + a.chunk - 1) / a.chunk, lane = threadIdx.x;
-  const float* part = a.part + out * a.chunks * D;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D) +
-                     out * a.chunks;
-  const int d = min(lane * 4, D - 4);
-  float m = -INFINITY, total = 0.0f;
-  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = 0; k0 < count; k0 += 64) {
-    const int here = min(64, count - k0);
-    const float2 own = lane < here ? ml[k0 + lane] : make_float2(-INFINITY, 0.0f);
-    float most = fmaxf(m, rows_max(own.x));
-#pragma unroll
-    for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
-    const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
-    const float f = __builtin_amdgcn_exp2f(own.x - base);
-    total = total * keep + wave_sum(own.y * f);
-    y *= keep;
-    m = most;
-    for (int k = 0; k < here; k += 4) {
-      v4f x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + static_cast<int64_t>(k0 + min(k + i, here - 1)) * D + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y += x[i] * (k + i < here ? __shfl(f, k + i) : 0.0f);
-    }
-  }
-  y *= total == 0.0f ? 0.0f : 1.0f / total;
-  if (lane * 4 < D) store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D);
+  const v4f y = join_parts(a.part + out * a.chunks * D + min(lane * 4, D - 4), D, ml + out * a.chunks, 1, count, lane);
+  if (lane * 4 < D) store4(a.y_type, a.y, (out * D + lane * 4) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
 
 // How a call is cut: row tiles per workgroup and tokens per chunk, from the sizes that the host knows.

@@ -1,13 +1,11 @@
 // The paged 4-bit cache of keys and values (its layout: include/qmm.h).
 #pragma once
 
-#include "typed.hpp"
+#include "attn.hpp"
 
 namespace qmm {
 
 constexpr int kCellTokens = 16;
-
-inline bool attn_head_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 inline bool kv_q4_shape(int64_t pages, int64_t page, int64_t Hk, int64_t D) {
   return Hk >= 1 && Hk <= 1024 && attn_head_dim(D) && page >= 16 && page <= (int64_t{1} << 20) && page % 16 == 0 &&

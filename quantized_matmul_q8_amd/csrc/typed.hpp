@@ -6,9 +6,9 @@
 
 namespace qmm {
 
-// Rows of heads: a stride of at least all of them, and 16-byte steps for any type.
+// Rows of heads: a stride of at least all of them, 16-byte steps for any type, and 64 rows' bytes within 32 bits.
 inline bool strided_rows(int64_t stride, int64_t heads, int64_t D) {
-  return stride >= heads * D && stride % 8 == 0 && stride < (int64_t{1} << 31);
+  return stride >= heads * D && stride % 8 == 0 && stride < (int64_t{1} << 24);
 }
 
 inline bool known_type(int t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_BF16; }

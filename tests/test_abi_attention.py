@@ -106,7 +106,7 @@ def test_cached_attention_workspace():
 
 def prompt(**kw):
     a = dict(q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, t=BF16, cq=FAKE, ck=FAKE, B=2, sc=0.1, ca=1, win=0, y=FAKE,
-             yt=F16, Tq=10, Tk=20, Hq=8, Hk=4, D=64) | kw
+             yt=F16, Tq=10, Tk=20, Hq=8, Hk=4, D=64, ws=FAKE, wsb=1 << 40) | kw
     return L.attn_prompt(*a.values(), NUL)
 
 
@@ -119,7 +119,19 @@ def test_prompt_errors():
     for p in ("q", "k", "v", "cq", "ck", "y"):
         assert prompt(**{p: NUL}) == NULL, p
         assert prompt(**{p: MISAL}) == ALIGN, p
+    assert prompt(ws=MISAL) == ALIGN
     assert prompt(B=0, q=NUL) == OK and prompt(Tq=0, y=NUL) == OK
+
+
+def test_prompt_workspace():
+    f = L.attn_prompt_workspace_bytes
+    for sizes in ((-1, 1, 1, 8, 4, 64), (1, -1, 1, 8, 4, 64), (1, 1, -1, 8, 4, 64), (1, 1, 1, 6, 4, 64), (1, 1, 1, 8, 4, 80),
+                  (1, 1 << 30, 1, 8, 4, 64)):
+        assert f(*sizes) == 0
+    need = f(1, 16, 1 << 16, 8, 4, 64)
+    if need:
+        assert prompt(B=1, Tq=16, Tk=1 << 16, wsb=need - 1) == WS
+        assert prompt(B=1, Tq=16, Tk=1 << 16, ws=NUL, wsb=0) == NULL
 
 
 def test_binding_refuses_what_does_not_fit():
