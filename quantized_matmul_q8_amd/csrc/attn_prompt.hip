@@ -62,6 +62,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// c + both of a pair, in fp32.  Terms are summed as the product with the values takes them, rounded.
+template <bool BF16>
+__device__ __forceinline__ float add2(uint32_t pair, float c) {
+  if constexpr (BF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, pair), b2{static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)}, c, false);
+  } else {
+    typedef _Float16 f2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f2, pair), f2{static_cast<_Float16>(1.0f), static_cast<_Float16>(1.0f)}, c, false);
+  }
+}
+
 // 16 bytes per lane from base + off into LDS at lds + 16 * lane; see dma16.
 __device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds) {
   uint32_t saved;
@@ -271,9 +283,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
       for (int i = 0; i < 16; i += 2) {
         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], mul, base));
         const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + 1], mul, base));
-        sum += e0;
-        sum += e1;
         w[i / 2] = pack2<BF16>(e0, e1);
+        sum = add2<BF16>(w[i / 2], sum);
       }
       p[2 * kb] = op4(w[0], w[1], w[2], w[3]);
       p[2 * kb + 1] = op4(w[4], w[5], w[6], w[7]);
