@@ -122,7 +122,7 @@ __device__ __forceinline__ Place find_place(const PromptArgs& a, int n, int lane
 }
 
 template <int D, int BN, bool BF16>
-__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
   constexpr int C = D / 8, kRowBytes = 2 * D, kTile = BN * kRowBytes;  // chunks of a row
   constexpr int G = gcd16(C), kPeriod = 16 / G;                        // K: chunk ^ (row / kPeriod) % G
   constexpr int kVShift = C % 16 == 0 ? 0 : 1, kVMask = C % 16 == 0 ? 3 : C % 8 == 0 ? 1 : 0;  // V: chunk ^ 4 * ...
@@ -402,18 +402,21 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int
   if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
 }
 
+// Workgroups that the chip holds at once: two per CU, one where D > 128 takes a wave's registers past half of them.
+constexpr int prompt_slots(int64_t D) { return D <= 128 ? 512 : 256; }
+
 // The most tiles that sequences of Tq tokens in all may have, and how many ways
-// their keys are split: so many that about two workgroups per CU come to be,
-// none below 256 keys of an average sequence.
+// their keys are split: as many as fill the chip once with the tiles of B
+// sequences of about one size, none below 256 keys of an average sequence.
 struct PromptPlan {
   int64_t tiles, splits;
 };
-static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk) {
+static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
   PromptPlan p;
-  const int64_t rows = Tq * (Hq / Hk);
-  p.tiles = std::min(rows, (rows + kRows - 1) / kRows + B);
-  const int64_t groups = std::max<int64_t>(1, p.tiles * Hk), keys = B > 0 ? Tk / B : 0;
-  p.splits = std::max<int64_t>(1, std::min<int64_t>({512 / groups, keys / 256, 64}));
+  const int64_t rows = Tq * (Hq / Hk), whole = (rows + kRows - 1) / kRows;
+  p.tiles = std::min(rows, whole + B);
+  const int64_t groups = std::max<int64_t>(1, whole + (B - 1) / 2) * Hk, keys = B > 0 ? Tk / B : 0;
+  p.splits = std::max<int64_t>(1, std::min<int64_t>({prompt_slots(D) / groups, keys / 256, 64}));
   return p;
 }
 
@@ -435,7 +438,7 @@ using namespace qmm;
 
 extern "C" size_t attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
   if (!prompt_shape(B, Tq, Tk, Hq, Hk, D)) return 0;
-  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk);
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);
   return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles * Hk * p.splits * kRows * (D + 2) * 4);
 }
 
@@ -455,7 +458,7 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
       !aligned16(ws))
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
-  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk);
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);
   const int64_t grid = p.tiles * Hk * p.splits;
   if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const PromptArgs a{q, k, v, cu_q, cu_k, y, static_cast<float*>(ws), q_stride, k_stride, v_stride, scale,
@@ -468,8 +471,8 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
     case 64: launch_prompt<64, 64>(a, type == QMM_BF16, g, st); break;
     case 96: launch_prompt<96, 64>(a, type == QMM_BF16, g, st); break;
     case 128: launch_prompt<128, 64>(a, type == QMM_BF16, g, st); break;
-    case 192: launch_prompt<192, 32>(a, type == QMM_BF16, g, st); break;
-    default: launch_prompt<256, 32>(a, type == QMM_BF16, g, st); break;
+    case 192: launch_prompt<192, 64>(a, type == QMM_BF16, g, st); break;
+    default: launch_prompt<256, 64>(a, type == QMM_BF16, g, st); break;
   }
   if (p.splits > 1)
     hipLaunchKernelGGL(attn_prompt_join_kernel, dim3(static_cast<unsigned>(p.tiles * Hk * (kRows / 4))), dim3(256), 0, st,
