@@ -130,7 +130,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   constexpr int kSteps = D / 16, kBlocks = D / 32, kKeys = BN / 32;
   constexpr float kLift = BF16 ? 0.0f : 7.0f;  // terms of up to 2^(8 + kLift): f16 holds them, and those down to 2^-31
   constexpr float kSlack = 8.0f;               // a maximum is followed when it is passed by 2^8
-  __shared__ __attribute__((aligned(1024))) uint8_t s_k[2][kTile], s_v[2][kTile];
+  // Where registers allow it, the products of a tile's keys run beside the terms of the tile before: a third buffer of keys.
+  constexpr bool kAhead = D <= 128;
+  constexpr int kKeyBufs = kAhead ? 3 : 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_k[kKeyBufs][kTile], s_v[2][kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
 
@@ -187,26 +190,42 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   const uint8_t* k_base = static_cast<const uint8_t*>(a.k) + (static_cast<int64_t>(pl.k0) * a.k_stride + kh * D) * 2;
   const uint8_t* v_base = static_cast<const uint8_t*>(a.v) + (static_cast<int64_t>(pl.k0) * a.v_stride + kh * D) * 2;
   const uint32_t k_lds = lds_addr(&s_k[0][0]) + wave * (kCopies * 1024), v_lds = lds_addr(&s_v[0][0]) + wave * (kCopies * 1024);
-  const auto copy = [&](int t, int buf) {
-    const uint8_t* kb = k_base + static_cast<int64_t>(t) * BN * k_bytes;
-    const uint8_t* vb = v_base + static_cast<int64_t>(t) * BN * v_bytes;
+  const auto copy = [&](int t, const uint8_t* from, uint32_t bytes, const uint32_t (&off)[kCopies], uint32_t lds, bool v) {
+    const uint8_t* at = from + static_cast<int64_t>(t) * BN * bytes;
     const int left = pl.nk - 1 - t * BN;
-    const uint32_t k_to = k_lds + buf * kTile, v_to = v_lds + buf * kTile;
     if (left >= BN - 1) {
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        dma16_at(kb, k_off[i], k_to + i * 1024);
-        dma16_at(vb, v_off[i], v_to + i * 1024);
-      }
+      for (int i = 0; i < kCopies; ++i) dma16_at(at, off[i], lds + i * 1024);
     } else {
 #pragma unroll 1
       for (int i = 0; i < kCopies; ++i) {
         uint32_t ko, vo;
         offsets(i, left, ko, vo);
-        dma16_at(kb, ko, k_to + i * 1024);
-        dma16_at(vb, vo, v_to + i * 1024);
+        dma16_at(at, v ? vo : ko, lds + i * 1024);
       }
     }
+  };
+  // Byte offsets of the buffers of tiles t and t + 1 of keys and of the one to fill, and of tile t of values.
+  uint32_t key_buf = 0, next_buf = kTile, fill_buf = kKeyBufs == 3 ? 2 * kTile : 0, value_buf = 0;
+  if (tile0 < tile1) {
+    copy(tile0, k_base, k_bytes, k_off, k_lds, false);
+    copy(tile0, v_base, v_bytes, v_off, v_lds, true);
+    if (kAhead && tile0 + 1 < tile1) copy(tile0 + 1, k_base, k_bytes, k_off, k_lds + kTile, false);
+  }
+  // Before tile t: its copies (and the next keys') are there for every wave, and what the other buffers held has been read.
+  const auto enter = [&](int t) {
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (kAhead ? t + 2 < tile1 : t + 1 < tile1)
+      copy(t + (kAhead ? 2 : 1), k_base, k_bytes, k_off, k_lds + (kAhead ? fill_buf : next_buf), false);
+    if (t + 1 < tile1) copy(t + 1, v_base, v_bytes, v_off, v_lds + (value_buf ^ kTile), true);
+  };
+  const auto leave = [&]() {
+    const uint32_t k = key_buf;
+    key_buf = next_buf;
+    next_buf = kAhead ? fill_buf : k;
+    fill_buf = k;
+    value_buf ^= kTile;
   };
 
   // LDS addresses of this lane's operands in the first buffer.  The permutations touch bits that are clear in a row's
@@ -236,46 +255,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   for (int b = 0; b < kBlocks; ++b) o[b] = v16f{};
   float top = -INFINITY, base = kLift, sum = 0.0f;
 
-  if (tile0 < tile1) copy(tile0, 0);
-  for (int t = tile0; t < tile1; ++t) {
-    const int buf = (t - tile0) & 1, key0 = t * BN;
-    wait_vmcnt<0>();
-    __syncthreads();  // every wave's copies of this tile are there, and the other buffer has been read
-    if (t + 1 < tile1) copy(t + 1, buf ^ 1);
-    if (!active || key0 > wave_at1 || key0 + BN - 1 < wave_lo0) continue;
-
-    const uint32_t k_here = k_at + buf * kTile, v_here = v_at + buf * kTile;
-    v16f s[kKeys];
-#pragma unroll
-    for (int kb = 0; kb < kKeys; ++kb) s[kb] = v16f{};
+  const auto products = [&](v16f (&s)[kKeys], uint32_t buf) {
+    const uint32_t here = k_at + buf;
 #pragma unroll
     for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-      for (int kb = 0; kb < kKeys; ++kb) s[kb] = mfma32<BF16>(k_operand(k_here, kb, st), q[st], s[kb]);
-    const bool whole = key0 + BN - 1 <= wave_at0 && key0 >= wave_lo1;
-    const int at_here = at - key0 - 4 * h, lo_here = lo - key0 - 4 * h;
-    if (!whole) {
-#pragma unroll
       for (int kb = 0; kb < kKeys; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = key_of(kb, i) <= at_here && key_of(kb, i) >= lo_here ? s[kb][i] : -INFINITY;
-    }
-    float most = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < kKeys; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) most = fmaxf(most, s[kb][i]);
-    most = halves_max(most);
-    if (__builtin_amdgcn_ballot_w64(most > top + slack)) {
-      most = fmaxf(most, top);
-      const float keep = __builtin_amdgcn_exp2f((top - (most == -INFINITY ? 0.0f : most)) * mul);
-      sum *= keep;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
-      top = most;
-      base = kLift - (most == -INFINITY ? 0.0f : most) * mul;
-    }
-    v4u p[BN / 16];
+        s[kb] = mfma32<BF16>(k_operand(here, kb, st), q[st], st == 0 ? v16f{} : s[kb]);
+  };
+  const auto terms = [&](const v16f (&s)[kKeys], v4u (&p)[BN / 16]) {
 #pragma unroll
     for (int kb = 0; kb < kKeys; ++kb) {
       uint32_t w[8];
@@ -289,26 +277,27 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
       p[2 * kb] = op4(w[0], w[1], w[2], w[3]);
       p[2 * kb + 1] = op4(w[4], w[5], w[6], w[7]);
     }
-
-    // Where keys of the tile are not seen, a term of 0 times a value that is
-    // not finite would be NaN.  Products with zeros tell whether there are any.
-    bool odd = false;
-    if (!whole) {
-      v16f z = {};
+  };
+  const auto values = [&](uint32_t v_here, const v4u (&p)[BN / 16]) {
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
+    for (int kk = 0; kk < BN / 16; ++kk)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) z = mfma32<BF16>(v_operand(v_here, kk, b), op4(0u, 0u, 0u, 0u), z);
-      float any = 0.0f;
+      for (int b = 0; b < kBlocks; ++b) o[b] = mfma32<BF16>(v_operand(v_here, kk, b), p[kk], o[b]);
+  };
+  // Tiles of which some keys are not seen by some rows.  There a term of 0
+  // times a value that is not finite would be NaN; products with zeros tell
+  // whether there are any.
+  const auto part_values = [&](uint32_t v_here, const v4u (&p)[BN / 16], int at_here, int lo_here) {
+    v16f z = {};
 #pragma unroll
-      for (int i = 0; i < 16; ++i) any += z[i];
-      odd = __builtin_amdgcn_ballot_w64(any != any) != 0;
-    }
-    if (!odd) {
+    for (int kk = 0; kk < BN / 16; ++kk)
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
+      for (int b = 0; b < kBlocks; ++b) z = mfma32<BF16>(v_operand(v_here, kk, b), op4(0u, 0u, 0u, 0u), z);
+    float any = 0.0f;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[b] = mfma32<BF16>(v_operand(v_here, kk, b), p[kk], o[b]);
+    for (int i = 0; i < 16; ++i) any += z[i];
+    if (__builtin_amdgcn_ballot_w64(any != any) == 0) {
+      values(v_here, p);
     } else {
       // The finite values as above; then, in loops that are not unrolled, how
       // many of the others each query sees: +inf counts 1, -inf 128, NaN 16384
@@ -357,7 +346,133 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
           if (u == b) o[u] += found;
       }
     }
+  };
+
+  // The maximum of new products; where it is passed by too much, all so far is brought to it.
+  const auto follow = [&](const v16f (&s)[kKeys]) {
+    float most = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < kKeys; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) most = fmaxf(most, s[kb][i]);
+    most = halves_max(most);
+    if (__builtin_amdgcn_ballot_w64(most > top + slack)) {
+      most = fmaxf(most, top);
+      const float keep = __builtin_amdgcn_exp2f((top - (most == -INFINITY ? 0.0f : most)) * mul);
+      sum *= keep;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
+      top = most;
+      base = kLift - (most == -INFINITY ? 0.0f : most) * mul;
+    }
+  };
+
+  // The tiles of which this wave's rows see something, and those that all of them see whole.
+  const int wave0 = max(tile0, wave_lo0 / BN), wave1 = active ? min(tile1, wave_at1 < 0 ? 0 : wave_at1 / BN + 1) : 0;
+  const int whole0 = max(wave0, (wave_lo1 + BN - 1) / BN), whole1 = min(wave1, wave_at0 < 0 ? 0 : (wave_at0 + 1) / BN);
+  // one tile by itself
+  const auto alone = [&](int t) {
+    enter(t);
+    if (t >= wave0 && t < wave1) {
+      const bool whole = t >= whole0 && t < whole1;
+      const int at_here = at - t * BN - 4 * h, lo_here = lo - t * BN - 4 * h;
+      v16f s[kKeys];
+      v4u p[BN / 16];
+      products(s, key_buf);
+      if (!whole) {
+#pragma unroll
+        for (int kb = 0; kb < kKeys; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[kb][i] = key_of(kb, i) <= at_here && key_of(kb, i) >= lo_here ? s[kb][i] : -INFINITY;
+      }
+      follow(s);
+      terms(s, p);
+      if (whole) values(v_at + value_buf, p);
+      else part_values(v_at + value_buf, p, at_here, lo_here);
+    }
+    leave();
+  };
+
+  int t = tile0;
+  if constexpr (kAhead) {
+    const int run0 = whole1 - whole0 >= 2 ? whole0 : tile1, run1 = whole1 - whole0 >= 2 ? whole1 : tile1;
+    for (; t < run0; ++t) alone(t);
+    if (t < run1) {
+      v16f x[kKeys], y[kKeys];
+      v4u p[BN / 16];
+      // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
+      // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
+      // first ones its share of the terms, two of them exponentiated and the two before packed.
+      const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
+        constexpr int kFirst = kSteps * kKeys, kSecond = BN / 16 * kBlocks, kPairs = kKeys * 8;
+        const uint32_t k_here = k_at + next_buf, v_here = v_at + value_buf;
+        v4u f[4];
+        const auto operand = [&](int m) {
+          return m < kFirst ? k_operand(k_here, m % kKeys, m / kKeys)
+                            : v_operand(v_here, (m - kFirst) / kBlocks, (m - kFirst) % kBlocks);
+        };
+        float e[2][2];
+        const auto raise = [&](int n) {
+          const v16f& c = cur[n / 8];
+          e[n & 1][0] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2], mul, base));
+          e[n & 1][1] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2 + 1], mul, base));
+        };
+        const auto pack = [&](int n) {
+          const uint32_t w = pack2<BF16>(e[n & 1][0], e[n & 1][1]);
+          p[n / 4][n % 4] = w;
+          sum = add2<BF16>(w, sum);
+        };
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) f[m] = operand(m);
+#pragma unroll
+        for (int m = 0; m < kFirst; ++m) {
+          __builtin_amdgcn_sched_barrier(0);
+          next[m % kKeys] = mfma32<BF16>(f[m % 4], q[m / kKeys], m < kKeys ? v16f{} : next[m % kKeys]);
+          f[m % 4] = operand(m + 4);
+#pragma unroll
+          for (int n = m * kPairs / kFirst; n < (m + 1) * kPairs / kFirst; ++n) {
+            raise(n);
+            if (n > 0) pack(n - 1);
+          }
+        }
+        pack(kPairs - 1);
+#pragma unroll
+        for (int m = 0; m < kSecond; ++m) {
+          __builtin_amdgcn_sched_barrier(0);
+          o[m % kBlocks] = mfma32<BF16>(f[(kFirst + m) % 4], p[m / kBlocks], o[m % kBlocks]);
+          if (m + 4 < kSecond) f[(kFirst + m) % 4] = operand(kFirst + m + 4);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        follow(next);
+      };
+      enter(t);
+      products(x, key_buf);
+      follow(x);
+      int left = run1 - t - 1;  // steps with a next tile
+      for (; left >= 2; left -= 2) {
+        step(x, y);
+        leave();
+        enter(++t);
+        step(y, x);
+        leave();
+        enter(++t);
+      }
+      if (left) {
+        step(x, y);
+        leave();
+        enter(++t);
+#pragma unroll
+        for (int kb = 0; kb < kKeys; ++kb) x[kb] = y[kb];
+      }
+      terms(x, p);
+      values(v_at + value_buf, p);
+      leave();
+      ++t;
+    }
   }
+  for (; t < tile1; ++t) alone(t);
   wait_vmcnt<0>();
 
   if (!active) return;
