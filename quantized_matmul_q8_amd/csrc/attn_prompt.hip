@@ -74,12 +74,14 @@ __device__ __forceinline__ float add2(uint32_t pair, float c) {
   }
 }
 
-// 16 bytes per lane from base + off into LDS at lds + 16 * lane; see dma16.
-__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds) {
+// 16 bytes per lane from off bytes into a buffer to LDS at lds + 16 * lane; zeros for what lies past the buffer's end.
+// Not tracked by the compiler: see dma16.
+__device__ __forceinline__ void copy16(v4u buffer, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+                   "s_mov_b32 m0, %0"
                    : "=&s"(saved)
-                   : "v"(off), "s"(base), "s"(lds)
+                   : "v"(off), "s"(buffer), "s"(lds)
                    : "memory");
 }
 
@@ -176,49 +178,54 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   const int count = max(0, (all_end + BN - 1) / BN - all_first), per = (count + a.splits - 1) / a.splits;
   const int tile0 = all_first + min(count, split * per), tile1 = all_first + min(count, (split + 1) * per);
 
-  // copies: where each of this lane's chunks stands in a tile of the rows
+  // Copies: where each of this lane's chunks stands in a tile of the rows, and the tile as a buffer that ends with the
+  // sequence's last row, so that rows behind it are zeros.
   const uint32_t k_bytes = static_cast<uint32_t>(a.k_stride) * 2, v_bytes = static_cast<uint32_t>(a.v_stride) * 2;
-  const auto offsets = [&](int i, int left, uint32_t& k_off, uint32_t& v_off) {
-    const int at16 = (wave * kCopies + i) * 64 + lane, r = at16 / C, c = at16 % C;
-    const uint32_t from = static_cast<uint32_t>(min(r, left));  // rows behind the sequence's last repeat it
-    k_off = from * k_bytes + static_cast<uint32_t>((c ^ ((r / kPeriod) & (G - 1))) * 16);
-    v_off = from * v_bytes + static_cast<uint32_t>((c ^ (4 * ((r >> kVShift) & kVMask))) * 16);
-  };
   uint32_t k_off[kCopies], v_off[kCopies];
 #pragma unroll
-  for (int i = 0; i < kCopies; ++i) offsets(i, BN, k_off[i], v_off[i]);
-  const uint8_t* k_base = static_cast<const uint8_t*>(a.k) + (static_cast<int64_t>(pl.k0) * a.k_stride + kh * D) * 2;
-  const uint8_t* v_base = static_cast<const uint8_t*>(a.v) + (static_cast<int64_t>(pl.k0) * a.v_stride + kh * D) * 2;
+  for (int i = 0; i < kCopies; ++i) {
+    const int at16 = (wave * kCopies + i) * 64 + lane, r = at16 / C, c = at16 % C;
+    k_off[i] = r * k_bytes + static_cast<uint32_t>((c ^ ((r / kPeriod) & (G - 1))) * 16);
+    v_off[i] = r * v_bytes + static_cast<uint32_t>((c ^ (4 * ((r >> kVShift) & kVMask))) * 16);
+  }
+  const uint64_t k_base = reinterpret_cast<uint64_t>(a.k) + (static_cast<int64_t>(pl.k0) * a.k_stride + kh * D) * 2;
+  const uint64_t v_base = reinterpret_cast<uint64_t>(a.v) + (static_cast<int64_t>(pl.k0) * a.v_stride + kh * D) * 2;
   const uint32_t k_lds = lds_addr(&s_k[0][0]) + wave * (kCopies * 1024), v_lds = lds_addr(&s_v[0][0]) + wave * (kCopies * 1024);
-  const auto copy = [&](int t, const uint8_t* from, uint32_t bytes, const uint32_t (&off)[kCopies], uint32_t lds, bool v) {
-    const uint8_t* at = from + static_cast<int64_t>(t) * BN * bytes;
-    const int left = pl.nk - 1 - t * BN;
-    if (left >= BN - 1) {
+  const auto tile_of = [&](uint64_t base, uint32_t bytes, int t) {
+    const int64_t first = static_cast<int64_t>(t) * BN, rows_left = min(int64_t{BN}, pl.nk - first);
+    const uint64_t at = base + first * bytes;
+    const uint32_t size = rows_left > 0 ? static_cast<uint32_t>(rows_left - 1) * bytes + kRowBytes : 0u;
+    v4u r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu, size, 0x00020000u};
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) dma16_at(at, off[i], lds + i * 1024);
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < kCopies; ++i) {
-        uint32_t ko, vo;
-        offsets(i, left, ko, vo);
-        dma16_at(at, v ? vo : ko, lds + i * 1024);
-      }
-    }
+    for (int k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_readfirstlane(r[k]);
+    return r;
   };
   // Byte offsets of the buffers of tiles t and t + 1 of keys and of the one to fill, and of tile t of values.
-  uint32_t key_buf = 0, next_buf = kTile, fill_buf = kKeyBufs == 3 ? 2 * kTile : 0, value_buf = 0;
+  uint32_t key_buf = 0, next_buf = kTile, fill_buf = kKeyBufs == 3 ? 2 * kTile : kTile, value_buf = 0;
+  const auto copy_k = [&](int t, uint32_t buf) {
+    const v4u tile = tile_of(k_base, k_bytes, t);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy16(tile, k_off[i], k_lds + buf + i * 1024);
+  };
+  const auto copy_v = [&](int t, uint32_t buf) {
+    const v4u tile = tile_of(v_base, v_bytes, t);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy16(tile, v_off[i], v_lds + buf + i * 1024);
+  };
   if (tile0 < tile1) {
-    copy(tile0, k_base, k_bytes, k_off, k_lds, false);
-    copy(tile0, v_base, v_bytes, v_off, v_lds, true);
-    if (kAhead && tile0 + 1 < tile1) copy(tile0 + 1, k_base, k_bytes, k_off, k_lds + kTile, false);
+    copy_k(tile0, key_buf);
+    copy_v(tile0, value_buf);
+    if (kAhead) copy_k(tile0 + 1, next_buf);
   }
-  // Before tile t: its copies (and the next keys') are there for every wave, and what the other buffers held has been read.
-  const auto enter = [&](int t) {
+  // Before a tile: its copies (and the next keys') are there for every wave, and what the other buffers held has been read,
+  // so that they may be filled.  Behind the last tile they are filled with zeros.
+  const auto enter = [&]() {
     wait_vmcnt<0>();
     __syncthreads();
-    if (kAhead ? t + 2 < tile1 : t + 1 < tile1)
-      copy(t + (kAhead ? 2 : 1), k_base, k_bytes, k_off, k_lds + (kAhead ? fill_buf : next_buf), false);
-    if (t + 1 < tile1) copy(t + 1, v_base, v_bytes, v_off, v_lds + (value_buf ^ kTile), true);
+  };
+  const auto fill = [&](int t) {
+    copy_k(t + (kAhead ? 2 : 1), fill_buf);
+    copy_v(t + 1, value_buf ^ kTile);
   };
   const auto leave = [&]() {
     const uint32_t k = key_buf;
@@ -348,14 +355,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     }
   };
 
-  // The maximum of new products; where it is passed by too much, all so far is brought to it.
-  const auto follow = [&](const v16f (&s)[kKeys]) {
-    float most = s[0][0];
+  // Two products more into a maximum.
+  const auto higher = [](float most, const v16f (&s)[kKeys], int n) {
+    return fmaxf(fmaxf(most, s[n / 8][n % 8 * 2]), s[n / 8][n % 8 * 2 + 1]);
+  };
+  const auto highest = [&](const v16f (&s)[kKeys]) {
+    float most = -INFINITY;
 #pragma unroll
-    for (int kb = 0; kb < kKeys; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) most = fmaxf(most, s[kb][i]);
-    most = halves_max(most);
+    for (int n = 0; n < kKeys * 8; ++n) most = higher(most, s, n);
+    return halves_max(most);
+  };
+  // The maximum of new products: where it passes what all so far goes by too far, that is brought to it.
+  const auto follow = [&](float most) {
     if (__builtin_amdgcn_ballot_w64(most > top + slack)) {
       most = fmaxf(most, top);
       const float keep = __builtin_amdgcn_exp2f((top - (most == -INFINITY ? 0.0f : most)) * mul);
@@ -372,7 +383,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   const int whole0 = max(wave0, (wave_lo1 + BN - 1) / BN), whole1 = min(wave1, wave_at0 < 0 ? 0 : (wave_at0 + 1) / BN);
   // one tile by itself
   const auto alone = [&](int t) {
-    enter(t);
+    enter();
+    fill(t);
     if (t >= wave0 && t < wave1) {
       const bool whole = t >= whole0 && t < whole1;
       const int at_here = at - t * BN - 4 * h, lo_here = lo - t * BN - 4 * h;
@@ -386,7 +398,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
           for (int i = 0; i < 16; ++i)
             s[kb][i] = key_of(kb, i) <= at_here && key_of(kb, i) >= lo_here ? s[kb][i] : -INFINITY;
       }
-      follow(s);
+      follow(highest(s));
       terms(s, p);
       if (whole) values(v_at + value_buf, p);
       else part_values(v_at + value_buf, p, at_here, lo_here);
@@ -403,11 +415,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
       v4u p[BN / 16];
       // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
       // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
-      // first ones its share of the terms, two of them exponentiated and the two before packed.
+      // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
       const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
+        const v4u k_tile = tile_of(k_base, k_bytes, t + 2), v_tile = tile_of(v_base, v_bytes, t + 1);
         constexpr int kFirst = kSteps * kKeys, kSecond = BN / 16 * kBlocks, kPairs = kKeys * 8;
+        constexpr int kAheadBy = 6, kMaxIn = kSecond - 2;
         const uint32_t k_here = k_at + next_buf, v_here = v_at + value_buf;
-        v4u f[4];
+        v4u f[kAheadBy];
+        float most = -INFINITY;
         const auto operand = [&](int m) {
           return m < kFirst ? k_operand(k_here, m % kKeys, m / kKeys)
                             : v_operand(v_here, (m - kFirst) / kBlocks, (m - kFirst) % kBlocks);
@@ -425,12 +440,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
         };
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) f[m] = operand(m);
+        for (int m = 0; m < kAheadBy; ++m) f[m] = operand(m);
 #pragma unroll
         for (int m = 0; m < kFirst; ++m) {
           __builtin_amdgcn_sched_barrier(0);
-          next[m % kKeys] = mfma32<BF16>(f[m % 4], q[m / kKeys], m < kKeys ? v16f{} : next[m % kKeys]);
-          f[m % 4] = operand(m + 4);
+          next[m % kKeys] = mfma32<BF16>(f[m % kAheadBy], q[m / kKeys], m < kKeys ? v16f{} : next[m % kKeys]);
+          f[m % kAheadBy] = operand(m + kAheadBy);
+          static_assert(kFirst >= 4 * kCopies);
+          if (m % 4 == 0 && m / 4 < kCopies) copy16(k_tile, k_off[m / 4], k_lds + fill_buf + m / 4 * 1024);
+          if (m % 4 == 2 && m / 4 < kCopies) copy16(v_tile, v_off[m / 4], v_lds + (value_buf ^ kTile) + m / 4 * 1024);
 #pragma unroll
           for (int n = m * kPairs / kFirst; n < (m + 1) * kPairs / kFirst; ++n) {
             raise(n);
@@ -441,31 +459,35 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
 #pragma unroll
         for (int m = 0; m < kSecond; ++m) {
           __builtin_amdgcn_sched_barrier(0);
-          o[m % kBlocks] = mfma32<BF16>(f[(kFirst + m) % 4], p[m / kBlocks], o[m % kBlocks]);
-          if (m + 4 < kSecond) f[(kFirst + m) % 4] = operand(kFirst + m + 4);
+          o[m % kBlocks] = mfma32<BF16>(f[(kFirst + m) % kAheadBy], p[m / kBlocks], o[m % kBlocks]);
+          if (m + kAheadBy < kSecond) f[(kFirst + m) % kAheadBy] = operand(kFirst + m + kAheadBy);
+#pragma unroll
+          for (int n = m * kPairs / kMaxIn; n < min(kPairs, (m + 1) * kPairs / kMaxIn); ++n) most = higher(most, next, n);
+          if (m == kMaxIn - 1) most = halves_max(most);
         }
         __builtin_amdgcn_sched_barrier(0);
-        follow(next);
+        follow(most);
       };
-      enter(t);
+      enter();
       products(x, key_buf);
-      follow(x);
+      follow(highest(x));
       int left = run1 - t - 1;  // steps with a next tile
       for (; left >= 2; left -= 2) {
         step(x, y);
         leave();
-        enter(++t);
+        enter(), ++t;
         step(y, x);
         leave();
-        enter(++t);
+        enter(), ++t;
       }
       if (left) {
         step(x, y);
         leave();
-        enter(++t);
+        enter(), ++t;
 #pragma unroll
         for (int kb = 0; kb < kKeys; ++kb) x[kb] = y[kb];
       }
+      fill(t);
       terms(x, p);
       values(v_at + value_buf, p);
       leave();
