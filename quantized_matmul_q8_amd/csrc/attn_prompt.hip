@@ -85,6 +85,12 @@ __device__ __forceinline__ void copy16(v4u buffer, uint32_t off, uint32_t lds) {
                    : "memory");
 }
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+  return static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32))) << 32 |
+         static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x)));
+}
+
 constexpr int gcd16(int c) { return c % 16 == 0 ? 16 : c % 8 == 0 ? 8 : c % 4 == 0 ? 4 : c % 2 == 0 ? 2 : 1; }
 
 // Which sequence a tile belongs to, by the waves' lanes: 64 sequences at a time.
@@ -188,27 +194,29 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     k_off[i] = r * k_bytes + static_cast<uint32_t>((c ^ ((r / kPeriod) & (G - 1))) * 16);
     v_off[i] = r * v_bytes + static_cast<uint32_t>((c ^ (4 * ((r >> kVShift) & kVMask))) * 16);
   }
-  const uint64_t k_base = reinterpret_cast<uint64_t>(a.k) + (static_cast<int64_t>(pl.k0) * a.k_stride + kh * D) * 2;
-  const uint64_t v_base = reinterpret_cast<uint64_t>(a.v) + (static_cast<int64_t>(pl.k0) * a.v_stride + kh * D) * 2;
+  // where the next tiles to copy begin
+  const int64_t first_key = pl.k0 + static_cast<int64_t>(tile0) * BN;
+  uint64_t k_next = uniform(reinterpret_cast<uint64_t>(a.k) + (first_key * a.k_stride + kh * D) * 2);
+  uint64_t v_next = uniform(reinterpret_cast<uint64_t>(a.v) + (first_key * a.v_stride + kh * D) * 2);
+  const uint32_t k_step = BN * k_bytes, v_step = BN * v_bytes;
   const uint32_t k_lds = lds_addr(&s_k[0][0]) + wave * (kCopies * 1024), v_lds = lds_addr(&s_v[0][0]) + wave * (kCopies * 1024);
-  const auto tile_of = [&](uint64_t base, uint32_t bytes, int t) {
-    const int64_t first = static_cast<int64_t>(t) * BN, rows_left = min(int64_t{BN}, pl.nk - first);
-    const uint64_t at = base + first * bytes;
-    const uint32_t size = rows_left > 0 ? static_cast<uint32_t>(rows_left - 1) * bytes + kRowBytes : 0u;
-    v4u r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu, size, 0x00020000u};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_readfirstlane(r[k]);
-    return r;
+  // tile t of rows of `bytes`, which begins at `at`
+  const auto tile_of = [&](uint64_t at, uint32_t bytes, int t) {
+    const int left = min(BN, pl.nk - t * BN);
+    return v4u{static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu,
+               left > 0 ? static_cast<uint32_t>(left - 1) * bytes + kRowBytes : 0u, 0x00020000u};
   };
   // Byte offsets of the buffers of tiles t and t + 1 of keys and of the one to fill, and of tile t of values.
   uint32_t key_buf = 0, next_buf = kTile, fill_buf = kKeyBufs == 3 ? 2 * kTile : kTile, value_buf = 0;
   const auto copy_k = [&](int t, uint32_t buf) {
-    const v4u tile = tile_of(k_base, k_bytes, t);
+    const v4u tile = tile_of(k_next, k_bytes, t);
+    k_next += k_step;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy16(tile, k_off[i], k_lds + buf + i * 1024);
   };
   const auto copy_v = [&](int t, uint32_t buf) {
-    const v4u tile = tile_of(v_base, v_bytes, t);
+    const v4u tile = tile_of(v_next, v_bytes, t);
+    v_next += v_step;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy16(tile, v_off[i], v_lds + buf + i * 1024);
   };
@@ -417,9 +425,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
       // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
       // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
       const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
-        const v4u k_tile = tile_of(k_base, k_bytes, t + 2), v_tile = tile_of(v_base, v_bytes, t + 1);
+        const v4u k_tile = tile_of(k_next, k_bytes, t + 2), v_tile = tile_of(v_next, v_bytes, t + 1);
+        k_next += k_step;
+        v_next += v_step;
         constexpr int kFirst = kSteps * kKeys, kSecond = BN / 16 * kBlocks, kPairs = kKeys * 8;
-        constexpr int kAheadBy = 6, kMaxIn = kSecond - 2;
+        constexpr int kAheadBy = 5, kMaxIn = kSecond - 2;
         const uint32_t k_here = k_at + next_buf, v_here = v_at + value_buf;
         v4u f[kAheadBy];
         float most = -INFINITY;
