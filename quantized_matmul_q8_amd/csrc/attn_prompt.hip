@@ -138,9 +138,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   constexpr int kSteps = D / 16, kBlocks = D / 32, kKeys = BN / 32;
   constexpr float kLift = BF16 ? 0.0f : 7.0f;  // terms of up to 2^(8 + kLift): f16 holds them, and those down to 2^-31
   constexpr float kSlack = 8.0f;               // a maximum is followed when it is passed by 2^8
-  // Where registers allow it, the products of a tile's keys run beside the terms of the tile before: a third buffer of keys.
-  constexpr bool kAhead = D <= 128;
-  constexpr int kKeyBufs = kAhead ? 3 : 2;
+  constexpr int kKeyBufs = 3;
   __shared__ __attribute__((aligned(1024))) uint8_t s_k[kKeyBufs][kTile], s_v[2][kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
@@ -207,7 +205,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
                left > 0 ? static_cast<uint32_t>(left - 1) * bytes + kRowBytes : 0u, 0x00020000u};
   };
   // Byte offsets of the buffers of tiles t and t + 1 of keys and of the one to fill, and of tile t of values.
-  uint32_t key_buf = 0, next_buf = kTile, fill_buf = kKeyBufs == 3 ? 2 * kTile : kTile, value_buf = 0;
+  uint32_t key_buf = 0, next_buf = kTile, fill_buf = 2 * kTile, value_buf = 0;
   const auto copy_k = [&](int t, uint32_t buf) {
     const v4u tile = tile_of(k_next, k_bytes, t);
     k_next += k_step;
@@ -223,7 +221,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   if (tile0 < tile1) {
     copy_k(tile0, key_buf);
     copy_v(tile0, value_buf);
-    if (kAhead) copy_k(tile0 + 1, next_buf);
+    copy_k(tile0 + 1, next_buf);
   }
   // Before a tile: its copies (and the next keys') are there for every wave, and what the other buffers held has been read,
   // so that they may be filled.  Behind the last tile they are filled with zeros.
@@ -232,13 +230,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     __syncthreads();
   };
   const auto fill = [&](int t) {
-    copy_k(t + (kAhead ? 2 : 1), fill_buf);
+    copy_k(t + 2, fill_buf);
     copy_v(t + 1, value_buf ^ kTile);
   };
   const auto leave = [&]() {
     const uint32_t k = key_buf;
     key_buf = next_buf;
-    next_buf = kAhead ? fill_buf : k;
+    next_buf = fill_buf;
     fill_buf = k;
     value_buf ^= kTile;
   };
@@ -415,94 +413,92 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   };
 
   int t = tile0;
-  if constexpr (kAhead) {
-    const int run0 = whole1 - whole0 >= 2 ? whole0 : tile1, run1 = whole1 - whole0 >= 2 ? whole1 : tile1;
-    for (; t < run0; ++t) alone(t);
-    if (t < run1) {
-      v16f x[kKeys], y[kKeys];
-      v4u p[BN / 16];
-      // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
-      // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
-      // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
-      const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
-        const v4u k_tile = tile_of(k_next, k_bytes, t + 2), v_tile = tile_of(v_next, v_bytes, t + 1);
-        k_next += k_step;
-        v_next += v_step;
-        constexpr int kFirst = kSteps * kKeys, kSecond = BN / 16 * kBlocks, kPairs = kKeys * 8;
-        constexpr int kAheadBy = 5, kMaxIn = kSecond - 2;
-        const uint32_t k_here = k_at + next_buf, v_here = v_at + value_buf;
-        v4u f[kAheadBy];
-        float most = -INFINITY;
-        const auto operand = [&](int m) {
-          return m < kFirst ? k_operand(k_here, m % kKeys, m / kKeys)
-                            : v_operand(v_here, (m - kFirst) / kBlocks, (m - kFirst) % kBlocks);
-        };
-        float e[2][2];
-        const auto raise = [&](int n) {
-          const v16f& c = cur[n / 8];
-          e[n & 1][0] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2], mul, base));
-          e[n & 1][1] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2 + 1], mul, base));
-        };
-        const auto pack = [&](int n) {
-          const uint32_t w = pack2<BF16>(e[n & 1][0], e[n & 1][1]);
-          p[n / 4][n % 4] = w;
-          sum = add2<BF16>(w, sum);
-        };
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < kAheadBy; ++m) f[m] = operand(m);
-#pragma unroll
-        for (int m = 0; m < kFirst; ++m) {
-          __builtin_amdgcn_sched_barrier(0);
-          next[m % kKeys] = mfma32<BF16>(f[m % kAheadBy], q[m / kKeys], m < kKeys ? v16f{} : next[m % kKeys]);
-          f[m % kAheadBy] = operand(m + kAheadBy);
-          static_assert(kFirst >= 4 * kCopies);
-          if (m % 4 == 0 && m / 4 < kCopies) copy16(k_tile, k_off[m / 4], k_lds + fill_buf + m / 4 * 1024);
-          if (m % 4 == 2 && m / 4 < kCopies) copy16(v_tile, v_off[m / 4], v_lds + (value_buf ^ kTile) + m / 4 * 1024);
-#pragma unroll
-          for (int n = m * kPairs / kFirst; n < (m + 1) * kPairs / kFirst; ++n) {
-            raise(n);
-            if (n > 0) pack(n - 1);
-          }
-        }
-        pack(kPairs - 1);
-#pragma unroll
-        for (int m = 0; m < kSecond; ++m) {
-          __builtin_amdgcn_sched_barrier(0);
-          o[m % kBlocks] = mfma32<BF16>(f[(kFirst + m) % kAheadBy], p[m / kBlocks], o[m % kBlocks]);
-          if (m + kAheadBy < kSecond) f[(kFirst + m) % kAheadBy] = operand(kFirst + m + kAheadBy);
-#pragma unroll
-          for (int n = m * kPairs / kMaxIn; n < min(kPairs, (m + 1) * kPairs / kMaxIn); ++n) most = higher(most, next, n);
-          if (m == kMaxIn - 1) most = halves_max(most);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        follow(most);
+  const int run0 = whole1 - whole0 >= 2 ? whole0 : tile1, run1 = whole1 - whole0 >= 2 ? whole1 : tile1;
+  for (; t < run0; ++t) alone(t);
+  if (t < run1) {
+    v16f x[kKeys], y[kKeys];
+    v4u p[BN / 16];
+    // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
+    // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
+    // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
+    const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
+      const v4u k_tile = tile_of(k_next, k_bytes, t + 2), v_tile = tile_of(v_next, v_bytes, t + 1);
+      k_next += k_step;
+      v_next += v_step;
+      constexpr int kFirst = kSteps * kKeys, kSecond = BN / 16 * kBlocks, kPairs = kKeys * 8;
+      constexpr int kAheadBy = 5, kMaxIn = kSecond - 2;
+      const uint32_t k_here = k_at + next_buf, v_here = v_at + value_buf;
+      v4u f[kAheadBy];
+      float most = -INFINITY;
+      const auto operand = [&](int m) {
+        return m < kFirst ? k_operand(k_here, m % kKeys, m / kKeys)
+                          : v_operand(v_here, (m - kFirst) / kBlocks, (m - kFirst) % kBlocks);
       };
-      enter();
-      products(x, key_buf);
-      follow(highest(x));
-      int left = run1 - t - 1;  // steps with a next tile
-      for (; left >= 2; left -= 2) {
-        step(x, y);
-        leave();
-        enter(), ++t;
-        step(y, x);
-        leave();
-        enter(), ++t;
-      }
-      if (left) {
-        step(x, y);
-        leave();
-        enter(), ++t;
+      float e[2][2];
+      const auto raise = [&](int n) {
+        const v16f& c = cur[n / 8];
+        e[n & 1][0] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2], mul, base));
+        e[n & 1][1] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[n % 8 * 2 + 1], mul, base));
+      };
+      const auto pack = [&](int n) {
+        const uint32_t w = pack2<BF16>(e[n & 1][0], e[n & 1][1]);
+        p[n / 4][n % 4] = w;
+        sum = add2<BF16>(w, sum);
+      };
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int kb = 0; kb < kKeys; ++kb) x[kb] = y[kb];
+      for (int m = 0; m < kAheadBy; ++m) f[m] = operand(m);
+#pragma unroll
+      for (int m = 0; m < kFirst; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        next[m % kKeys] = mfma32<BF16>(f[m % kAheadBy], q[m / kKeys], m < kKeys ? v16f{} : next[m % kKeys]);
+        f[m % kAheadBy] = operand(m + kAheadBy);
+        static_assert(kFirst >= 4 * kCopies);
+        if (m % 4 == 0 && m / 4 < kCopies) copy16(k_tile, k_off[m / 4], k_lds + fill_buf + m / 4 * 1024);
+        if (m % 4 == 2 && m / 4 < kCopies) copy16(v_tile, v_off[m / 4], v_lds + (value_buf ^ kTile) + m / 4 * 1024);
+#pragma unroll
+        for (int n = m * kPairs / kFirst; n < (m + 1) * kPairs / kFirst; ++n) {
+          raise(n);
+          if (n > 0) pack(n - 1);
+        }
       }
-      fill(t);
-      terms(x, p);
-      values(v_at + value_buf, p);
+      pack(kPairs - 1);
+#pragma unroll
+      for (int m = 0; m < kSecond; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        o[m % kBlocks] = mfma32<BF16>(f[(kFirst + m) % kAheadBy], p[m / kBlocks], o[m % kBlocks]);
+        if (m + kAheadBy < kSecond) f[(kFirst + m) % kAheadBy] = operand(kFirst + m + kAheadBy);
+#pragma unroll
+        for (int n = m * kPairs / kMaxIn; n < min(kPairs, (m + 1) * kPairs / kMaxIn); ++n) most = higher(most, next, n);
+        if (m == kMaxIn - 1) most = halves_max(most);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      follow(most);
+    };
+    enter();
+    products(x, key_buf);
+    follow(highest(x));
+    int left = run1 - t - 1;  // steps with a next tile
+    for (; left >= 2; left -= 2) {
+      step(x, y);
       leave();
-      ++t;
+      enter(), ++t;
+      step(y, x);
+      leave();
+      enter(), ++t;
     }
+    if (left) {
+      step(x, y);
+      leave();
+      enter(), ++t;
+#pragma unroll
+      for (int kb = 0; kb < kKeys; ++kb) x[kb] = y[kb];
+    }
+    fill(t);
+    terms(x, p);
+    values(v_at + value_buf, p);
+    leave();
+    ++t;
   }
   for (; t < tile1; ++t) alone(t);
   wait_vmcnt<0>();
@@ -618,8 +614,8 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
     case 64: launch_prompt<64, 64>(a, type == QMM_BF16, g, st); break;
     case 96: launch_prompt<96, 64>(a, type == QMM_BF16, g, st); break;
     case 128: launch_prompt<128, 64>(a, type == QMM_BF16, g, st); break;
-    case 192: launch_prompt<192, 64>(a, type == QMM_BF16, g, st); break;
-    default: launch_prompt<256, 64>(a, type == QMM_BF16, g, st); break;
+    case 192: launch_prompt<192, 32>(a, type == QMM_BF16, g, st); break;
+    default: launch_prompt<256, 32>(a, type == QMM_BF16, g, st); break;
   }
   if (p.splits > 1)
     hipLaunchKernelGGL(attn_prompt_join_kernel, dim3(static_cast<unsigned>(p.tiles * Hk * (kRows / 4))), dim3(256), 0, st,
