@@ -16,6 +16,7 @@ Tensor layouts (uint8 unless stated):
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -299,18 +300,19 @@ def mmvq_q4g(w: torch.Tensor, scales: torch.Tensor, xq: torch.Tensor, *, zeros: 
 
 def _heads(t: torch.Tensor, name: str, H: int | None = None, D: int | None = None):
     """Checks rows of heads ``[T, H, D]`` (a token's heads next to each other, the tokens any multiple of 8
-    values apart); returns (type code, values from token to token)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    code = _TYPES.get(t.dtype)
+    values apart); returns (type code, values from token to token, T, H, D)."""
+    code = _TYPES.get(getattr(t, "dtype", None))
     if code is None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device")
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (D is not None and t.shape[2] != D):
+    shape = t.shape
+    if len(shape) != 3 or (H is not None and shape[1] != H) or (D is not None and shape[2] != D):
         raise ValueError(f"{name} must be [T, {'heads' if H is None else H}, {'D' if D is None else D}], got "
-                         f"{tuple(t.shape)}")
-    T, H, D = t.shape
+                         f"{tuple(shape)}")
+    T, H, D = shape
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: a token's heads must stand next to each other, got strides {t.stride()}")
@@ -319,7 +321,17 @@ def _heads(t: torch.Tensor, name: str, H: int | None = None, D: int | None = Non
     elif st < H * D or st % 8:
         raise ValueError(f"{name}: tokens must be a multiple of 8 values apart and must not overlap, got strides "
                          f"{t.stride()}")
-    return code, st
+    return code, st, T, H, D
+
+
+def _ints(t: torch.Tensor, dtype: torch.dtype, name: str, index: int, shape: tuple) -> int:
+    """Checks a contiguous tensor of whole numbers on device ``index``; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and t.shape == shape):
+        _need(t, dtype, name, len(shape))
+        _on(index, **{name: t})
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _rope_args(rope, positions, T: int, D: int, index: int):
@@ -328,17 +340,42 @@ def _rope_args(rope, positions, T: int, D: int, index: int):
         if positions is not None:
             raise ValueError("positions need a rope table")
         return None, 0, 0, None
-    _need(rope, torch.float32, "rope", 2)
     if positions is None:
         raise ValueError("a rope table needs positions")
-    _need(positions, torch.int32, "positions", 1)
-    if positions.shape[0] != T:
-        raise ValueError(f"positions must have shape ({T},), got {tuple(positions.shape)}")
-    P, rot = rope.shape
+    P, rot = rope.shape if isinstance(rope, torch.Tensor) and rope.dim() == 2 else (0, 0)
     if P < 1 or rot < 16 or rot % 16 or rot > D:
+        _need(rope, torch.float32, "rope", 2)
         raise ValueError(f"rope must be [positions, rot] with rot a multiple of 16 up to D = {D}, got {tuple(rope.shape)}")
-    _on(index, rope=rope, positions=positions)
-    return rope.data_ptr(), P, rot, positions.data_ptr()
+    return (_ints(rope, torch.float32, "rope", index, (P, rot)), P, rot,
+            _ints(positions, torch.int32, "positions", index, (T,)))
+
+
+def _head_weight(w, name: str, D: int, index: int) -> int:
+    """Checks the weight of a head's norm; returns its type code."""
+    code = _typed(w, name, 1)
+    if w.shape[0] != D:
+        raise ValueError(f"{name} must have shape ({D},), got {tuple(w.shape)}")
+    if w.get_device() != index:
+        _on(index, **{name: w})
+    return code
+
+
+def _heads_out(out, like: torch.Tensor, dtype, T: int, H: int, D: int, stride: int, index: int, name: str):
+    """(out, type code, stride): a new output for ``like``, or the caller's, checked."""
+    if out is None:
+        t = like.dtype if dtype is None else dtype
+        if t not in _TYPES:
+            raise TypeError(f"dtype must be float32, float16 or bfloat16, got {t}")
+        return like.new_empty((T, H, D), dtype=t), _TYPES[t], H * D
+    code, s, n, _, _ = _heads(out, name, H, D)
+    if dtype is not None and out.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {out.dtype}")
+    if n != T:
+        raise ValueError(f"{name} must be of {T} tokens, got {tuple(out.shape)}")
+    _on(index, **{name: out})
+    if out.data_ptr() == like.data_ptr() and T > 0 and (out.dtype != like.dtype or s != stride):
+        raise ValueError(f"{name}: in place needs the dtype and strides of the input")
+    return out, code, s
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: torch.Tensor | None = None,
@@ -356,61 +393,41 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: torch.Ten
     and 2i + 1 if ``interleaved``; values from rot on pass.  Returns ``(q_out,
     k_out)`` in ``dtype`` (default: that of q); ``q_out=q`` works in place.
     """
-    code, qs = _heads(q, "q")
-    T, Hq, D = q.shape
-    index, dev = q.get_device(), q.device
+    code, qs, T, Hq, D = _heads(q, "q")
+    index = q.get_device()
     if D % 32 or not 32 <= D <= 512:
         raise ValueError(f"q: D = {D} must be a multiple of 32 up to 512")
     if not eps >= 0.0:
         raise ValueError(f"eps must be at least 0, got {eps}")
-    Hk = ks = wt = 0
+    Hk = ks = kos = wt = 0
+    kp = kop = qw = kw = None
     if k is not None:
-        kc, ks = _heads(k, "k", None, D)
+        kc, ks, n, Hk, _ = _heads(k, "k", None, D)
         if kc != code:
             raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
-        if k.shape[0] != T:
+        if n != T:
             raise ValueError(f"k must be of {T} tokens, got {tuple(k.shape)}")
-        Hk = k.shape[1]
-        _on(index, k=k)
+        if k.get_device() != index:
+            _on(index, k=k)
+        kp = k.data_ptr()
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            c = _typed(w, name, 1)
-            if w.shape[0] != D:
-                raise ValueError(f"{name} must have shape ({D},), got {tuple(w.shape)}")
-            if q_weight is not None and w.dtype != q_weight.dtype:
-                raise TypeError("q_weight and k_weight must have one dtype")
-            wt = c
-    _on(index, q_weight=q_weight, k_weight=k_weight)
+    if q_weight is not None:
+        wt, qw = _head_weight(q_weight, "q_weight", D, index), q_weight.data_ptr()
+    if k_weight is not None:
+        c = _head_weight(k_weight, "k_weight", D, index)
+        if q_weight is not None and c != wt:
+            raise TypeError("q_weight and k_weight must have one dtype")
+        wt, kw = c, k_weight.data_ptr()
     rp, P, rot, pp = _rope_args(rope, positions, T, D, index)
-
-    def output(out, like, H, name):
-        t = dtype or (like.dtype if out is None else out.dtype)
-        if t not in _TYPES:
-            raise TypeError(f"dtype must be float32, float16 or bfloat16, got {t}")
-        if out is None:
-            out = torch.empty((T, H, D), dtype=t, device=dev)
-        c, s = _heads(out, name, H, D)
-        if out.dtype != t:
-            raise TypeError(f"{name} must be {t}, got {out.dtype}")
-        if out.shape[0] != T:
-            raise ValueError(f"{name} must be of {T} tokens, got {tuple(out.shape)}")
-        _on(index, **{name: out})
-        if out.data_ptr() == like.data_ptr() and T > 0 and (out.dtype != like.dtype or (T > 1 and out.stride() != like.stride())):
-            raise ValueError(f"{name}: in place needs the dtype and strides of the input")
-        return out, c, s
-
-    q_out, oc, qos = output(q_out, q, Hq, "q_out")
-    kos = 0
+    q_out, oc, qos = _heads_out(q_out, q, dtype, T, Hq, D, qs, index, "q_out")
     if k is not None:
-        k_out, kc, kos = output(k_out, k, Hk, "k_out")
+        k_out, kc, kos = _heads_out(k_out, k, dtype, T, Hk, D, ks, index, "k_out")
         if kc != oc:
             raise TypeError("q_out and k_out must have one dtype")
-    _enqueue(index, _lib.LIB.qk_norm_rope, q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, code,
-             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), wt,
-             weight_offset, eps, rp, P, rot, int(bool(interleaved)), pp, q_out.data_ptr(), qos,
-             None if k is None else k_out.data_ptr(), kos, oc, T, Hq, Hk, D)
+        kop = k_out.data_ptr()
+    _enqueue(index, _lib.LIB.qk_norm_rope, q.data_ptr(), qs, kp, ks, code, qw, kw, wt, weight_offset, eps, rp, P, rot,
+             1 if interleaved else 0, pp, q_out.data_ptr(), qos, kop, kos, oc, T, Hq, Hk, D)
     return q_out, k_out
 
 
@@ -423,20 +440,14 @@ def kv_cache_q4(pages: int, page: int, Hk: int, D: int, device) -> torch.Tensor:
 
 def _kv_cache(cache: torch.Tensor):
     """(pages, page, Hk, D) of a cache."""
-    _need(cache, torch.uint8, "cache", 4)
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.is_cuda and cache.is_contiguous()
+            and cache.dim() == 4):
+        _need(cache, torch.uint8, "cache", 4)
     pages, Hk, cells, size = cache.shape
     if pages < 1 or Hk < 1 or cells < 1 or size not in (1280, 1920, 2560, 3840, 5120):
         raise ValueError(f"cache must be [pages, Hk, page/16, 20 D] with D one of 64, 96, 128, 192, 256, got "
                          f"{tuple(cache.shape)}")
     return pages, 16 * cells, Hk, size // 20
-
-
-def _slots(slots: torch.Tensor, index: int, T: int | None = None) -> int:
-    _need(slots, torch.int64, "slots", 1)
-    if T is not None and slots.shape[0] != T:
-        raise ValueError(f"slots must have shape ({T},), got {tuple(slots.shape)}")
-    _on(index, slots=slots)
-    return slots.shape[0]
 
 
 def kv_append_q4(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *,
@@ -451,16 +462,16 @@ def kv_append_q4(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: t
     """
     pages, page, Hk, D = _kv_cache(cache)
     index = cache.get_device()
-    code, ks = _heads(k, "k", Hk, D)
-    vc, vs = _heads(v, "v", Hk, D)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    kc, ks, T, _, _ = _heads(k, "k", Hk, D)
+    vc, vs, n, _, _ = _heads(v, "v", Hk, D)
+    if n != T:
         raise ValueError(f"v must be of {T} tokens, got {tuple(v.shape)}")
-    _slots(slots, index, T)
-    _on(index, k=k, v=v)
+    if k.get_device() != index or v.get_device() != index:
+        _on(index, k=k, v=v)
+    sp = _ints(slots, torch.int64, "slots", index, (T,))
     rp, P, rot, pp = _rope_args(rope, positions, T, D, index)
-    _enqueue(index, _lib.LIB.kv_append_q4, k.data_ptr(), ks, code, v.data_ptr(), vs, vc, rp, P, rot,
-             int(bool(interleaved)), pp, slots.data_ptr(), cache.data_ptr(), pages, page, T, Hk, D)
+    _enqueue(index, _lib.LIB.kv_append_q4, k.data_ptr(), ks, kc, v.data_ptr(), vs, vc, rp, P, rot,
+             1 if interleaved else 0, pp, sp, cache.data_ptr(), pages, page, T, Hk, D)
     return cache
 
 
@@ -469,17 +480,21 @@ def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = to
     """The keys and values ``[T, Hk, D]`` that the slots (int64 ``[T]``) of ``cache`` stand for, in ``dtype``
     (float32, float16: exact; bfloat16: rounded once).  A slot outside the cache gives zeros."""
     pages, page, Hk, D = _kv_cache(cache)
-    index, dev = cache.get_device(), cache.device
-    T = _slots(slots, index)
-    if dtype not in _TYPES:
+    index = cache.get_device()
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        _need(slots, torch.int64, "slots", 1)
+    T = slots.shape[0]
+    sp = _ints(slots, torch.int64, "slots", index, (T,))
+    code = _TYPES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-    k = _out(k, (T, Hk, D), dtype, dev, "k")
-    v = _out(v, (T, Hk, D), dtype, dev, "v")
-    _enqueue(index, _lib.LIB.kv_read_q4, cache.data_ptr(), pages, page, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-             _TYPES[dtype], T, Hk, D)
+    k = cache.new_empty((T, Hk, D), dtype=dtype) if k is None else _out(k, (T, Hk, D), dtype, cache.device, "k")
+    v = cache.new_empty((T, Hk, D), dtype=dtype) if v is None else _out(v, (T, Hk, D), dtype, cache.device, "v")
+    _enqueue(index, _lib.LIB.kv_read_q4, cache.data_ptr(), pages, page, sp, k.data_ptr(), v.data_ptr(), code, T, Hk, D)
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_q4_workspace_bytes(B: int, n: int, Hq: int, Hk: int, D: int, max_len: int) -> int:
     """Bytes of workspace of :func:`attn_q4`; max_len is the table's width times the page size."""
     return int(_lib.LIB.attn_q4_workspace_bytes(B, n, Hq, Hk, D, max_len))
@@ -488,6 +503,29 @@ def attn_q4_workspace_bytes(B: int, n: int, Hq: int, Hk: int, D: int, max_len: i
 def _half(code: int, t: torch.Tensor, name: str) -> None:
     if code == _lib.QMM_F32:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _attn_out(out, q: torch.Tensor, dtype, index: int):
+    """(out, type code): a new output of q's shape, or the caller's, checked."""
+    if out is None:
+        t = q.dtype if dtype is None else dtype
+        if t not in _TYPES:
+            raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {t}")
+        return torch.empty(q.shape, dtype=t, device=q.device), _TYPES[t]
+    _out(out, tuple(q.shape), out.dtype if dtype is None else dtype, q.device)
+    return out, _typed(out, "out", q.dim())
+
+
+def _attn_ws(ws, need: int, q: torch.Tensor, index: int):
+    """(workspace, its address, its bytes): the caller's, checked, or a new one if any is needed."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = q.new_empty(need, dtype=torch.uint8)
+        return ws, ws.data_ptr(), need
+    _need(ws, torch.uint8, "ws", 1)
+    _on(index, ws=ws)
+    return ws, ws.data_ptr(), ws.shape[0]
 
 
 def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, *,
@@ -504,38 +542,32 @@ def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     pages, page, Hk, D = _kv_cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [B, n, Hq, D] or [B, Hq, D]")
-    B, n = q.shape[0], q.shape[1] if q.dim() == 4 else 1
-    rows = q
+    B, n, rows = q.shape[0], 1, q
     if q.dim() == 4:
+        n = q.shape[1]
         if B > 1 and n > 1 and q.stride(0) != n * q.stride(1):
             raise ValueError(f"q: the tokens must be the same distance apart over all sequences, got strides {q.stride()}")
-        rows = q.flatten(0, 1)
-    code, qs = _heads(rows, "q", None, D)
+        rows = q[:, 0] if n == 1 else q.flatten(0, 1)
+    code, qs, _, Hq, _ = _heads(rows, "q", None, D)
     _half(code, q, "q")
-    Hq = rows.shape[1]
     if Hq % Hk or not Hq:
         raise ValueError(f"q: {Hq} heads are no multiple of the cache's {Hk}")
-    _need(table, torch.int32, "table", 2)
-    _need(lens, torch.int32, "lens", 1)
-    if table.shape[0] != B or lens.shape[0] != B or table.shape[1] < 1:
-        raise ValueError(f"table must be [{B}, W] and lens [{B}], got {tuple(table.shape)} and {tuple(lens.shape)}")
     index = cache.get_device()
-    _on(index, q=q, table=table, lens=lens)
-    out = _out(out, tuple(q.shape), out_dtype or (q.dtype if out is None else out.dtype), q.device)
-    yt = _typed(out, "out", q.dim())
-    W = table.shape[1]
-    need = _lib.LIB.attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page)
-    if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    else:
-        _need(ws, torch.uint8, "ws", 1)
-        _on(index, ws=ws)
-    _enqueue(index, _lib.LIB.attn_q4, q.data_ptr(), qs, code, cache.data_ptr(), pages, page, table.data_ptr(), W,
-             lens.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(), yt, B, n, Hq, Hk, D,
-             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    if q.get_device() != index:
+        _on(index, q=q)
+    W = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else 0
+    if W < 1:
+        _need(table, torch.int32, "table", 2)
+        raise ValueError(f"table must be [{B}, W], got {tuple(table.shape)}")
+    tp, lp = _ints(table, torch.int32, "table", index, (B, W)), _ints(lens, torch.int32, "lens", index, (B,))
+    out, yt = _attn_out(out, q, out_dtype, index)
+    ws, wp, size = _attn_ws(ws, attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page), q, index)
+    _enqueue(index, _lib.LIB.attn_q4, q.data_ptr(), qs, code, cache.data_ptr(), pages, page, tp, W, lp,
+             D ** -0.5 if scale is None else scale, window, out.data_ptr(), yt, B, n, Hq, Hk, D, wp, size)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_prompt_workspace_bytes(B: int, Tq: int, Tk: int, Hq: int, Hk: int, D: int) -> int:
     """Bytes of workspace of :func:`attn_prompt`."""
     return int(_lib.LIB.attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D))
@@ -554,37 +586,30 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     that sees no key gives zeros; rows of ``out`` outside the sequences are left
     as they were.  Returns [Tq, Hq, D] in ``out_dtype`` (default: q's).
     """
-    code, qs = _heads(q, "q")
+    code, qs, Tq, Hq, D = _heads(q, "q")
     _half(code, q, "q")
-    Tq, Hq, D = q.shape
-    kc, ks = _heads(k, "k", None, D)
-    Tk, Hk = k.shape[:2]
-    vc, vs = _heads(v, "v", Hk, D)
+    kc, ks, Tk, Hk, _ = _heads(k, "k", None, D)
+    vc, vs, n, _, _ = _heads(v, "v", Hk, D)
     if kc != code or vc != code:
         raise TypeError(f"k and v must be {q.dtype}, got {k.dtype} and {v.dtype}")
-    if v.shape[0] != Tk:
+    if n != Tk:
         raise ValueError(f"k and v must be of as many tokens, got {tuple(k.shape)} and {tuple(v.shape)}")
     if not Hk or not Hq or Hq % Hk:
         raise ValueError(f"q: {Hq} heads are no multiple of the {Hk} of k")
-    cu_k = cu_q if cu_k is None else cu_k
-    _need(cu_q, torch.int32, "cu_q", 1)
-    _need(cu_k, torch.int32, "cu_k", 1)
-    B = cu_q.shape[0] - 1
-    if B < 0 or cu_k.shape[0] != B + 1:
-        raise ValueError(f"cu_q and cu_k must have the same shape [B + 1], got {tuple(cu_q.shape)} and {tuple(cu_k.shape)}")
     index = q.get_device()
-    _on(index, k=k, v=v, cu_q=cu_q, cu_k=cu_k)
-    out = _out(out, (Tq, Hq, D), out_dtype or (q.dtype if out is None else out.dtype), q.device)
-    yt = _typed(out, "out", 3)
-    need = _lib.LIB.attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D)
-    if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    else:
-        _need(ws, torch.uint8, "ws", 1)
-        _on(index, ws=ws)
-    _enqueue(index, _lib.LIB.attn_prompt, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, cu_q.data_ptr(),
-             cu_k.data_ptr(), B, D ** -0.5 if scale is None else scale, int(bool(causal)), window, out.data_ptr(), yt, Tq,
-             Tk, Hq, Hk, D, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    if k.get_device() != index or v.get_device() != index:
+        _on(index, k=k, v=v)
+    B = cu_q.shape[0] - 1 if isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 else -1
+    if B < 0:
+        _need(cu_q, torch.int32, "cu_q", 1)
+        raise ValueError("cu_q must have at least one entry")
+    cq = _ints(cu_q, torch.int32, "cu_q", index, (B + 1,))
+    ck = cq if cu_k is None else _ints(cu_k, torch.int32, "cu_k", index, (B + 1,))
+    out, yt = _attn_out(out, q, out_dtype, index)
+    ws, wp, size = _attn_ws(ws, attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D), q, index)
+    _enqueue(index, _lib.LIB.attn_prompt, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, cq, ck, B,
+             D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), yt, Tq, Tk, Hq, Hk, D,
+             wp, size)
     return out
 
 
