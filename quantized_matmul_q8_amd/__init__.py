@@ -542,13 +542,15 @@ def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     pages, page, Hk, D = _kv_cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [B, n, Hq, D] or [B, Hq, D]")
-    B, n, rows = q.shape[0], 1, q
-    if q.dim() == 4:
-        n = q.shape[1]
-        if B > 1 and n > 1 and q.stride(0) != n * q.stride(1):
+    if q.dim() == 3:
+        n, (code, qs, B, Hq, _) = 1, _heads(q, "q", None, D)
+    else:
+        (B, n, Hq, d), (sb, sn, sh, sd) = q.shape, q.stride()
+        if B > 1 and n > 1 and sb != n * sn:
             raise ValueError(f"q: the tokens must be the same distance apart over all sequences, got strides {q.stride()}")
-        rows = q[:, 0] if n == 1 else q.flatten(0, 1)
-    code, qs, _, Hq, _ = _heads(rows, "q", None, D)
+        code, qs = _TYPES.get(q.dtype, _lib.QMM_F32), (sn if n > 1 else sb) if B * n > 1 else Hq * D
+        if d != D or not q.is_cuda or sd != 1 or (sh != D and Hq > 1) or qs < Hq * D or qs % 8:
+            _heads(q.flatten(0, 1) if n > 1 else q[:, 0], "q", None, D)  # says what does not fit
     _half(code, q, "q")
     if Hq % Hk or not Hq:
         raise ValueError(f"q: {Hq} heads are no multiple of the cache's {Hk}")

@@ -29,7 +29,6 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStep = 32;    // tokens of a step: two cells
-constexpr int kWaves = 4;    // of a workgroup
 constexpr float kLift = 15.0f;  // terms are 2^15 at most: f16 then keeps those down to 2^-39 of the largest
 
 struct AttnQ4Args {
@@ -190,8 +189,8 @@ __device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const Magi
   if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, magic, p, o);
 }
 
-template <int NB, int RT>
-__global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
+template <int NB, int RT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
   constexpr int D = 32 * NB, kRow = D + 4;
   __shared__ float s_o[kWaves][16][kRow];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -382,7 +381,7 @@ __global__ __launch_bounds__(256) void attn_q4_kernel(AttnQ4Args a) {
     for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&s_o[wave][col][b * 16 + 4 * c]) = o[r][b];
     __syncthreads();
     const int row0 = (row_block * RT + r) * 16, rows = min(16, a.rows - row0);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 256) {
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
       const int row = x / (D / 4), d = x % (D / 4) * 4;
       float m = s_m[0][row];
 #pragma unroll
@@ -426,30 +425,38 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   if (lane * 4 < D) store4(a.y_type, a.y, (out * D + lane * 4) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
 
-// How a call is cut: row tiles per workgroup and tokens per chunk, from the sizes that the host knows.
+// How a call is cut, from the sizes that the host knows: waves and row tiles of
+// a workgroup, tokens per chunk.  Short sequences of up to 16 rows are one
+// chunk of eight waves: one launch (1 x 1000, 32/8 heads of 128: ONE us, TWO
+// with four waves, chunks of 256 and their joining).
 struct AttnQ4Plan {
-  int tiles, row_blocks, chunk, chunks;
+  int waves, tiles, row_blocks, chunk, chunks;
 };
+
+constexpr int64_t kOneChunk = 1024;
 
 static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   AttnQ4Plan p;
   const int64_t rows = n * (Hq / Hk), most = D > 128 ? 2 : 4;
   p.tiles = static_cast<int>(rows <= 16 ? 1 : rows <= 32 ? 2 : most);
   p.row_blocks = static_cast<int>((rows + 16 * p.tiles - 1) / (16 * p.tiles));
+  p.waves = rows <= 16 && max_len <= kOneChunk ? 8 : 4;
   const int64_t groups = std::max<int64_t>(1, B * Hk * p.row_blocks), want = (4096 + groups - 1) / groups;
   int64_t chunk = (max_len + want - 1) / want;
   chunk = std::max<int64_t>(256, std::min<int64_t>(2048, chunk));
   chunk = std::max(chunk, (max_len + std::max<int64_t>(64, want) - 1) / std::max<int64_t>(64, want));
+  if (p.waves == 8) chunk = kOneChunk;
   p.chunk = static_cast<int>((chunk + 127) / 128 * 128);
   p.chunks = static_cast<int>((max_len + p.chunk - 1) / p.chunk);
   return p;
 }
 
 template <int NB>
-static void launch_attn_q4(const AttnQ4Args& a, int tiles, dim3 g, hipStream_t st) {
-  if (tiles == 1) hipLaunchKernelGGL((attn_q4_kernel<NB, 1>), g, dim3(256), 0, st, a);
-  else if (tiles == 2 || NB > 4) hipLaunchKernelGGL((attn_q4_kernel<NB, 2>), g, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((attn_q4_kernel<NB, NB <= 4 ? 4 : 2>), g, dim3(256), 0, st, a);
+static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, dim3 g, hipStream_t st) {
+  if (p.waves == 8) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 8>), g, dim3(512), 0, st, a);
+  else if (p.tiles == 1) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 4>), g, dim3(256), 0, st, a);
+  else if (p.tiles == 2 || NB > 4) hipLaunchKernelGGL((attn_q4_kernel<NB, 2, 4>), g, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((attn_q4_kernel<NB, NB <= 4 ? 4 : 2, 4>), g, dim3(256), 0, st, a);
 }
 
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
@@ -495,11 +502,11 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
   const dim3 g(static_cast<unsigned>(grid));
   hipStream_t st = to_stream(stream);
   switch (D) {
-    case 64: launch_attn_q4<2>(a, p.tiles, g, st); break;
-    case 96: launch_attn_q4<3>(a, p.tiles, g, st); break;
-    case 128: launch_attn_q4<4>(a, p.tiles, g, st); break;
-    case 192: launch_attn_q4<6>(a, p.tiles, g, st); break;
-    default: launch_attn_q4<8>(a, p.tiles, g, st); break;
+    case 64: launch_attn_q4<2>(a, p, g, st); break;
+    case 96: launch_attn_q4<3>(a, p, g, st); break;
+    case 128: launch_attn_q4<4>(a, p, g, st); break;
+    case 192: launch_attn_q4<6>(a, p, g, st); break;
+    default: launch_attn_q4<8>(a, p, g, st); break;
   }
   if (p.chunks > 1)
     hipLaunchKernelGGL(attn_q4_join_kernel, dim3(static_cast<unsigned>(B * n * Hq)), dim3(64), 0, st, a,
