@@ -50,32 +50,17 @@ struct AttnQ4Args {
 
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
 
-// The constants of a code's unpacking, in vector registers that the compiler
-// cannot see through: an instruction has room for one literal, so with these an
-// and and an or are one (v_bfi), not two.
-struct Magic {
-  uint32_t low = 0x000f000fu, high = 0x00f000f0u, big = 0x64006400u, small = 0x54005400u;
-  __device__ __forceinline__ Magic() {
-    __asm__ volatile("" : "+v"(big), "+v"(small));
-    __asm__ volatile("" : "+s"(low), "+s"(high));
-  }
-};
-
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  __asm__("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(bits));
-  return r;
-}
-
-// Eight codes of a dword -> the f16 numbers of pairs (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ void codes(uint32_t w, const Magic& k, h2 (&x)[4]) {
-  const h2 big = {static_cast<_Float16>(1024.0f), static_cast<_Float16>(1024.0f)};
-  const h2 small = {static_cast<_Float16>(64.0f), static_cast<_Float16>(64.0f)};
-  const uint32_t u = w >> 8;
-  x[0] = as_h2(and_or(w, k.low, k.big)) - big;
-  x[1] = as_h2(and_or(w, k.high, k.small)) - small;
-  x[2] = as_h2(and_or(u, k.low, k.big)) - big;
-  x[3] = as_h2(and_or(u, k.high, k.small)) - small;
+// Eight codes of a dword -> the f16 numbers of bytes' low halves (0, 1), (2, 3)
+// and high halves (0, 1), (2, 3).  A byte n of 0..15 read as an 8-bit float with
+// three bits of fraction is n * 2^-9, below 8 a subnormal one; the conversion of
+// two multiplies by 2^9.  (With n or-ed into an f16's low bits and the offset
+// subtracted, 13 instead of 11 instructions for eight values.)
+__device__ __forceinline__ void codes(uint32_t w, h2 (&x)[4]) {
+  const uint32_t low = w & 0x0f0f0f0fu, high = (w >> 4) & 0x0f0f0f0fu;
+  x[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(low, 512.0f, false);
+  x[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(low, 512.0f, true);
+  x[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(high, 512.0f, false);
+  x[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(high, 512.0f, true);
 }
 
 __device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
@@ -139,9 +124,9 @@ struct Cell {
   }
 
   // A operand of the products with the queries, number j.
-  __device__ __forceinline__ h8 key_operand(int j, const Magic& magic) const {
+  __device__ __forceinline__ h8 key_operand(int j) const {
     h2 x[4];
-    codes(k[j], magic, x);
+    codes(k[j], x);
     const int s = j < 4 * Runs<NB>::kQuads ? j / 4 : (Runs<NB>::kPair && j < 4 * Runs<NB>::kQuads + 2) ? Runs<NB>::kQuads
                                                                                                     : Runs<NB>::kScales - 1;
     const h2 dm = as_h2(ks[s]), d = {dm.x, dm.x}, m = {dm.y, dm.y};
@@ -151,17 +136,28 @@ struct Cell {
   }
 
   // This cell's half of the A operands of block b's two tiles: dims c and c + 16, four tokens each.
+  // The tokens of each quad come in the order 0, 2, 1, 3.
   template <int b>
-  __device__ __forceinline__ void value_operands(const Magic& magic, h2 (&low)[2], h2 (&high)[2]) const {
+  __device__ __forceinline__ void value_operands(h2 (&low)[2], h2 (&high)[2]) const {
     h2 x[4];
-    codes(v[b], magic, x);
+    codes(v[b], x);
     const uint32_t s = vs[b / 4];
-    const h2 d01 = as_h2(row_bcast<b % 4 * 4>(s)), d23 = as_h2(row_bcast<b % 4 * 4 + 1>(s));
-    const h2 m01 = as_h2(row_bcast<b % 4 * 4 + 2>(s)), m23 = as_h2(row_bcast<b % 4 * 4 + 3>(s));
-    low[0] = __builtin_elementwise_fma(x[0], d01, m01);
-    low[1] = __builtin_elementwise_fma(x[2], d23, m23);
-    high[0] = __builtin_elementwise_fma(x[1], d01, m01);
-    high[1] = __builtin_elementwise_fma(x[3], d23, m23);
+    const h2 d02 = as_h2(row_bcast<b % 4 * 4>(s)), d13 = as_h2(row_bcast<b % 4 * 4 + 1>(s));
+    const h2 m02 = as_h2(row_bcast<b % 4 * 4 + 2>(s)), m13 = as_h2(row_bcast<b % 4 * 4 + 3>(s));
+    low[0] = __builtin_elementwise_fma(x[0], d02, m02);
+    low[1] = __builtin_elementwise_fma(x[1], d13, m13);
+    high[0] = __builtin_elementwise_fma(x[2], d02, m02);
+    high[1] = __builtin_elementwise_fma(x[3], d13, m13);
+  }
+
+  // The values' scales as they are stored, tokens 0 and 1, then 2 and 3, in lanes next to each other -> 0 and 2, 1 and 3.
+  __device__ __forceinline__ void pair_scales(int lane) {
+    const uint32_t pick = (lane & 1) ? 0x03020706u : 0x05040100u;  // bytes of (other, own), own the low ones
+#pragma unroll
+    for (int r = 0; r < kVs; ++r) {
+      const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(vs[r]), 0xb1, 0xf, 0xf, false));
+      vs[r] = __builtin_amdgcn_perm(other, vs[r], pick);
+    }
   }
 };
 
@@ -175,18 +171,18 @@ __device__ __forceinline__ int operand_dim(int j, int c) {
 }
 
 template <int NB, int RT, int b = 0>
-__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const Magic& magic, const h8 (&p)[RT],
+__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (&p)[RT],
                                            v4f (&o)[RT][2 * NB]) {
   h2 l0[2], u0[2], l1[2], u1[2];
-  cell[0].template value_operands<b>(magic, l0, u0);
-  cell[1].template value_operands<b>(magic, l1, u1);
+  cell[0].template value_operands<b>(l0, u0);
+  cell[1].template value_operands<b>(l1, u1);
   const h8 low = join(l0[0], l0[1], l1[0], l1[1]), high = join(u0[0], u0[1], u1[0], u1[1]);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     o[r][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(low, p[r], o[r][2 * b], 0, 0, 0);
     o[r][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(high, p[r], o[r][2 * b + 1], 0, 0, 0);
   }
-  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, magic, p, o);
+  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, p, o);
 }
 
 template <int NB, int RT, int kWaves>
@@ -248,6 +244,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(f[j][k], -e));
     }
+    // in the order of the keys' codes
+#pragma unroll
+    for (int j = 0; j < NB; ++j) q[r][j] = __builtin_shufflevector(q[r][j], q[r][j], 0, 4, 1, 5, 2, 6, 3, 7);
     // a factor above zero, so that the largest product is the largest score
     const _Float16 sign = static_cast<_Float16>(mul[r] == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
@@ -273,7 +272,6 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
     return static_cast<uint32_t>(static_cast<uint64_t>(cell) * a.page_mul >> a.page_shift);
   };
   const auto there = [&](int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages); };
-  const Magic magic;
 
   // one step's two cells and their page numbers
   struct Step {
@@ -304,7 +302,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const h8 k = st.cell[u].key_operand(j, magic);
+        const h8 k = st.cell[u].key_operand(j);
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
       }
@@ -321,6 +319,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
           s[r][k >> 2][k & 3] = seen ? s[r][k >> 2][k & 3] : -INFINITY;
         }
     }
+    st.cell[0].pair_scales(lane);
+    st.cell[1].pair_scales(lane);
     h8 p[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -340,10 +340,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
       for (int k = 0; k < 8; ++k) {
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3], mul[r], base[r]));
         sum[r] += e;
-        p[r][k] = static_cast<_Float16>(e);
+        p[r][(k & 4) + kv_quad_byte(k & 3)] = static_cast<_Float16>(e);
       }
     }
-    add_values<NB, RT>(st.cell, magic, p, o);
+    add_values<NB, RT>(st.cell, p, o);
   };
 
   // Loads run one step ahead in the other buffer and look-ups two; behind the
