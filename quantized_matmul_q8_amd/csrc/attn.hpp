@@ -38,17 +38,18 @@ __device__ __forceinline__ float halves_sum(float v) {
   return halves_join(v, [](float a, float b) { return a + b; });
 }
 
-// One row of four dims per lane from `count` partial results: part + k * step
-// holds number k's sums of terms times values, ml[k * ml_step] its maximum and
-// sum of terms.  The maxima and sums by the lanes, 64 at a time, then the
-// partial results in order, four loads in flight.  Zeros if all sums are 0.
-__device__ __forceinline__ v4f join_parts(const float* part, int64_t step, const float2* ml, int64_t ml_step, int count,
+// One row of four dims per lane from `count` partial results: at `part` + step *
+// at(k) number k's sums of terms times values, in ml[at(k)] its maximum and sum
+// of terms.  The maxima and sums by the lanes, 64 at a time, then the partial
+// results in order, four loads in flight.  Zeros if all sums are 0.
+template <typename At>
+__device__ __forceinline__ v4f join_parts(const At& at, const float* part, int64_t step, const float2* ml, int count,
                                           int lane) {
   float m = -INFINITY, total = 0.0f;
   v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int k0 = 0; k0 < count; k0 += 64) {
     const int here = min(64, count - k0);
-    const float2 own = lane < here ? ml[(k0 + lane) * ml_step] : make_float2(-INFINITY, 0.0f);
+    const float2 own = lane < here ? ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
     float most = fmaxf(m, rows_max(own.x));
 #pragma unroll
     for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
@@ -60,7 +61,7 @@ __device__ __forceinline__ v4f join_parts(const float* part, int64_t step, const
     for (int k = 0; k < here; k += 4) {
       v4f x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + (k0 + min(k + i, here - 1)) * step);
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + at(k0 + min(k + i, here - 1)) * step);
 #pragma unroll
       for (int i = 0; i < 4; ++i) y += x[i] * (k + i < here ? __shfl(f, k + i) : 0.0f);
     }

@@ -540,7 +540,7 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int
   if (!pl.found || row >= pl.nq * a.group) return;
   const int64_t slot = (static_cast<int64_t>(n) * a.Hk + kh) * a.splits * kRows + in_tile;
   const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.tiles) * a.Hk * a.splits * kRows * D);
-  const v4f y = join_parts(a.part + slot * D + min(lane * 4, D - 4), kRows * D, ml + slot, kRows, a.splits, lane);
+  const v4f y = join_parts([&](int k) { return slot + k * kRows; }, a.part + min(lane * 4, D - 4), D, ml, a.splits, lane);
   const int64_t out = (static_cast<int64_t>(pl.q0 + row / a.group) * a.Hq + kh * a.group + row % a.group) * D;
   if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
 }

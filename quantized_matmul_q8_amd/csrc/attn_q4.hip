@@ -14,9 +14,14 @@
 // their bits (0x6400 | n = 1024 + n, 0x5400 | n << 4 = 64 + n), a subtraction
 // that is exact, and one fma: the numbers that the format stands for.
 //
-// A sequence is cut into chunks of tokens, one per workgroup, so that a few
-// long sequences fill the chip; partial results go to the workspace and a
-// second kernel joins them.
+// How the work is dealt out (the host knows no lengths):
+//   short sequences  a workgroup of eight waves takes a sequence and head whole
+//   few of them      each is cut into as many equal parts as fill the chip
+//   many             the steps of all are dealt out to a fixed number of
+//                    workgroups in equal runs, found from the lengths by each,
+//                    so that ragged lengths fill the chip alike
+// Parts, and runs that begin or end inside a sequence, leave partial results in
+// the workspace, and a second kernel joins these.
 #include "attn.hpp"
 #include "kv_q4.hpp"
 
@@ -37,11 +42,15 @@ struct AttnQ4Args {
   const int32_t* table;
   const int32_t* lens;
   void* y;
-  float* part;  // [B * Hq * n rows][chunks][D], then [rows][chunks] pairs (m, l)
+  float* part;  // [slots][rows of a row block][D], then as many pairs (m, l)
   int64_t q_stride, pages, W;
   int64_t max_len;
   float scale;
-  int window, B, n, Hq, Hk, group, rows, row_blocks, chunks, chunk, cells;
+  int window, B, n, Hq, Hk, group, rows, row_blocks, block_rows, cells;
+  int slots;   // of partial results
+  int groups;  // workgroups of equal runs; 0: parts
+  int parts;   // the most of a sequence and head
+  int least;   // the fewest steps of a run or part
   // a cell's page is cell * page_mul >> page_shift: right for cells below 2^31
   uint32_t page_mul, page_shift;
   bool bf16;
@@ -185,30 +194,116 @@ __device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (
   if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, p, o);
 }
 
+// A sequence's length, and the first key that any of its queries sees, in whole steps.
+struct Extent {
+  int len, floor_at, first, steps;  // at least one step, which writes the zeros of an empty sequence
+};
+__device__ __forceinline__ Extent extent_of(const AttnQ4Args& a, int32_t stored) {
+  Extent e;
+  e.len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(stored))));
+  e.floor_at = a.window > 0 ? max(0, e.len - a.n - a.window + 1) : 0;
+  e.first = e.floor_at / kStep * kStep;
+  e.steps = max(1, (e.len - e.first + kStep - 1) / kStep);
+  return e;
+}
+
+// The sequences' steps in a row, by a wave: 64 sequences at a time.  Sums of
+// steps of one head and row block.
+struct Steps {
+  int total = 0;   // of all sequences
+  int before = 0;  // of those before `seq`
+  int seq = 0;
+};
+__device__ __forceinline__ int scan_steps(const AttnQ4Args& a, int b0, int lane, int& mine) {
+  mine = b0 + lane < a.B ? extent_of(a, a.lens[min(b0 + lane, a.B - 1)]).steps : 0;
+  int upto = mine;
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int o = __shfl_up(upto, k);
+    upto += lane >= k ? o : 0;
+  }
+  return upto;
+}
+__device__ __forceinline__ int total_steps(const AttnQ4Args& a, int lane) {
+  int total = 0, mine;
+  for (int b0 = 0; b0 < a.B; b0 += 64) total += __builtin_amdgcn_readlane(scan_steps(a, b0, lane, mine), 63);
+  return total;
+}
+// The sequence in which step `pos` of all heads' lies, and the steps before it; or those before sequence `seq` (pos < 0).
+__device__ __forceinline__ Steps find_steps(const AttnQ4Args& a, int64_t pos, int seq, int lane) {
+  Steps s;
+  const int64_t heads = static_cast<int64_t>(a.Hk) * a.row_blocks;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    int mine;
+    const int upto = scan_steps(a, b0, lane, mine);
+    const uint64_t here = pos < 0 ? (seq < b0 + 64 ? 1ull << (seq - b0) : 0ull)
+                                  : __builtin_amdgcn_ballot_w64((s.before + upto) * heads > pos);
+    if (here) {
+      const int at = __builtin_ctzll(here);
+      s.seq = b0 + at;
+      s.before += __builtin_amdgcn_readlane(upto - mine, at);
+      return s;
+    }
+    s.before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return s;
+}
+
 template <int NB, int RT, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
-  constexpr int D = 32 * NB, kRow = D + 4;
-  __shared__ float s_o[kWaves][16][kRow];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+struct AttnQ4Shared {
+  float o[kWaves][16][32 * NB + 4];
+  float m[kWaves][16], l[kWaves][16];
+};
+
+// Steps `from` .. `to` of one sequence, key head and row block; `slot`: where a partial result goes, or -1 for a whole one.
+template <int NB, int RT, int kWaves>
+__device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB, RT, kWaves>& sh, int seq, int kh,
+                                            int row_block, const Extent& ext, int from, int to, int64_t slot) {
+  constexpr int D = 32 * NB;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
-  // Workgroups go to the eight dies in turn.  The chunk varies slowest, so that
-  // every die has as many of the later ones, which short sequences lack (with it
-  // fastest, 64 x 8192 of ragged lengths took 109 us); the row blocks of one
-  // chunk, which read the same tokens, are eight apart, so on one die.
-  const int span = kXcds * a.row_blocks, row_block = blockIdx.x % span / kXcds;
-  int id = blockIdx.x / span * kXcds + blockIdx.x % kXcds;
-  const int kh = id % a.Hk;
-  id /= a.Hk;
-  const int seq = id % a.B, chunk = id / a.B;
-  if (chunk >= a.chunks) return;
-  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(as_scalar(a.lens)[seq]))));
-  // the first key that any query sees, in whole steps
-  const int floor_at = a.window > 0 ? max(0, len - a.n - a.window + 1) : 0;
-  const int first = floor_at / kStep * kStep;
-  const int begin = first + chunk * a.chunk, end = min(len, begin + a.chunk);
-  const bool split = len - first > a.chunk;
-  if (chunk > 0 && begin >= len) return;
+  const int len = ext.len, floor_at = ext.floor_at;
+  const int begin = ext.first + from * kStep, end = min(len, ext.first + to * kStep);
+
+  const scalar_ints pages = as_scalar(a.table + static_cast<int64_t>(seq) * a.W);
+  const uint64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
+  const uint8_t* head = a.cache + kh * head_bytes;
+  const uint32_t last_cell = static_cast<uint32_t>(max(0, len - 1)) / kCellTokens;  // nothing behind it is looked up or loaded
+  const auto page_of = [&](uint32_t cell) {
+    return static_cast<uint32_t>(static_cast<uint64_t>(cell) * a.page_mul >> a.page_shift);
+  };
+  const auto there = [&](int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages); };
+
+  // one step's two cells and their page numbers
+  struct Step {
+    Cell<NB> cell[2];
+    int page[2];
+  };
+  const auto look_up = [&](int t, int (&page)[2]) {
+#pragma unroll
+    for (uint32_t u = 0; u < 2; ++u) page[u] = pages[page_of(min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell))];
+  };
+  const auto load = [&](Step& s, int t, const int (&page)[2]) {
+#pragma unroll
+    for (uint32_t u = 0; u < 2; ++u) {
+      const uint32_t cell = min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell);
+      const uint32_t pg = there(page[u]) ? page[u] : 0;
+      s.cell[u].load(head + pg * page_bytes + (cell - page_of(cell) * a.cells) * static_cast<uint32_t>(cell_bytes), lane);
+      s.page[u] = page[u];
+    }
+  };
+  // Loads run one step ahead in the other buffer and look-ups two; behind the
+  // end they repeat the last cell, so that every step waits for the same loads.
+  // The first ones before the queries, which have to be waited for.
+  const int stride = kWaves * kStep;
+  int t = begin + wave * kStep;
+  Step x, y;
+  int page[2], ahead[2];
+  if (t < end) {
+    look_up(t, page);
+    look_up(t + stride, ahead);
+    load(x, t, page);
+  }
 
   // queries: this lane's row of each tile, its place, and what a product is multiplied with
   h8 q[RT][NB];
@@ -264,33 +359,6 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
     for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const scalar_ints pages = as_scalar(a.table + static_cast<int64_t>(seq) * a.W);
-  const uint64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
-  const uint8_t* head = a.cache + kh * head_bytes;
-  const uint32_t last_cell = static_cast<uint32_t>(max(0, len - 1)) / kCellTokens;  // nothing behind it is looked up or loaded
-  const auto page_of = [&](uint32_t cell) {
-    return static_cast<uint32_t>(static_cast<uint64_t>(cell) * a.page_mul >> a.page_shift);
-  };
-  const auto there = [&](int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages); };
-
-  // one step's two cells and their page numbers
-  struct Step {
-    Cell<NB> cell[2];
-    int page[2];
-  };
-  const auto look_up = [&](int t, int (&page)[2]) {
-#pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) page[u] = pages[page_of(min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell))];
-  };
-  const auto load = [&](Step& s, int t, const int (&page)[2]) {
-#pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) {
-      const uint32_t cell = min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell);
-      const uint32_t pg = there(page[u]) ? page[u] : 0;
-      s.cell[u].load(head + pg * page_bytes + (cell - page_of(cell) * a.cells) * static_cast<uint32_t>(cell_bytes), lane);
-      s.page[u] = page[u];
-    }
-  };
   const auto work = [&](Step& st, int t) {
     const bool there0 = there(st.page[0]), there1 = there(st.page[1]);
     // whether every query sees the whole step
@@ -346,16 +414,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
     add_values<NB, RT>(st.cell, p, o);
   };
 
-  // Loads run one step ahead in the other buffer and look-ups two; behind the
-  // end they repeat the last cell, so that every step waits for the same loads.
-  const int stride = kWaves * kStep;
-  int t = begin + wave * kStep;
   if (t < end) {
-    Step x, y;
-    int page[2], ahead[2];
-    look_up(t, page);
-    look_up(t + stride, ahead);
-    load(x, t, page);
     // in pairs, with no way out between the two: each step then waits for its own loads alone
     const int steps = (end - t + stride - 1) / stride;
     for (int k = 1; k < steps; k += 2) {
@@ -376,34 +435,33 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const float l = rows_sum(sum[r]);
-    if (c == 0) s_m[wave][col] = top[r] * mul[r], s_l[wave][col] = l;
+    if (c == 0) sh.m[wave][col] = top[r] * mul[r], sh.l[wave][col] = l;
 #pragma unroll
-    for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&s_o[wave][col][b * 16 + 4 * c]) = o[r][b];
+    for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
     __syncthreads();
     const int row0 = (row_block * RT + r) * 16, rows = min(16, a.rows - row0);
     for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
       const int row = x / (D / 4), d = x % (D / 4) * 4;
-      float m = s_m[0][row];
+      float m = sh.m[0][row];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][row]);
-      const float base = m == -INFINITY ? 0.0f : m;
+      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
+      const float zero = m == -INFINITY ? 0.0f : m;
       float total = 0.0f;
       v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_m[w][row] - base);
-        total += s_l[w][row] * f;
-        y += *reinterpret_cast<const v4f*>(&s_o[w][row][d]) * f;
+        const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - zero);
+        total += sh.l[w][row] * f;
+        y += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
       }
-      const int i = (row0 + row) / a.group, h = kh * a.group + (row0 + row) % a.group;
-      const int64_t out = (static_cast<int64_t>(seq) * a.n + i) * a.Hq + h;
-      if (split) {
-        *reinterpret_cast<v4f*>(a.part + (out * a.chunks + chunk) * D + d) = y;
-        if (d == 0) {
-          float* ml = a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D + (out * a.chunks + chunk) * 2;
-          ml[0] = m, ml[1] = total;
-        }
+      if (slot >= 0) {
+        const int64_t at_row = slot * a.block_rows + r * 16 + row;
+        *reinterpret_cast<v4f*>(a.part + at_row * D + d) = y;
+        if (d == 0)
+          reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D)[at_row] = make_float2(m, total);
       } else {
+        const int i = (row0 + row) / a.group, h = kh * a.group + (row0 + row) % a.group;
+        const int64_t out = (static_cast<int64_t>(seq) * a.n + i) * a.Hq + h;
         y *= total == 0.0f ? 0.0f : 1.0f / total;
         store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
       }
@@ -412,56 +470,150 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
   }
 }
 
-// Joins the chunks of one row, a wave each; sequences of one chunk have been written.
+// One workgroup for each sequence, key head and row block: no partial results.
+template <int NB, int RT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
+  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
+  const int row_block = blockIdx.x % a.row_blocks, kh = blockIdx.x / a.row_blocks % a.Hk;
+  const int seq = blockIdx.x / a.row_blocks / a.Hk;
+  const Extent e = extent_of(a, as_scalar(a.lens)[seq]);
+  attn_q4_run<NB, RT, kWaves>(a, sh, seq, kh, row_block, e, 0, e.steps, -1);
+}
+
+// The parts of a sequence of so many steps.
+__device__ __forceinline__ int parts_of(const AttnQ4Args& a, int steps) { return min(a.parts, (steps + a.least - 1) / a.least); }
+
+// Parts or equal runs.
+template <int NB, int RT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void attn_q4_split_kernel(AttnQ4Args a) {
+  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
+  const int lane = threadIdx.x & 63, heads = a.Hk * a.row_blocks, id = blockIdx.x;
+  int seq, head, from, to;
+  int64_t slot, left = 0;  // left: steps of the run behind this sequence and head's
+  Extent e;
+  if (a.groups == 0) {
+    // parts vary slowest: the first ones, which every sequence has, over all dies
+    const int items = a.B * heads, item = id % items, part = id / items;
+    seq = item / heads, head = item % heads;
+    e = extent_of(a, as_scalar(a.lens)[seq]);
+    const int parts = parts_of(a, e.steps);
+    if (part >= parts) return;
+    const int each = e.steps / parts, more = e.steps % parts;  // the first ones have one more
+    from = part * each + min(part, more);
+    to = from + each + (part < more ? 1 : 0);
+    slot = parts == 1 ? -1 : id;
+  } else {
+    const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
+    const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
+    const int64_t first = id * per, last = min(total, first + per);
+    if (first >= last) return;
+    const Steps at = find_steps(a, first, 0, lane);
+    seq = at.seq;
+    e = extent_of(a, as_scalar(a.lens)[seq]);
+    const int64_t in = first - static_cast<int64_t>(at.before) * heads;
+    head = static_cast<int>(in / e.steps);
+    from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
+    to = static_cast<int>(min(static_cast<int64_t>(e.steps), from + last - first));
+    slot = from == 0 && to == e.steps ? -1 : 2 * int64_t{id};
+    left = last - first - (to - from);
+  }
+  for (;;) {
+    attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to, slot);
+    if (left == 0) break;
+    if (++head == heads) {
+      head = 0;
+      e = extent_of(a, as_scalar(a.lens)[++seq]);
+    }
+    from = 0;
+    to = static_cast<int>(min(static_cast<int64_t>(e.steps), left));
+    slot = to == e.steps ? -1 : 2 * int64_t{id} + 1;
+    left -= to;
+  }
+}
+
+// Joins the partial results of one row, a wave each.
 __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
+  const int lane = threadIdx.x, h = blockIdx.x % a.Hq, i = blockIdx.x / a.Hq % a.n, seq = blockIdx.x / a.Hq / a.n;
+  const int row = i * a.group + h % a.group, in = row % a.block_rows, heads = a.Hk * a.row_blocks;
+  const int head = h / a.group * a.row_blocks + row / a.block_rows;
+  const int steps = extent_of(a, as_scalar(a.lens)[seq]).steps;
+  int64_t first, second, step;  // the slots: the first, and the others' beginning and distance
+  int count;
+  if (a.groups == 0) {
+    count = parts_of(a, steps);
+    step = static_cast<int64_t>(a.B) * heads;
+    first = static_cast<int64_t>(seq) * heads + head;
+    second = first + step;
+  } else {
+    const Steps at = find_steps(a, -1, seq, lane);
+    const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
+    const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
+    const int64_t begin = static_cast<int64_t>(at.before) * heads + static_cast<int64_t>(head) * steps;
+    const int64_t g0 = begin / per, g1 = (begin + steps - 1) / per;
+    count = static_cast<int>(g1 - g0 + 1);
+    // the first run's second result, unless the run begins with it; the others' first
+    first = 2 * g0 + (begin == g0 * per ? 0 : 1);
+    second = 2 * (g0 + 1);
+    step = 2;
+  }
+  if (count == 1) return;  // whole, and written
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D);
+  const v4f y = join_parts([&](int k) { return (k == 0 ? first : second + (k - 1) * step) * a.block_rows + in; },
+                           a.part + min(lane * 4, D - 4), D, ml, count, lane);
   const int64_t out = blockIdx.x;
-  const int seq = static_cast<int>(out / (static_cast<int64_t>(a.n) * a.Hq));
-  const int len = static_cast<int>(max(int64_t{0}, min(a.max_len, static_cast<int64_t>(as_scalar(a.lens)[seq]))));
-  const int first = a.window > 0 ? max(0, len - a.n - a.window + 1) / kStep * kStep : 0;
-  if (len - first <= a.chunk) return;
-  const int count = (len - first + a.chunk - 1) / a.chunk, lane = threadIdx.x;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.B) * a.n * a.Hq * a.chunks * D);
-  const v4f y = join_parts(a.part + out * a.chunks * D + min(lane * 4, D - 4), D, ml + out * a.chunks, 1, count, lane);
   if (lane * 4 < D) store4(a.y_type, a.y, (out * D + lane * 4) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
 
-// How a call is cut, from the sizes that the host knows: waves and row tiles of
-// a workgroup, tokens per chunk.  Short sequences of up to 16 rows are one
-// chunk of eight waves: one launch (1 x 1000, 32/8 heads of 128: ONE us, TWO
-// with four waves, chunks of 256 and their joining).
+// How a call is cut, from the sizes that the host knows.
 struct AttnQ4Plan {
-  int waves, tiles, row_blocks, chunk, chunks;
+  int waves, tiles, row_blocks;
+  int groups, parts, least;  // all 0: whole sequences
+  int64_t slots;
 };
 
-constexpr int64_t kOneChunk = 1024;
+constexpr int64_t kOneRun = 1024;  // the longest sequences that are taken whole, in tokens
+constexpr int kGroups = 512;       // two workgroups per CU
+constexpr int kLeast = 8;          // steps: two a wave
 
 static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
-  AttnQ4Plan p;
+  AttnQ4Plan p{4, 1, 1, 0, 0, 0, 0};
   const int64_t rows = n * (Hq / Hk), most = D > 128 ? 2 : 4;
   p.tiles = static_cast<int>(rows <= 16 ? 1 : rows <= 32 ? 2 : most);
   p.row_blocks = static_cast<int>((rows + 16 * p.tiles - 1) / (16 * p.tiles));
-  p.waves = rows <= 16 && max_len <= kOneChunk ? 8 : 4;
-  const int64_t groups = std::max<int64_t>(1, B * Hk * p.row_blocks), want = (4096 + groups - 1) / groups;
-  int64_t chunk = (max_len + want - 1) / want;
-  chunk = std::max<int64_t>(256, std::min<int64_t>(2048, chunk));
-  chunk = std::max(chunk, (max_len + std::max<int64_t>(64, want) - 1) / std::max<int64_t>(64, want));
-  if (p.waves == 8) chunk = kOneChunk;
-  p.chunk = static_cast<int>((chunk + 127) / 128 * 128);
-  p.chunks = static_cast<int>((max_len + p.chunk - 1) / p.chunk);
+  if (rows <= 16 && max_len <= kOneRun) {
+    p.waves = 8;
+    return p;
+  }
+  const int64_t items = B * Hk * p.row_blocks, steps = (max_len + kStep - 1) / kStep + 1;
+  p.least = kLeast;
+  if (items >= kGroups / 2) {
+    p.groups = static_cast<int>(std::min<int64_t>(kGroups, (items * steps + kLeast - 1) / kLeast));
+    p.slots = 2 * p.groups;
+  } else {
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kGroups / std::max<int64_t>(1, items), (steps + kLeast - 1) / kLeast)));
+    p.slots = p.parts == 1 ? 0 : items * p.parts;
+  }
   return p;
 }
 
+template <int NB, int RT>
+static void launch_split(const AttnQ4Args& a, dim3 g, hipStream_t st) {
+  hipLaunchKernelGGL((attn_q4_split_kernel<NB, RT, 4>), g, dim3(256), 0, st, a);
+}
 template <int NB>
-static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, dim3 g, hipStream_t st) {
-  if (p.waves == 8) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 8>), g, dim3(512), 0, st, a);
-  else if (p.tiles == 1) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 4>), g, dim3(256), 0, st, a);
-  else if (p.tiles == 2 || NB > 4) hipLaunchKernelGGL((attn_q4_kernel<NB, 2, 4>), g, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((attn_q4_kernel<NB, NB <= 4 ? 4 : 2, 4>), g, dim3(256), 0, st, a);
+static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, hipStream_t st) {
+  const unsigned items = static_cast<unsigned>(a.B) * a.Hk * a.row_blocks;
+  const dim3 g(p.groups ? static_cast<unsigned>(p.groups) : items * p.parts);
+  if (p.waves == 8) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 8>), dim3(items), dim3(512), 0, st, a);
+  else if (p.tiles == 1) launch_split<NB, 1>(a, g, st);
+  else if (p.tiles == 2 || NB > 4) launch_split<NB, 2>(a, g, st);
+  else launch_split<NB, NB <= 4 ? 4 : 2>(a, g, st);
 }
 
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   return B >= 0 && n >= 1 && n <= QMM_ATTN_MAX_N && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
-         attn_head_dim(D) && max_len >= 1 && max_len <= (int64_t{1} << 30) && B < (int64_t{1} << 26) / (n * Hq);
+         attn_head_dim(D) && max_len >= 1 && max_len <= (int64_t{1} << 30) && B < (int64_t{1} << 26) / (n * Hq) &&
+         B * ((max_len + kStep - 1) / kStep + 1) < (int64_t{1} << 31);
 }
 
 }  // namespace qmm
@@ -470,8 +622,8 @@ using namespace qmm;
 
 extern "C" size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   if (!attn_q4_shape(B, n, Hq, Hk, D, max_len)) return 0;
-  const int64_t chunks = attn_q4_plan(B, n, Hq, Hk, D, max_len).chunks;
-  return chunks == 1 ? 0 : static_cast<size_t>(B * n * Hq * chunks * (D + 2) * 4 + 15) / 16 * 16;
+  const AttnQ4Plan p = attn_q4_plan(B, n, Hq, Hk, D, max_len);
+  return static_cast<size_t>(p.slots) * (16 * p.tiles) * (D + 2) * 4;
 }
 
 extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* cache, int64_t pages, int64_t page,
@@ -489,26 +641,24 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
   const AttnQ4Plan p = attn_q4_plan(B, n, Hq, Hk, D, W * page);
-  const int64_t grid = (B * Hk * p.chunks + kXcds - 1) / kXcds * kXcds * p.row_blocks;
-  if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const int cells = static_cast<int>(page / kCellTokens);
   uint32_t shift = 31;
   while ((int64_t{1} << (shift - 31)) < cells) ++shift;
   const AttnQ4Args a{q, static_cast<const uint8_t*>(cache), table, lens, y, static_cast<float*>(ws), q_stride, pages, W,
                      W * page, scale, static_cast<int>(window), static_cast<int>(B), static_cast<int>(n),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk),
-                     static_cast<int>(n * (Hq / Hk)), p.row_blocks, p.chunks, p.chunk, cells,
+                     static_cast<int>(n * (Hq / Hk)), p.row_blocks, 16 * p.tiles, cells,
+                     static_cast<int>(p.slots), p.groups, p.parts, p.least,
                      static_cast<uint32_t>(((uint64_t{1} << shift) + cells - 1) / cells), shift, type == QMM_BF16, y_type};
-  const dim3 g(static_cast<unsigned>(grid));
   hipStream_t st = to_stream(stream);
   switch (D) {
-    case 64: launch_attn_q4<2>(a, p, g, st); break;
-    case 96: launch_attn_q4<3>(a, p, g, st); break;
-    case 128: launch_attn_q4<4>(a, p, g, st); break;
-    case 192: launch_attn_q4<6>(a, p, g, st); break;
-    default: launch_attn_q4<8>(a, p, g, st); break;
+    case 64: launch_attn_q4<2>(a, p, st); break;
+    case 96: launch_attn_q4<3>(a, p, st); break;
+    case 128: launch_attn_q4<4>(a, p, st); break;
+    case 192: launch_attn_q4<6>(a, p, st); break;
+    default: launch_attn_q4<8>(a, p, st); break;
   }
-  if (p.chunks > 1)
+  if (p.slots > 0)
     hipLaunchKernelGGL(attn_q4_join_kernel, dim3(static_cast<unsigned>(B * n * Hq)), dim3(64), 0, st, a,
                        static_cast<int>(D));
   return launch_status();
