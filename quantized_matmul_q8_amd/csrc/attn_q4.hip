@@ -483,51 +483,49 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
 // The parts of a sequence of so many steps.
 __device__ __forceinline__ int parts_of(const AttnQ4Args& a, int steps) { return min(a.parts, (steps + a.least - 1) / a.least); }
 
-// Parts or equal runs.
+// Equal parts of a sequence and head each.  The parts vary slowest: the first ones, which every sequence has, over all dies.
 template <int NB, int RT, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void attn_q4_split_kernel(AttnQ4Args a) {
+__global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a) {
   __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
-  const int lane = threadIdx.x & 63, heads = a.Hk * a.row_blocks, id = blockIdx.x;
-  int seq, head, from, to;
-  int64_t slot, left = 0;  // left: steps of the run behind this sequence and head's
-  Extent e;
-  if (a.groups == 0) {
-    // parts vary slowest: the first ones, which every sequence has, over all dies
-    const int items = a.B * heads, item = id % items, part = id / items;
-    seq = item / heads, head = item % heads;
-    e = extent_of(a, as_scalar(a.lens)[seq]);
-    const int parts = parts_of(a, e.steps);
-    if (part >= parts) return;
-    const int each = e.steps / parts, more = e.steps % parts;  // the first ones have one more
-    from = part * each + min(part, more);
-    to = from + each + (part < more ? 1 : 0);
-    slot = parts == 1 ? -1 : id;
-  } else {
-    const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
-    const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
-    const int64_t first = id * per, last = min(total, first + per);
-    if (first >= last) return;
-    const Steps at = find_steps(a, first, 0, lane);
-    seq = at.seq;
-    e = extent_of(a, as_scalar(a.lens)[seq]);
-    const int64_t in = first - static_cast<int64_t>(at.before) * heads;
-    head = static_cast<int>(in / e.steps);
-    from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
-    to = static_cast<int>(min(static_cast<int64_t>(e.steps), from + last - first));
-    slot = from == 0 && to == e.steps ? -1 : 2 * int64_t{id};
-    left = last - first - (to - from);
-  }
+  const unsigned heads = a.Hk * a.row_blocks, items = a.B * heads, item = blockIdx.x % items, seq = item / heads;
+  const int part = blockIdx.x / items, head = item % heads;
+  const Extent e = extent_of(a, as_scalar(a.lens)[seq]);
+  const int parts = parts_of(a, e.steps);
+  if (part >= parts) return;
+  const int each = static_cast<unsigned>(e.steps) / parts, more = e.steps - each * parts;  // the first ones have one more
+  const int from = part * each + min(part, more), to = from + each + (part < more ? 1 : 0);
+  attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to,
+                              parts == 1 ? -1 : int64_t{blockIdx.x});
+}
+
+// Equal runs of the steps of all.
+template <int NB, int RT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a) {
+  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
+  const int lane = threadIdx.x & 63, heads = a.Hk * a.row_blocks;
+  const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
+  const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
+  const int64_t first = blockIdx.x * per;
+  int64_t left = min(total - first, per);  // steps of the run
+  if (left <= 0) return;
+  const Steps at = find_steps(a, first, 0, lane);
+  int seq = at.seq;
+  Extent e = extent_of(a, as_scalar(a.lens)[seq]);
+  const int64_t in = first - static_cast<int64_t>(at.before) * heads;
+  int head = static_cast<int>(in / e.steps), from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
+  int64_t slot = 2 * int64_t{blockIdx.x};
   for (;;) {
-    attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to, slot);
+    const int to = static_cast<int>(min(static_cast<int64_t>(e.steps), from + left));
+    attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to,
+                                from == 0 && to == e.steps ? -1 : slot);
+    left -= to - from;
     if (left == 0) break;
+    from = 0;
+    slot = 2 * int64_t{blockIdx.x} + 1;  // the last one's, should it not be whole
     if (++head == heads) {
       head = 0;
       e = extent_of(a, as_scalar(a.lens)[++seq]);
     }
-    from = 0;
-    to = static_cast<int>(min(static_cast<int64_t>(e.steps), left));
-    slot = to == e.steps ? -1 : 2 * int64_t{id} + 1;
-    left -= to;
   }
 }
 
@@ -598,7 +596,8 @@ static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
 
 template <int NB, int RT>
 static void launch_split(const AttnQ4Args& a, dim3 g, hipStream_t st) {
-  hipLaunchKernelGGL((attn_q4_split_kernel<NB, RT, 4>), g, dim3(256), 0, st, a);
+  if (a.groups) hipLaunchKernelGGL((attn_q4_runs_kernel<NB, RT, 4>), g, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((attn_q4_parts_kernel<NB, RT, 4>), g, dim3(256), 0, st, a);
 }
 template <int NB>
 static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, hipStream_t st) {
