@@ -431,8 +431,8 @@ int swiglu_q8_1(const float* g_u, void* hq, int64_t R, int64_t F, void* stream);
  * q_out and k_out have strides of their own; q_out == q is allowed where type
  * and stride are the same, and so for k; no other buffers may overlap.
  * Squares may leave the fp32 range at either end; a head of zeros gives zeros.
- * Requires 0 <= T < 2^31, 1 <= Hq, Hk <= 1024, D % 32 == 0, 32 <= D <= 512,
- * eps >= 0, 1 <= P < 2^31.  T == 0 is a no-op.
+ * Requires T >= 0, 1 <= Hq, Hk <= 1024, T * (Hq + Hk) < 2^31, D % 32 == 0, 32
+ * <= D <= 512, eps >= 0, 1 <= P < 2^31.  T == 0 is a no-op.
  */
 int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int type, const void* q_weight,
                  const void* k_weight, int w_type, float weight_offset, float eps, const float* rope, int64_t P,
@@ -467,8 +467,8 @@ int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_strid
  * beyond +-32768 as that):
  *   d = f16((max - min) / 15), m = f16(min),
  *   n = clamp(rint((x - m) * (1/d)), 0, 15), 0 where d == 0
- * in IEEE fp32 without contraction: the bytes are defined to the bit, and
- * every value that the cache holds is finite.  A NULL rope (with rot == 0)
+ * in IEEE fp32 without contraction, zeros without a sign: the bytes are defined
+ * to the bit, and every value that the cache holds is finite.  A NULL rope (with rot == 0)
  * stores the keys unturned and takes no positions.
  * Requires T >= 0, 1 <= Hk <= 1024, D one of 64, 96, 128, 192, 256, page % 16
  * == 0 and 16 <= page <= 2^20, 1 <= pages < 2^31, T * Hk < 2^31.  T == 0 is a

@@ -42,7 +42,7 @@ def q4_blocks(x: np.ndarray):
     """fp32 ``x[..., D]`` -> codes [..., D], d and m [..., D/32] as f16: the steps of kv_append_q4."""
     x = np.asarray(x, F32)
     b = np.clip(np.where(np.isnan(x), F32(0), x), F32(-32768), F32(32768)).reshape(*x.shape[:-1], -1, 32)
-    lo, hi = b.min(-1) + F32(0), b.max(-1)
+    lo, hi = b.min(-1) + F32(0), b.max(-1) + F32(0)              # no minus zero
     d, m = ((hi - lo) / F32(15)).astype(np.float16), lo.astype(np.float16)
     df = d.astype(F32)
     with np.errstate(divide="ignore"):

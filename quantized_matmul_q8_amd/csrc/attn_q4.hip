@@ -30,7 +30,6 @@
 
 namespace qmm {
 
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStep = 32;    // tokens of a step: two cells
@@ -57,19 +56,14 @@ struct AttnQ4Args {
   int y_type;
 };
 
-__device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
-
-// Eight codes of a dword -> the f16 numbers of bytes' low halves (0, 1), (2, 3)
-// and high halves (0, 1), (2, 3).  A byte n of 0..15 read as an 8-bit float with
-// three bits of fraction is n * 2^-9, below 8 a subnormal one; the conversion of
-// two multiplies by 2^9.  (With n or-ed into an f16's low bits and the offset
-// subtracted, 13 instead of 11 instructions for eight values.)
+// Eight codes of a dword -> the f16 numbers of bytes' low halves (0, 1), (2, 3) and high halves (0, 1), (2, 3).  (With a
+// code or-ed into an f16's low bits and the offset subtracted: 13 instead of 11 instructions with the scales.)
 __device__ __forceinline__ void codes(uint32_t w, h2 (&x)[4]) {
   const uint32_t low = w & 0x0f0f0f0fu, high = (w >> 4) & 0x0f0f0f0fu;
-  x[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(low, 512.0f, false);
-  x[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(low, 512.0f, true);
-  x[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(high, 512.0f, false);
-  x[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(high, 512.0f, true);
+  x[0] = codes_to_f16<false>(low);
+  x[1] = codes_to_f16<true>(low);
+  x[2] = codes_to_f16<false>(high);
+  x[3] = codes_to_f16<true>(high);
 }
 
 __device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
@@ -569,7 +563,10 @@ struct AttnQ4Plan {
   int64_t slots;
 };
 
-constexpr int64_t kOneRun = 1024;  // the longest sequences that are taken whole, in tokens
+// The longest sequences that are taken whole, in tokens: one launch.  1 x 1000,
+// 32/8 heads of 128: 9.7 us in a graph and 10.7 us a call by itself; as parts
+// 8.5 and 14.3; 32 x 1000: 12.1 and, as parts, 16.2 in a graph.
+constexpr int64_t kWhole = 1024;
 constexpr int kGroups = 512;       // two workgroups per CU
 constexpr int kLeast = 8;          // steps: two a wave
 
@@ -578,11 +575,11 @@ static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
   const int64_t rows = n * (Hq / Hk), most = D > 128 ? 2 : 4;
   p.tiles = static_cast<int>(rows <= 16 ? 1 : rows <= 32 ? 2 : most);
   p.row_blocks = static_cast<int>((rows + 16 * p.tiles - 1) / (16 * p.tiles));
-  if (rows <= 16 && max_len <= kOneRun) {
+  const int64_t items = B * Hk * p.row_blocks, steps = (max_len + kStep - 1) / kStep + 1;
+  if (rows <= 16 && max_len <= kWhole) {
     p.waves = 8;
     return p;
   }
-  const int64_t items = B * Hk * p.row_blocks, steps = (max_len + kStep - 1) / kStep + 1;
   p.least = kLeast;
   if (items >= kGroups / 2) {
     p.groups = static_cast<int>(std::min<int64_t>(kGroups, (items * steps + kLeast - 1) / kLeast));

@@ -17,47 +17,66 @@ struct AppendArgs {
   const int64_t* slots;
   uint8_t* cache;
   int64_t P, pages, page, T;
-  int Hk, D, rot, row_lanes, per_wave;
+  int Hk, D, rot, row_lanes, per_wave, shift;
   bool interleaved;
 };
 
-// The codes of a block by a quad of lanes, eight values each, packed 4 bits
-// each in the order of the values; and its d and m as f16 bits.
-__device__ __forceinline__ uint32_t q4_block_4lanes(const float (&x)[8], uint32_t& dm) {
-#pragma clang fp contract(off)
-  float v[8], lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -32768.0f), 32768.0f) : 0.0f;
-    lo = fminf(lo, v[j]);
-    hi = fmaxf(hi, v[j]);
-  }
-  lo = fminf(lo, lane8_xchg<0xb1>(lo));
-  lo = fminf(lo, lane8_xchg<0x4e>(lo)) + 0.0f;  // no minus zero
-  hi = fmaxf(hi, lane8_xchg<0xb1>(hi));
-  hi = fmaxf(hi, lane8_xchg<0x4e>(hi));
-  const uint32_t db = f2h_bits((hi - lo) / 15.0f), mb = f2h_bits(lo);
-  const float d = h2f(db), m = h2f(mb), inv = d > 0.0f ? 1.0f / d : 0.0f;
-  uint32_t codes = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float n = fminf(fmaxf(rintf((v[j] - m) * inv), 0.0f), 15.0f);
-    codes |= static_cast<uint32_t>(n) << (4 * j);
-  }
-  dm = db | mb << 16;
-  return codes;
-}
+// Eight of a block's values, by a quad of lanes.
+struct Block8 {
+  float v[8], d, m, inv;
+  uint32_t dm;  // d and m as f16 bits
 
-// Eight codes in order -> a dword of the key layout: byte i holds codes
-// {0, 4, 1, 5}[i] and the code two further.
-__device__ __forceinline__ uint32_t key_dword(uint32_t c) {
-  uint32_t w = 0;
+  // d, m and 1/d.  Quotients are the IEEE ones: with a correctly rounded
+  // reciprocal of the divisor one step from the remainder rounds correctly
+  // (Markstein), and so does one step of the reciprocal itself for a divisor of
+  // eleven bits.
+  __device__ __forceinline__ void scales() {
+#pragma clang fp contract(off)
+    float lo = v[0], hi = v[0], any = v[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = (i & 1) * 4 + (i >> 1);
-    w |= ((c >> (4 * n)) & 15u) << (8 * i) | ((c >> (4 * n + 8)) & 15u) << (8 * i + 4);
+    for (int j = 1; j < 8; ++j) {
+      lo = fminf(lo, v[j]);
+      hi = fmaxf(hi, v[j]);
+      any += v[j];
+    }
+    // what is not a number or beyond the range (or sums to either) goes the long way
+    if (__builtin_amdgcn_ballot_w64(!(fabsf(any) <= 32768.0f * 8.0f) || lo < -32768.0f || hi > 32768.0f)) {
+      lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = v[j] == v[j] ? fminf(fmaxf(v[j], -32768.0f), 32768.0f) : 0.0f;
+        lo = fminf(lo, v[j]);
+        hi = fmaxf(hi, v[j]);
+      }
+    }
+    lo = fminf(lo, lane8_xchg<0xb1>(lo));
+    lo = fminf(lo, lane8_xchg<0x4e>(lo)) + 0.0f;  // no minus zero
+    hi = fmaxf(hi, lane8_xchg<0xb1>(hi));
+    hi = fmaxf(hi, lane8_xchg<0x4e>(hi));
+    constexpr float kFifteenth = 1.0f / 15.0f;
+    const float span = hi - lo, q = span * kFifteenth;
+    float steps = __builtin_fmaf(__builtin_fmaf(-15.0f, q, span), kFifteenth, q);
+    __asm__("" : "+v"(steps));  // rounded to fp32 before f16: not one instruction that rounds once
+    const uint32_t db = f2h_bits(steps), mb = f2h_bits(lo);
+    d = h2f(db), m = h2f(mb);
+    const float r = __builtin_amdgcn_rcpf(d);
+    inv = d > 0.0f ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : 0.0f;
+    dm = db | mb << 16;
   }
-  return w;
+
+  // 1.5 * 2^23 + code j: rounds to the nearest even and leaves the code in the low bits
+  __device__ __forceinline__ uint32_t code(int j) const {
+#pragma clang fp contract(off)
+    const float p = (v[j] - m) * inv;
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(p, 0.0f, 15.0f) + kMagic);
+  }
+};
+
+// Sums of kMagicBits << 4i over what a dword of codes joins, modulo 2^32.
+constexpr uint32_t magic_at(uint32_t step, int count) {
+  uint32_t s = 0;
+  for (int i = 0; i < count; ++i) s += kMagicBits << (step * i);
+  return s;
 }
 
 template <int KT, int VT>
@@ -65,26 +84,32 @@ __global__ __launch_bounds__(256) void kv_append_q4_kernel(AppendArgs a) {
 #pragma clang fp contract(off)
   const int lane = threadIdx.x & 63, groups = 64 / a.row_lanes;
   const int j = lane % a.row_lanes, group = lane / a.row_lanes;
-  const int units = (a.Hk + groups - 1) / groups, segs = (units + a.per_wave - 1) / a.per_wave;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const uint32_t units = (a.Hk + groups - 1) / groups, segs = (units + a.per_wave - 1) / a.per_wave;
+  const uint32_t item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = item / segs;
   if (t >= a.T) return;
-  const int64_t slot = a.slots[t];
+  const int64_t slot = scalar_int64(a.slots, t);
   if (slot < 0 || slot >= a.pages * a.page) return;
-  const int u0 = static_cast<int>(item % segs) * a.per_wave, u1 = min(units, u0 + a.per_wave);
+  const int u0 = static_cast<int>(item % segs) * a.per_wave, u1 = min(static_cast<int>(units), u0 + a.per_wave);
   const bool in_row = j < a.D / 8, turned = j < a.rot / 8;
   const int half = a.rot / 16, nb = a.D / 32, b = j >> 2, part = j & 3;
   const int tok = static_cast<int>(slot % kCellTokens);
+  const int64_t cell0 = kv_cell(slot, a.page, a.shift, 0, a.Hk, a.D), head_bytes = a.page / kCellTokens * (20 * a.D);
   float cos[8], sin[8];
   if (turned) {
-    const int64_t row = max(int64_t{0}, min(a.P - 1, static_cast<int64_t>(a.positions[t]))) * a.rot;
+    const int64_t row = max(int64_t{0}, min(a.P - 1, static_cast<int64_t>(as_scalar(a.positions)[t]))) * a.rot;
     if (a.interleaved) {
       const float4 c = load4(QMM_F32, a.rope, row / 4 + j), s = load4(QMM_F32, a.rope, (row + a.rot / 2) / 4 + j);
       cos[0] = c.x, cos[1] = c.y, cos[2] = c.z, cos[3] = c.w;
       sin[0] = s.x, sin[1] = s.y, sin[2] = s.z, sin[3] = s.w;
     } else {
-      load8(QMM_F32, a.rope, row / 8 + j % half, cos);
-      load8(QMM_F32, a.rope, (row + a.rot / 2) / 8 + j % half, sin);
+      const int k = j < half ? j : j - half;
+      load8(QMM_F32, a.rope, row / 8 + k, cos);
+      load8(QMM_F32, a.rope, (row + a.rot / 2) / 8 + k, sin);
+      if (j < half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sin[i] = -sin[i];  // of the other value of the pair
+      }
     }
   }
   for (int u = u0; u < u1; ++u) {
@@ -96,49 +121,52 @@ __global__ __launch_bounds__(256) void kv_append_q4_kernel(AppendArgs a) {
       key.load(a.x[0], (t * a.stride[0] + static_cast<int64_t>(h) * a.D) / 8 + j);
       val.load(a.x[1], (t * a.stride[1] + static_cast<int64_t>(h) * a.D) / 8 + j);
     }
-    float x[2][8];
+    Block8 k, v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[0][i] = on ? key.get(i) : 0.0f, x[1][i] = on ? val.get(i) : 0.0f;
+    for (int i = 0; i < 8; ++i) k.v[i] = on ? key.get(i) : 0.0f, v.v[i] = on ? val.get(i) : 0.0f;
     if (a.rot > 0) {
       if (a.interleaved) {
         if (turned) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = x[0][2 * i], q = x[0][2 * i + 1];
-            x[0][2 * i] = p * cos[i] - q * sin[i];
-            x[0][2 * i + 1] = q * cos[i] + p * sin[i];
+            const float p = k.v[2 * i], q = k.v[2 * i + 1];
+            k.v[2 * i] = p * cos[i] - q * sin[i];
+            k.v[2 * i + 1] = q * cos[i] + p * sin[i];
           }
         }
       } else {
         const int from = turned ? (j < half ? lane + half : lane - half) : lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float o = __shfl(x[0][i], from);
-          if (turned) {
-            const float c = x[0][i] * cos[i], s = o * sin[i];
-            x[0][i] = j < half ? c - s : c + s;
-          }
+          const float o = __shfl(k.v[i], from);
+          if (turned) k.v[i] = k.v[i] * cos[i] + o * sin[i];
         }
       }
     }
-    uint32_t kd, vd;
-    const uint32_t kc = q4_block_4lanes(x[0], kd), vc = q4_block_4lanes(x[1], vd);
-    // a byte of the values' codes joins dims c and c + 16 of a block: this lane's and those of the lane two further
-    const uint32_t other = static_cast<uint32_t>(lane8_xchg<0x4e>(static_cast<int>(vc)));
-    if (!on) continue;
-    uint8_t* cell = a.cache + kv_cell(slot, a.page, h, a.Hk, a.D);
-    *reinterpret_cast<uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4) = key_dword(kc);
-    const uint32_t low = part < 2 ? vc : other >> 16, high = part < 2 ? other : vc >> 16;
-    const int quad = tok >> 2, c0 = (part & 1) * 8 + (part >> 1) * 4;
+    k.scales();
+    v.scales();
+    // The key's codes 0, 2, 4, 6, 1, 3, 5, 7 from the low end on.  The value's in bytes, 0 to 3 and 4 to 7: a byte of the
+    // cache joins dims c and c + 16 of a block, so this lane's and those of the lane two further, half of them each.
+    uint32_t kc = 0, v03 = 0, v47 = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      cell[10 * a.D + ((quad * 16 + c0 + i) * nb + b) * 4 + kv_quad_byte(tok & 3)] =
-          static_cast<uint8_t>(((low >> (4 * i)) & 15u) | ((high >> (4 * i)) & 15u) << 4);
+    for (int i = 0; i < 8; ++i) kc += k.code(i) << (4 * ((i & 1) * 4 + (i >> 1)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v03 += v.code(i) << (8 * i), v47 += v.code(4 + i) << (8 * i);
+    kc -= magic_at(4, 8), v03 -= magic_at(8, 4), v47 -= magic_at(8, 4);
+    const uint32_t other = static_cast<uint32_t>(lane8_xchg<0x4e>(static_cast<int>(part < 2 ? v47 : v03)));
+    const uint32_t vc = part < 2 ? v03 | other << 4 : other | v47 << 4;
+    if (!on) continue;
+    uint8_t* cell = a.cache + cell0 + h * head_bytes;
+    *reinterpret_cast<uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4) = kc;
+    const int quad = tok >> 2, c0 = (part & 1) * 8 + (part >> 1) * 4;
+    uint8_t* to = cell + 10 * a.D + ((quad * 16 + c0) * nb + b) * 4 + kv_quad_byte(tok & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i * nb * 4] = static_cast<uint8_t>(vc >> (8 * i));
     if (part == 0) {
-      *reinterpret_cast<uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4) = kd;
+      *reinterpret_cast<uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4) = k.dm;
       uint16_t* vs = reinterpret_cast<uint16_t*>(cell + 18 * a.D + (quad * nb + b) * 16) + (tok & 3);
-      vs[0] = static_cast<uint16_t>(vd);
-      vs[4] = static_cast<uint16_t>(vd >> 16);
+      vs[0] = static_cast<uint16_t>(v.dm);
+      vs[4] = static_cast<uint16_t>(v.dm >> 16);
     }
   }
 }
@@ -148,52 +176,76 @@ struct ReadArgs {
   const int64_t* slots;
   void* y[2];
   int64_t pages, page, T;
-  int Hk, D, row_lanes;
+  int Hk, D, row_lanes, per_wave, shift;
 };
 
-// n * d + m as the f16 that it stands for, widened
-__device__ __forceinline__ float q4_value(uint32_t n, uint32_t d, uint32_t m) {
-  const _Float16 dh = __builtin_bit_cast(_Float16, static_cast<uint16_t>(d));
-  const _Float16 mh = __builtin_bit_cast(_Float16, static_cast<uint16_t>(m));
-  return static_cast<float>(__builtin_fmaf16(static_cast<_Float16>(static_cast<float>(n)), dh, mh));
+// Eight f16 numbers as values of a type.
+template <int TY>
+__device__ __forceinline__ void store_f16(void* p, int64_t i, const h2 (&x)[4]) {
+  if constexpr (TY == QMM_F16) {
+    static_cast<uint4*>(p)[i] = make_uint4(__builtin_bit_cast(uint32_t, x[0]), __builtin_bit_cast(uint32_t, x[1]),
+                                           __builtin_bit_cast(uint32_t, x[2]), __builtin_bit_cast(uint32_t, x[3]));
+  } else {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = static_cast<float>(x[k >> 1][k & 1]);
+    Raw8<TY> o;
+    o.set(f);
+    o.store(p, i);
+  }
 }
 
 template <int TY>
 __global__ __launch_bounds__(256) void kv_read_q4_kernel(ReadArgs a) {
   const int lane = threadIdx.x & 63, groups = 64 / a.row_lanes;
   const int j = lane % a.row_lanes, group = lane / a.row_lanes;
-  const int units = (a.Hk + groups - 1) / groups;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t t = item / units;
-  const int h = static_cast<int>(item % units) * groups + group;
-  if (t >= a.T || j >= a.D / 8 || h >= a.Hk) return;
-  const int64_t slot = a.slots[t];
+  const uint32_t units = (a.Hk + groups - 1) / groups, segs = (units + a.per_wave - 1) / a.per_wave;
+  const uint32_t item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = item / segs;
+  if (t >= a.T) return;
+  const int64_t slot = scalar_int64(a.slots, t);
+  const bool there = slot >= 0 && slot < a.pages * a.page;
+  const int u0 = static_cast<int>(item % segs) * a.per_wave, u1 = min(static_cast<int>(units), u0 + a.per_wave);
   const int nb = a.D / 32, b = j >> 2, part = j & 3, tok = static_cast<int>(slot & (kCellTokens - 1)), quad = tok >> 2;
-  float k[8] = {}, v[8] = {};
-  if (slot >= 0 && slot < a.pages * a.page) {
-    const uint8_t* cell = a.cache + kv_cell(slot, a.page, h, a.Hk, a.D);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4);
-    const uint32_t dm = *reinterpret_cast<const uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4);
+  const int c0 = (part & 1) * 8 + (part >> 1) * 4;
+  const int64_t cell0 = there ? kv_cell(slot, a.page, a.shift, 0, a.Hk, a.D) : 0;
+  const int64_t head_bytes = a.page / kCellTokens * (20 * a.D);
+  for (int u = u0; u < u1; ++u) {
+    const int h = u * groups + group;
+    const bool on = j < a.D / 8 && h < a.Hk;
+    uint32_t kw = 0, kd = 0, vw = 0, d = 0, m = 0;
+    if (there && on) {
+      const uint8_t* cell = a.cache + cell0 + h * head_bytes;
+      kw = *reinterpret_cast<const uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4);
+      kd = *reinterpret_cast<const uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4);
+      const uint8_t* from = cell + 10 * a.D + ((quad * 16 + c0) * nb + b) * 4 + kv_quad_byte(tok & 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = (i & 1) * 4 + (i >> 1);
-      k[n] = q4_value((w >> (8 * i)) & 15u, dm, dm >> 16);
-      k[n + 2] = q4_value((w >> (8 * i + 4)) & 15u, dm, dm >> 16);
+      for (int i = 0; i < 4; ++i) vw |= static_cast<uint32_t>(from[i * nb * 4]) << (8 * i);
+      const uint8_t* vs = cell + 18 * a.D + (quad * nb + b) * 16 + (tok & 3) * 2;
+      d = ld_u16(vs), m = ld_u16(vs + 8);
     }
-    const uint16_t* vs = reinterpret_cast<const uint16_t*>(cell + 18 * a.D + (quad * nb + b) * 16) + (tok & 3);
-    const uint32_t d = vs[0], m = vs[4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t byte = cell[10 * a.D + ((quad * 16 + (part & 1) * 8 + i) * nb + b) * 4 + kv_quad_byte(tok & 3)];
-      v[i] = q4_value(part < 2 ? byte & 15u : byte >> 4, d, m);
-    }
+    // bytes of dims c and c + 16: this lane keeps its own dims' codes and takes the rest from the lane two further
+    const uint32_t low = vw & 0x0f0f0f0fu, high = (vw >> 4) & 0x0f0f0f0fu;
+    const uint32_t other = static_cast<uint32_t>(lane8_xchg<0x4e>(static_cast<int>(part < 2 ? high : low)));
+    if (!on) continue;
+    const uint32_t v03 = part < 2 ? low : other, v47 = part < 2 ? other : high;
+    // bytes of kw: codes 0 and 2, 4 and 6, 1 and 3, 5 and 7
+    const uint32_t k0415 = kw & 0x0f0f0f0fu, k2637 = (kw >> 4) & 0x0f0f0f0fu;
+    const uint32_t k0123 = __builtin_amdgcn_perm(k2637, k0415, 0x06040200u), k4567 = __builtin_amdgcn_perm(k2637, k0415, 0x07050301u);
+    const auto values = [](uint32_t a03, uint32_t a47, uint32_t d16, uint32_t m16, h2 (&x)[4]) {
+      const h2 dd = as_h2(d16 | d16 << 16), mm = as_h2(m16 | m16 << 16);
+      x[0] = __builtin_elementwise_fma(codes_to_f16<false>(a03), dd, mm);
+      x[1] = __builtin_elementwise_fma(codes_to_f16<true>(a03), dd, mm);
+      x[2] = __builtin_elementwise_fma(codes_to_f16<false>(a47), dd, mm);
+      x[3] = __builtin_elementwise_fma(codes_to_f16<true>(a47), dd, mm);
+    };
+    const int64_t at = (t * a.Hk + h) * (a.D / 8) + j;
+    h2 x[4];
+    values(k0123, k4567, kd & 0xffffu, kd >> 16, x);
+    store_f16<TY>(a.y[0], at, x);
+    values(v03, v47, d, m, x);
+    store_f16<TY>(a.y[1], at, x);
   }
-  const int64_t at = (t * a.Hk + h) * (a.D / 8) + j;
-  Raw8<TY> o;
-  o.set(k);
-  o.store(a.y[0], at);
-  o.set(v);
-  o.store(a.y[1], at);
 }
 
 template <int KT>
@@ -201,6 +253,11 @@ static void launch_append(const AppendArgs& a, int v_type, dim3 g, hipStream_t s
   if (v_type == QMM_F32) hipLaunchKernelGGL((kv_append_q4_kernel<KT, QMM_F32>), g, dim3(256), 0, st, a);
   else if (v_type == QMM_F16) hipLaunchKernelGGL((kv_append_q4_kernel<KT, QMM_F16>), g, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((kv_append_q4_kernel<KT, QMM_BF16>), g, dim3(256), 0, st, a);
+}
+
+// Of a token's units, each as many heads as a wave holds: all where there are tokens enough to fill the chip with waves.
+static int units_per_wave(int64_t T, int64_t units) {
+  return static_cast<int>(std::max<int64_t>(1, std::min(units, T * units / 8192)));
 }
 
 static int row_lanes_of(int64_t D) { return D == 64 ? 8 : D <= 128 ? 16 : 32; }
@@ -224,9 +281,10 @@ extern "C" int kv_append_q4(const void* k, int64_t k_stride, int k_type, const v
     return QMM_ERR_ALIGN;
   const int lanes = row_lanes_of(D), groups = 64 / lanes;
   const int64_t units = (Hk + groups - 1) / groups;
-  const int per = static_cast<int>(std::max<int64_t>(1, std::min(units, T * units / 16384)));
+  const int per = units_per_wave(T, units);
   const AppendArgs a{{k, v}, {k_stride, v_stride}, rope, positions, slots, static_cast<uint8_t*>(cache), P, pages, page,
-                     T, static_cast<int>(Hk), static_cast<int>(D), static_cast<int>(rot), lanes, per, interleaved != 0};
+                     T, static_cast<int>(Hk), static_cast<int>(D), static_cast<int>(rot), lanes, per, page_shift(page),
+                     interleaved != 0};
   const dim3 g(static_cast<unsigned>((T * ((units + per - 1) / per) + 3) / 4));
   hipStream_t st = to_stream(stream);
   if (k_type == QMM_F32) launch_append<QMM_F32>(a, v_type, g, st);
@@ -243,9 +301,11 @@ extern "C" int kv_read_q4(const void* cache, int64_t pages, int64_t page, const 
   if (!cache || !slots || !k || !v) return QMM_ERR_NULL;
   if (!aligned16(cache) || !aligned16(slots) || !aligned16(k) || !aligned16(v)) return QMM_ERR_ALIGN;
   const int lanes = row_lanes_of(D), groups = 64 / lanes;
+  const int64_t units = (Hk + groups - 1) / groups;
+  const int per = units_per_wave(T, units);
   const ReadArgs a{static_cast<const uint8_t*>(cache), slots, {k, v}, pages, page, T, static_cast<int>(Hk),
-                   static_cast<int>(D), lanes};
-  const dim3 g(static_cast<unsigned>((T * ((Hk + groups - 1) / groups) + 3) / 4)), blk(256);
+                   static_cast<int>(D), lanes, per, page_shift(page)};
+  const dim3 g(static_cast<unsigned>((T * ((units + per - 1) / per) + 3) / 4)), blk(256);
   hipStream_t st = to_stream(stream);
   if (type == QMM_F32) hipLaunchKernelGGL(kv_read_q4_kernel<QMM_F32>, g, blk, 0, st, a);
   else if (type == QMM_F16) hipLaunchKernelGGL(kv_read_q4_kernel<QMM_F16>, g, blk, 0, st, a);

@@ -12,10 +12,17 @@ inline bool kv_q4_shape(int64_t pages, int64_t page, int64_t Hk, int64_t D) {
          pages >= 1 && pages <= 0x7fffffff;
 }
 
-// First byte of the cell that holds a slot's token for head h.
-__device__ __forceinline__ int64_t kv_cell(int64_t slot, int64_t page, int h, int Hk, int D) {
-  const int64_t p = slot / page;
-  return ((p * Hk + h) * (page / kCellTokens) + (slot - p * page) / kCellTokens) * (20 * D);
+// First byte of the cell that holds a slot's token for head h.  `shift`: the page size is 2^shift, or -1.
+__device__ __forceinline__ int64_t kv_cell(int64_t slot, int64_t page, int shift, int h, int Hk, int D) {
+  const int64_t p = shift >= 0 ? slot >> shift
+                    : slot < (int64_t{1} << 32) ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(page) : slot / page;
+  const int cells = static_cast<int>(page) / kCellTokens, cell = static_cast<int>(slot - p * page) / kCellTokens;
+  return ((p * Hk + h) * cells + cell) * (20 * D);
+}
+inline int page_shift(int64_t page) {
+  int s = 0;
+  while ((int64_t{1} << s) < page) ++s;
+  return (int64_t{1} << s) == page ? s : -1;
 }
 
 // Memory that nothing writes while the kernel runs, read at addresses that are
@@ -23,6 +30,22 @@ __device__ __forceinline__ int64_t kv_cell(int64_t slot, int64_t page, int h, in
 typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
 __device__ __forceinline__ scalar_ints as_scalar(const int32_t* p) {
   return reinterpret_cast<scalar_ints>(reinterpret_cast<uintptr_t>(p));
+}
+
+__device__ __forceinline__ int64_t scalar_int64(const int64_t* p, int64_t i) {
+  const scalar_ints q = as_scalar(reinterpret_cast<const int32_t*>(p + i));
+  return static_cast<int64_t>(q[1]) << 32 | static_cast<uint32_t>(q[0]);
+}
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
+
+// Bytes 0 and 1 (or 2 and 3) of v, each 0..15, as f16 numbers.  A byte n read as
+// an 8-bit float with three bits of fraction is n * 2^-9, below 8 a subnormal
+// one; the conversion of two multiplies by 2^9.
+template <bool UPPER>
+__device__ __forceinline__ h2 codes_to_f16(uint32_t v) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.0f, UPPER);
 }
 
 // Where byte i of a quad's four value codes stands: tokens 0, 2, 1, 3.

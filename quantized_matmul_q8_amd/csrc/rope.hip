@@ -57,10 +57,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   const int lane = threadIdx.x & 63, groups = 64 / a.row_lanes;
   const int p = lane % a.row_lanes, group = lane / a.row_lanes;
   const int units = a.units[0] + a.units[1], segs = (units + a.per_wave - 1) / a.per_wave;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t t = item / segs;
+  const uint32_t item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = item / static_cast<uint32_t>(segs);
   if (t >= a.T) return;
-  const int u0 = static_cast<int>(item % segs) * a.per_wave, u1 = min(units, u0 + a.per_wave);
+  const int u0 = static_cast<int>(item % static_cast<uint32_t>(segs)) * a.per_wave, u1 = min(units, u0 + a.per_wave);
   const bool in_head = p < a.D / 16, turned = p < a.rot / 16, halves = turned && !a.interleaved;
   const int ca = halves ? p : 2 * p, cb = halves ? p + a.rot / 16 : 2 * p + 1;
   float cos[8], sin[8];
@@ -152,11 +152,11 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
                             int64_t T, int64_t Hq, int64_t Hk, int64_t D, void* stream) {
   if (!known_type(type) || !known_type(out_type) || ((q_weight || k_weight) && !known_type(w_type)))
     return QMM_ERR_UNSUPPORTED;
-  if (T < 0 || T > 0x7fffffff || Hq < 1 || Hq > 1024 || D < 32 || D > 512 || D % 32 != 0) return QMM_ERR_SHAPE;
+  if (Hq < 1 || Hq > 1024 || (k && (Hk < 1 || Hk > 1024)) || T < 0 || T > 0x7fffffff / (Hq + (k ? Hk : 0)) || D < 32 || D > 512 || D % 32 != 0) return QMM_ERR_SHAPE;
   if (rot < 0 || rot % 16 != 0 || rot > D || (rot > 0 && (P < 1 || P > 0x7fffffff))) return QMM_ERR_SHAPE;
   if (!(eps >= 0.0f)) return QMM_ERR_SHAPE;
   if (!strided_rows(q_stride, Hq, D) || !strided_rows(q_out_stride, Hq, D)) return QMM_ERR_SHAPE;
-  if (k && (Hk < 1 || Hk > 1024 || !strided_rows(k_stride, Hk, D) || !strided_rows(k_out_stride, Hk, D)))
+  if (k && (!strided_rows(k_stride, Hk, D) || !strided_rows(k_out_stride, Hk, D)))
     return QMM_ERR_SHAPE;
   if (T == 0) return QMM_OK;
   if (!q || !q_out || (k && !k_out) || (rot > 0 && (!rope || !positions))) return QMM_ERR_NULL;
@@ -172,9 +172,8 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   for (int s = 0; s < 2; ++s) a.units[s] = (a.heads[s] + groups - 1) / groups;
   const int64_t units = a.units[0] + a.units[1];
   a.per_wave = static_cast<int>(std::max<int64_t>(1, std::min(units, T * units / 16384)));
-  const int64_t waves = T * ((units + a.per_wave - 1) / a.per_wave), grid = (waves + 3) / 4;
-  if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
-  const dim3 g(static_cast<unsigned>(grid));
+  const int64_t waves = T * ((units + a.per_wave - 1) / a.per_wave);
+  const dim3 g(static_cast<unsigned>((waves + 3) / 4));
   hipStream_t st = to_stream(stream);
   if (type == QMM_F32) launch_rope<QMM_F32>(a, out_type, g, st);
   else if (type == QMM_F16) launch_rope<QMM_F16>(a, out_type, g, st);

@@ -107,6 +107,30 @@ def test_edge_blocks():
     check(1, 2, D, 16, rot=0, kv=(z, -z))
 
 
+def test_every_scale():
+    """Each positive f16 as d, with values at and beside every half step: the reciprocal's last bit decides there."""
+    d = np.arange(1, np.float16(2180).view(np.uint16) + 1, dtype=np.uint16).view(np.float16).astype(np.float32)
+    d = np.resize(d, (len(d) + 3) // 4 * 4).reshape(-1, 4, 1)
+    n = np.float32(0.5) + np.arange(15, dtype=np.float32)
+    x = np.concatenate((0 * d, 15 * d, n * d, np.nextafter(n * d, np.float32(0))), 2)       # 15 d has at most 15 bits
+    k, v = (dev(np.ascontiguousarray(x[:, i:i + 2].reshape(-1, 1, 64))) for i in (0, 2))
+    check(len(x), 1, 64, 64, rot=0, kv=(k, v))
+
+
+def test_spans_between_two_scales():
+    """Spans whose fifteenth part lies at, just below and just above the middle of two f16 numbers."""
+    f = np.arange(0, np.float16(2180).view(np.uint16), dtype=np.uint16)
+    mid = (f.view(np.float16).astype(np.float64) + (f + 1).view(np.float16).astype(np.float64)) / 2 * 15
+    mid = np.resize(mid, (len(mid) + 1) // 2 * 2).astype(np.float32)
+    spans = np.stack((np.nextafter(mid, np.float32(0)), mid, np.nextafter(mid, np.float32(1e9))), 1).reshape(-1, 6)
+    x = np.zeros((len(spans), 6, 32), np.float32)
+    x[:, :, 5], x[:, :, 9] = spans, spans / 3
+    k, v = (dev(x[:, i:i + 2].reshape(-1, 1, 64)) for i in (0, 2))
+    check(len(x), 1, 64, 64, rot=0, kv=(k, v))
+    k, v = (dev(x[:, i:i + 2].reshape(-1, 1, 64)) for i in (4, 1))
+    check(len(x), 1, 64, 64, rot=0, kv=(k, v))
+
+
 def test_ties_go_to_even_codes():
     # steps of exactly 1, 0 and 15 in the block: every half is a tie
     x = (torch.arange(32, device=DEV) / 2.0).clamp(max=15.0).repeat(1, 2, 2)
