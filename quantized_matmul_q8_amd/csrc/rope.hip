@@ -23,7 +23,7 @@ struct RopeArgs {
   const int32_t* positions;
   int64_t T, P;
   int D, rot, row_lanes, w_type, per_wave;
-  bool interleaved;
+  bool interleaved, large;
   float offset, eps;
 };
 
@@ -127,9 +127,11 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
       for (int j = 0; j < 8; ++j) lo[j] = v[j], hi[j] = v[8 + j];
       Raw8<YT> o;
       o.set(lo);
-      o.store(a.y[side], at + ca);
+      if (a.large) o.store_nt(a.y[side], at + ca);
+      else o.store(a.y[side], at + ca);
       o.set(hi);
-      o.store(a.y[side], at + cb);
+      if (a.large) o.store_nt(a.y[side], at + cb);
+      else o.store(a.y[side], at + cb);
     }
   }
 }
@@ -168,7 +170,8 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   const int groups = 64 / lanes;
   RopeArgs a{{q, k}, {q_weight, k_weight}, {q_out, k_out}, {q_stride, k_stride}, {q_out_stride, k_out_stride},
              {static_cast<int>(Hq), k ? static_cast<int>(Hk) : 0}, {0, 0}, rope, positions, T, P, static_cast<int>(D),
-             static_cast<int>(rot), lanes, w_type, 1, interleaved != 0, weight_offset, eps};
+             static_cast<int>(rot), lanes, w_type, 1, interleaved != 0,
+             large_output(T * (Hq + (k ? Hk : 0)) * D, out_type), weight_offset, eps};
   for (int s = 0; s < 2; ++s) a.units[s] = (a.heads[s] + groups - 1) / groups;
   const int64_t units = a.units[0] + a.units[1];
   a.per_wave = static_cast<int>(std::max<int64_t>(1, std::min(units, T * units / 16384)));

@@ -16,6 +16,12 @@ inline bool known_type(int t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
 
+// Outputs larger than half of the last-level cache (256 MB) are stored past the
+// caches: nothing finds all of them there.  65536 x 8 x 128 cached tokens read
+// back to bf16, 268 MB: 60 us, with stores through the caches 91; a smaller one
+// the next kernel finds.
+inline bool large_output(int64_t values, int type) { return values * (type == QMM_F32 ? 4 : 2) >= (int64_t{128} << 20); }
+
 // Storage of a type code and of four of its values.
 template <int TY> struct Typed;
 template <> struct Typed<QMM_F32> { using one = float; using four = float4; };
