@@ -268,7 +268,7 @@ static void launch_append(const AppendArgs& a, int v_type, dim3 g, hipStream_t s
 // Workgroups, and the heads of each: all of a token's where there are tokens enough to fill the chip, else fewer.
 static dim3 kv_grid(int64_t T, int64_t Hk, int lanes, int& heads) {
   const int64_t blocks = (T + 256 / lanes - 1) / (256 / lanes);
-  heads = static_cast<int>(std::max<int64_t>(1, std::min(Hk, blocks * Hk / 4096)));
+  heads = static_cast<int>(std::max<int64_t>(1, std::min(Hk, blocks * Hk / 1024)));
   return dim3(static_cast<unsigned>(blocks * ((Hk + heads - 1) / heads)));
 }
 
