@@ -8,6 +8,10 @@ namespace qmm {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// No sequence is longer.  A window that is wider sees the same and is cut to
+// this, so that the places of keys, less a window, stay in 32 bits.
+constexpr int64_t kMostTokens = int64_t{1} << 30;
+
 inline bool attn_head_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 // Over lanes l and l ^ 32, in both: one exchange of the wave's halves.

@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     }
     mul = mul == 0.0f ? 1.0f : mul;
   }
-  const float slack = kSlack / mul;
+  const float slack = fminf(kSlack / mul, 3.0e38f);  // finite: -inf, the first maximum, plus it stays -inf
 
   // the bounds of the wave's rows and of the workgroup's, the same for all lanes
   const bool active = row0 < rows;
@@ -564,9 +564,8 @@ static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int
 }
 
 static bool prompt_shape(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
-  constexpr int64_t kMost = int64_t{1} << 30;
-  return B >= 0 && Tq >= 0 && Tk >= 0 && Tq < kMost && Tk < kMost && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
-         attn_head_dim(D) && Tq < kMost / Hq && B < kMost / Hq;
+  return B >= 0 && Tq >= 0 && Tk >= 0 && Tq < kMostTokens && Tk < kMostTokens && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
+         attn_head_dim(D) && Tq < kMostTokens / Hq && B < kMostTokens / Hq;
 }
 
 template <int D, int BN>
@@ -605,7 +604,7 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
   const int64_t grid = p.tiles * Hk * p.splits;
   if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const PromptArgs a{q, k, v, cu_q, cu_k, y, static_cast<float*>(ws), q_stride, k_stride, v_stride, scale,
-                     static_cast<int>(window), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(B),
+                     static_cast<int>(std::min(window, kMostTokens)), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(B),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk), static_cast<int>(p.splits),
                      static_cast<int>(p.tiles), y_type, causal != 0};
   const dim3 g(static_cast<unsigned>(grid));

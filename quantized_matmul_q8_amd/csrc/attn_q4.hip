@@ -608,7 +608,7 @@ static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, hipStream_t
 
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   return B >= 0 && n >= 1 && n <= QMM_ATTN_MAX_N && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
-         attn_head_dim(D) && max_len >= 1 && max_len <= (int64_t{1} << 30) && B < (int64_t{1} << 26) / (n * Hq) &&
+         attn_head_dim(D) && max_len >= 1 && max_len <= kMostTokens && B < (int64_t{1} << 26) / (n * Hq) &&
          B * ((max_len + kStep - 1) / kStep + 1) < (int64_t{1} << 31);
 }
 
@@ -627,7 +627,7 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
                        int y_type, int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, void* ws, size_t ws_bytes,
                        void* stream) {
   if ((type != QMM_F16 && type != QMM_BF16) || !known_type(y_type)) return QMM_ERR_UNSUPPORTED;
-  if (!kv_q4_shape(pages, page, Hk, D) || W < 1 || W > (int64_t{1} << 30) / page) return QMM_ERR_SHAPE;
+  if (!kv_q4_shape(pages, page, Hk, D) || W < 1 || W > kMostTokens / page) return QMM_ERR_SHAPE;
   if (!attn_q4_shape(B, n, Hq, Hk, D, W * page) || !strided_rows(q_stride, Hq, D)) return QMM_ERR_SHAPE;
   if (!isfinite(scale) || window < 0 || window > 0x7fffffff) return QMM_ERR_SHAPE;
   if (B == 0) return QMM_OK;
@@ -641,7 +641,7 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
   uint32_t shift = 31;
   while ((int64_t{1} << (shift - 31)) < cells) ++shift;
   const AttnQ4Args a{q, static_cast<const uint8_t*>(cache), table, lens, y, static_cast<float*>(ws), q_stride, pages, W,
-                     W * page, scale, static_cast<int>(window), static_cast<int>(B), static_cast<int>(n),
+                     W * page, scale, static_cast<int>(std::min(window, kMostTokens)), static_cast<int>(B), static_cast<int>(n),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk),
                      static_cast<int>(n * (Hq / Hk)), p.row_blocks, 16 * p.tiles, cells,
                      static_cast<int>(p.slots), p.groups, p.parts, p.least,

@@ -101,6 +101,108 @@ def test_rows_that_see_nothing():
     assert not qmm.attn_prompt(q, none, none, cu([4]), cu([0])).any()
 
 
+# few rows and many keys: the keys of a tile are split and joined
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("xt", [F16, BF16])
+def test_split_keys(D, xt):
+    check([40], [1700], Hq=4, Hk=2, D=D, xt=xt, seed=D)
+    check([40], [1700], Hq=4, Hk=1, D=D, xt=xt, causal=False, seed=D + 1)
+    check([1], [2100], Hq=6, Hk=2, D=D, xt=xt, seed=D + 2)
+    check([150], [1030], Hq=2, Hk=2, D=D, xt=xt, yt=F32, window=200, seed=D + 3)      # most splits see nothing
+
+
+def test_split_keys_of_packed_sequences():
+    check([30, 1, 0, 50, 7], [1500, 700, 900, 2000, 0], Hq=4, Hk=2, D=128, seed=22)
+    check([30, 1, 0, 50, 7], [0, 700, 900, 20, 3000], Hq=2, Hk=1, D=64, xt=F16, causal=False, seed=23)
+    check([200, 3, 90], [100, 1500, 900], Hq=2, Hk=1, D=64, window=77, seed=24)       # some rows see nothing
+    check([300, 300], [1100, 1], Hq=1, Hk=1, D=192, xt=F16, seed=25)
+
+
+def test_split_rows_that_see_nothing():
+    q, k, v = inputs([700], [2000], 1, 1, 64, F16, 26)
+    for ends in ((600, 600, 1500), (700, 0, 2000)):
+        y = qmm.attn_prompt(q, k, v, cu([ends[0], 700 - ends[0]]), cu([ends[1], ends[2] - ends[1]]))
+        compare(y, q, k, v, [ends[0], 700 - ends[0]], [ends[1], ends[2] - ends[1]], True, 0, 0.125, F16)
+    assert not qmm.attn_prompt(q, k, v, cu([700]), cu([0])).any()
+
+
+@pytest.mark.parametrize("D,xt", [(64, BF16), (128, F16), (256, BF16)])
+def test_split_keys_that_are_not_seen_have_no_influence(D, xt):
+    n, L = 20, 1300
+    q, k, v = inputs([n], [L], 4, 2, D, xt, 27)
+    nan, inf = float("nan"), float("inf")
+    for window in (0, 300):
+        clean = qmm.attn_prompt(q, k, v, cu([n]), cu([L]), window=window)
+        for cut in (L - n, L - 7, L - 1):
+            k2, v2 = k.clone(), v.clone()
+            k2[cut + 1:, :, ::3], v2[cut + 1:, :, 1::2] = nan, inf
+            y = qmm.attn_prompt(q, k2, v2, cu([n]), cu([L]), window=window)
+            assert torch.equal(y[:cut + 1 - (L - n)], clean[:cut + 1 - (L - n)]), (window, cut)
+            if window:
+                k2[:L - n - window + 1], v2[:L - n - window + 1] = inf, nan
+                y = qmm.attn_prompt(q, k2, v2, cu([n]), cu([L]), window=window)
+                assert torch.equal(y[:cut + 1 - (L - n)], clean[:cut + 1 - (L - n)]), (window, cut)
+    # what is seen shows
+    v2 = v.clone()
+    v2[5, 0, 3], v2[900, 1, 7] = inf, nan
+    clean, y = qmm.attn_prompt(q, k, v, cu([n]), cu([L])), qmm.attn_prompt(q, k, v2, cu([n]), cu([L]))
+    assert torch.isnan(y[:, 2:, 7]).all() and not torch.isfinite(y[:, :2, 3]).any()
+    y[:, :2, 3], y[:, 2:, 7] = clean[:, :2, 3], clean[:, 2:, 7]
+    assert torch.equal(y, clean)
+
+
+def test_split_rows_outside_workspace_and_replays():
+    nq, nk, Hq, Hk, D = [40, 25], [1400, 700], 4, 2, 128
+    q, k, v = inputs([100], [2200], Hq, Hk, D, BF16, 28)
+    cq, ck = cu(nq, 10), cu(nk, 30)
+    need = qmm.attn_prompt_workspace_bytes(2, 100, 2200, Hq, Hk, D)
+    assert need > 0
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full((101, Hq, D), 7.0, dtype=BF16, device=DEV)
+    qmm.attn_prompt(q, k, v, cq, ck, out=out[:100], ws=ws[:-64])
+    compare(out, q, k, v, nq, nk, True, 0, D**-0.5, BF16, 10, 30)
+    assert torch.all(out[:10] == 7) and torch.all(out[75:] == 7) and torch.all(ws[-64:] == 0xFF)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qmm.attn_prompt(q, k, v, cq, ck, out=out[:100], ws=ws[:-64])
+    for r in range(4):
+        # other bounds of the sequences between replays
+        nq, nk = [[40, 25], [0, 90], [60, 1], [33, 33]][r], [[1400, 700], [10, 2100], [2000, 0], [60, 1800]][r]
+        cq.copy_(cu(nq, 10))
+        ck.copy_(cu(nk, 30))
+        out.fill_(7)
+        ws[:-64] = 0xFF
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, q, k, v, nq, nk, True, 0, D**-0.5, BF16, 10, 30)
+        assert torch.all(out[:10] == 7) and torch.all(out[10 + sum(nq):] == 7) and torch.all(ws[-64:] == 0xFF)
+
+
+def test_scales_next_to_zero():
+    # terms of all keys alike, whether the keys are split or not: the scale's products vanish
+    for nq, nk in (([70], [70]), ([20], [1500])):
+        for scale in (1e-38, -1e-42, 2.0**-149):
+            check(nq, nk, Hq=2, Hk=1, D=64, scale=scale, seed=29)
+            check(nq, nk, Hq=2, Hk=1, D=64, xt=F16, scale=scale, seed=30)
+
+
+def test_widest_windows_see_all():
+    for window in (2**30 - 1, 2**30, 2**31 - 1):
+        check([150], [40], Hq=2, Hk=1, D=64, window=window, seed=31)
+        check([3, 40], [700, 1500], Hq=2, Hk=1, D=64, window=window, seed=32)
+
+
+def test_rows_far_apart():
+    # strides that take the offsets past 32 bits
+    stride, n = (1 << 24) - 8, 140
+    q, k, v = inputs([n], [n], 4, 2, 64, BF16, 33)
+    wide = torch.zeros((n, stride), dtype=BF16, device=DEV)
+    wide[:, 8:264], wide[:, 4096:4224], wide[:, stride - 128:] = q.reshape(n, 256), k.reshape(n, 128), v.reshape(n, 128)
+    far = (wide[:, 8:264].view(n, 4, 64), wide[:, 4096:4224].view(n, 2, 64), wide[:, stride - 128:].view(n, 2, 64))
+    assert torch.equal(qmm.attn_prompt(*far, cu([60, 80])), qmm.attn_prompt(q, k, v, cu([60, 80])))
+
+
 def test_long_prompts():
     check([1100], Hq=2, Hk=1, D=128, seed=10)
     check([700, 333], Hq=2, Hk=2, D=64, xt=F16, seed=11)

@@ -117,6 +117,87 @@ def test_long_sequences(n):
     check([6000, 1], n, 4, 2, 64, 16, window=4500, seed=32 + n)
 
 
+def ragged(B, longest, seed):
+    """Lengths of a batch: mostly short ones, empty ones, single tokens, and the longest somewhere inside."""
+    g = qmm_synth.rng(seed)
+    lens = [int(x) for x in g.integers(0, 200, B)]
+    lens[1], lens[B // 3], lens[B // 2], lens[-1] = 1, longest, 0, 0
+    return lens
+
+
+# many sequences whose table allows long ones: equal runs of all sequences' steps, a run over several sequences
+@pytest.mark.parametrize("n,Hq,Hk,D,B", [(1, 8, 4, 128, 64), (3, 8, 4, 64, 66), (8, 32, 2, 128, 66), (8, 8, 2, 96, 128),
+                                         (2, 4, 2, 256, 130), (8, 10, 1, 192, 100), (1, 1, 1, 64, 300)])
+def test_runs_over_many_sequences(n, Hq, Hk, D, B):
+    check(ragged(B, 1500, n + B), n, Hq, Hk, D, 16, seed=B + D)
+    check(ragged(B, 1100, n + B + 1), n, Hq, Hk, D, 32, BF16, window=150, seed=B + D + 1)
+
+
+def test_runs_of_equal_and_of_single_sequences():
+    check([1030] * 64, 1, 4, 4, 64, seed=40)
+    check([0] * 40 + [4000] + [0] * 23, 2, 8, 4, 128, 16, seed=41)   # one sequence over many runs
+    check([0] * 63 + [1025], 1, 4, 4, 64, 16, window=3, seed=42)
+    check([1] * 63 + [1025], 8, 4, 4, 64, 16, BF16, window=1, seed=43)
+
+
+def test_runs_where_no_sequence_is_left():
+    cache, table, kv, q = setup([1100] * 64, 1, 4, 4, 64, 16, F16, 44)
+    for x in (0, -5):
+        assert not qmm.attn_q4(q, cache, dev(table), torch.full((64,), x, dtype=torch.int32, device=DEV)).any()
+
+
+# few sequences: equal parts, with every number of tiles of rows
+@pytest.mark.parametrize("n,Hq", [(8, 32), (8, 16), (4, 20), (5, 7), (2, 9)])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+def test_parts_of_many_rows(n, Hq, D):
+    check([1700, 9, 0, 600], n, Hq, 1, D, seed=Hq + D)
+    check([1500, 40], n, Hq, 1, D, 32, BF16, window=333, seed=Hq + D + 1)
+
+
+@pytest.mark.parametrize("n", [1, 8])
+def test_widest_windows_see_all(n):
+    for window in (2**30 - 1, 2**30, 2**31 - 1):
+        check([1, 5, 200], n, 4, 2, 64, 16, window=window, seed=50 + n)
+        check([2000, 3], n, 4, 2, 64, 16, window=window, seed=51 + n)
+
+
+@pytest.mark.parametrize("B,longest,n", [(64, 1100, 1), (3, 3000, 4), (5, 900, 2)])
+def test_replays_with_other_lengths(B, longest, n):
+    """A graph's cut follows the lengths in memory, not those of its capture."""
+    g = qmm_synth.rng(60)
+    cache, table, kv, q = setup([longest] * B, n, 4, 4, 64, 16, F16, 61)
+    lens, t = torch.zeros(B, dtype=torch.int32, device=DEV), dev(table)
+    ws = torch.empty(max(16, qmm.attn_q4_workspace_bytes(B, n, 4, 4, 64, table.shape[1] * 16)), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    qmm.attn_q4(q, cache, t, lens, out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qmm.attn_q4(q, cache, t, lens, out=out, ws=ws)
+    for r in range(5):
+        now = [longest] * B if r == 2 else [int(x) for x in g.integers(0, longest + 1, B)]
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(7)
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, qmm.attn_q4(q, cache, t, lens)), r
+        compare(out[:2], q[:2], [(k[:x], v[:x]) for (k, v), x in zip(kv, now[:2])], now[:2], n, 0, 0.125, F16)
+
+
+def test_rows_far_apart():
+    # a stride of queries that takes the offsets past 32 bits
+    stride = (1 << 24) - 8
+    B, n = 50, 3
+    wide = torch.zeros((B * n, stride), dtype=F16, device=DEV)
+    cache, table, kv, q = setup([40] * B, n, 4, 2, 64, 16, F16, 62)
+    wide[:, 8:8 + 256] = q.view(B * n, 256)
+    far = wide[:, 8:8 + 256].view(B, n, 4, 64)
+    lens = torch.full((B,), 40, dtype=torch.int32, device=DEV)
+    assert torch.equal(qmm.attn_q4(far, cache, dev(table), lens), qmm.attn_q4(q, cache, dev(table), lens))
+
+
 def test_rows_that_see_nothing():
     check([0], 1)
     check([0, 5, 0, 2, 1], 4, 6, 2, 64)

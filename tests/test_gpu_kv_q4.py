@@ -152,6 +152,21 @@ def test_reads_repeat_and_leave_out():
     assert qmm.kv_read_q4(cache, dev(slots[:0]))[0].shape == (0, 3, 96)
 
 
+@pytest.mark.parametrize("xt,T", [(BF16, 70000), (F16, 70001), (F32, 33000)])
+def test_large_reads_equal_small_ones(xt, T):
+    """Outputs past the caches' size are stored another way; the values are the same."""
+    Hk, D, page = 8, 128, 48
+    g = torch.Generator(device=DEV).manual_seed(5)
+    cache = torch.randint(0, 256, (300, Hk, 3, 20 * D), dtype=torch.uint8, device=DEV, generator=g)
+    half = cache.view(F16).view(300, Hk, 3, 2, 5 * D)
+    half[..., 4 * D:] = torch.rand(300, Hk, 3, 2, D, device=DEV, generator=g).half()       # scales and offsets
+    slots = torch.randint(-3, 300 * page + 3, (T,), dtype=torch.int64, device=DEV, generator=g)
+    k, v = qmm.kv_read_q4(cache, slots, xt)
+    for i in range(0, T, 10000):
+        ks, vs = qmm.kv_read_q4(cache, slots[i:i + 10000].clone(), xt)
+        assert torch.equal(k[i:i + 10000], ks) and torch.equal(v[i:i + 10000], vs), i
+
+
 def test_long_cache_offsets_past_32_bits():
     # 5 GB: the last pages lie behind 4 GiB
     D, Hk, page = 128, 8, 64

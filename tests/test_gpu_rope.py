@@ -144,6 +144,36 @@ def test_in_place_and_out_buffers_and_rows_behind():
     assert empty[0].shape == (0, Hq, D)
 
 
+@pytest.mark.parametrize("yt,T", [(BF16, 20000), (F16, 15000), (F32, 9001)])
+def test_large_outputs_equal_small_ones(yt, T):
+    """Outputs past the caches' size are stored another way; the values are the same."""
+    Hq, Hk, D = 32, 8, 128
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn(T, Hq + Hk, D, device=DEV, generator=g).to(BF16)
+    pos = torch.randint(0, 50, (T,), dtype=torch.int32, device=DEV, generator=g)
+    table = dev(oracle.rope_table(50, D))
+    w = 1 + 0.1 * torch.randn(D, device=DEV, generator=g)
+    q, k = qmm.qk_norm_rope(x[:, :Hq], x[:, Hq:], table, pos, q_weight=w, k_weight=w, dtype=yt)
+    for i in range(0, T, 5000):
+        qs, ks = qmm.qk_norm_rope(x[i:i + 5000, :Hq], x[i:i + 5000, Hq:], table, pos[i:i + 5000].clone(), q_weight=w, k_weight=w,
+                                  dtype=yt)
+        assert torch.equal(q[i:i + 5000], qs) and torch.equal(k[i:i + 5000], ks), i
+
+
+def test_rows_far_apart():
+    # a stride that takes the offsets past 32 bits
+    stride, T, D = (1 << 24) - 8, 140, 64
+    g = qmm_synth.rng(7)
+    x = dev(qmm_synth.activations(g, T, 6 * D)).to(BF16)
+    wide = torch.zeros((T, stride), dtype=BF16, device=DEV)
+    wide[:, stride - 6 * D:] = x
+    far = wide[:, stride - 6 * D:].view(T, 6, D)
+    pos, table = dev(g.integers(0, 50, T).astype(np.int32)), dev(oracle.rope_table(50, D))
+    for a, b in zip(qmm.qk_norm_rope(far[:, :4], far[:, 4:], table, pos),
+                    qmm.qk_norm_rope(x.view(T, 6, D)[:, :4], x.view(T, 6, D)[:, 4:], table, pos)):
+        assert torch.equal(a, b)
+
+
 def test_edge_heads():
     D = 64
     x = torch.zeros(1, 10, D, device=DEV)
