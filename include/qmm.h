@@ -431,8 +431,8 @@ int swiglu_q8_1(const float* g_u, void* hq, int64_t R, int64_t F, void* stream);
  * q_out and k_out have strides of their own; q_out == q is allowed where type
  * and stride are the same, and so for k; no other buffers may overlap.
  * Squares may leave the fp32 range at either end; a head of zeros gives zeros.
- * Requires T >= 0, 1 <= Hq, Hk <= 1024, T * (Hq + Hk) < 2^31, D % 32 == 0, 32
- * <= D <= 512, eps >= 0, 1 <= P < 2^31.  T == 0 is a no-op.
+ * Requires 0 <= T < 2^26, 1 <= Hq, Hk <= 1024, T * (Hq + Hk) < 2^31, D % 32 ==
+ * 0, 32 <= D <= 512, eps >= 0, 1 <= P < 2^31.  T == 0 is a no-op.
  */
 int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int type, const void* q_weight,
                  const void* k_weight, int w_type, float weight_offset, float eps, const float* rope, int64_t P,
@@ -470,9 +470,9 @@ int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_strid
  * in IEEE fp32 without contraction, zeros without a sign: the bytes are defined
  * to the bit, and every value that the cache holds is finite.  A NULL rope (with rot == 0)
  * stores the keys unturned and takes no positions.
- * Requires T >= 0, 1 <= Hk <= 1024, D one of 64, 96, 128, 192, 256, page % 16
- * == 0 and 16 <= page <= 2^20, 1 <= pages < 2^31, T * Hk < 2^31.  T == 0 is a
- * no-op.
+ * Requires 0 <= T < 2^26, 1 <= Hk <= 1024, D one of 64, 96, 128, 192, 256,
+ * page % 16 == 0 and 16 <= page <= 2^20, 1 <= pages < 2^31, T * Hk < 2^31.  T
+ * == 0 is a no-op.
  */
 int kv_append_q4(const void* k, int64_t k_stride, int k_type, const void* v, int64_t v_stride, int v_type,
                  const float* rope, int64_t P, int64_t rot, int interleaved, const int32_t* positions,
@@ -502,9 +502,9 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * Query i of n stands at len - n + i; it sees the keys up to its own place,
  * and with window > 0 of these the last `window`.  y = sum softmax(scale *
  * q . k) v over these.  A query that sees no key (len 0, or i < n - len) gives
- * zeros.  lens above W * page count as that, negative ones as 0; keys of a
- * page number outside [0, pages) are not seen; nothing of a page behind a
- * sequence's end is used, whatever it holds.
+ * zeros, and so does one whose every score is -inf.  lens above W * page count
+ * as that, negative ones as 0; keys of a page number outside [0, pages) are not
+ * seen; nothing of a page behind a sequence's end is used, whatever it holds.
  * Scores, softmax statistics and sums are fp32; the softmax's terms are
  * rounded to f16 (half a step, 2^-11 relative) where they meet the values.
  * ws: attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page) bytes of scratch, no
@@ -512,7 +512,8 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * must be ordered on one stream.  Equal calls give equal bits.
  * Requires B >= 0, 1 <= n <= QMM_ATTN_MAX_N, Hq % Hk == 0, Hq <= 1024, D one
  * of 64, 96, 128, 192, 256, scale finite, 0 <= window < 2^31, W >= 1, W * page
- * <= 2^30, B * n * Hq < 2^26, pages as kv_append_q4.  B == 0 is a no-op.
+ * <= 2^30, B * n * Hq < 2^26, B * (W * page / 32 + 1) < 2^31, pages as
+ * kv_append_q4.  B == 0 is a no-op.
  */
 int attn_q4(const void* q, int64_t q_stride, int type, const void* cache, int64_t pages, int64_t page,
             const int32_t* table, int64_t W, const int32_t* lens, float scale, int64_t window, void* y, int y_type,
@@ -543,8 +544,8 @@ size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
  * rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
  * values.
  * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
- * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, Tq * Hq and B * Hq
- * below 2^30.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.
+ * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, Tq * Hq < 2^30,
+ * B * Hq < 2^23.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.
  * ws: attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D) bytes of scratch, no
  * initialisation needed; may be NULL where that is 0.  Calls that share it
  * must be ordered on one stream.

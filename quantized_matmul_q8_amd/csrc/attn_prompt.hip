@@ -563,9 +563,12 @@ static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int
   return p;
 }
 
+// With Tq * Hq below 2^30 there are then less than 2^24 workgroups, a grid's most with 256 lanes each.
+constexpr int64_t kMostSequences = int64_t{1} << 23;
+
 static bool prompt_shape(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
   return B >= 0 && Tq >= 0 && Tk >= 0 && Tq < kMostTokens && Tk < kMostTokens && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
-         attn_head_dim(D) && Tq < kMostTokens / Hq && B < kMostTokens / Hq;
+         attn_head_dim(D) && Tq < kMostTokens / Hq && B < kMostSequences / Hq;
 }
 
 template <int D, int BN>
@@ -601,13 +604,11 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
   const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);
-  const int64_t grid = p.tiles * Hk * p.splits;
-  if (grid > 0x7fffffff) return QMM_ERR_SHAPE;
   const PromptArgs a{q, k, v, cu_q, cu_k, y, static_cast<float*>(ws), q_stride, k_stride, v_stride, scale,
                      static_cast<int>(std::min(window, kMostTokens)), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(B),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk), static_cast<int>(p.splits),
                      static_cast<int>(p.tiles), y_type, causal != 0};
-  const dim3 g(static_cast<unsigned>(grid));
+  const dim3 g(static_cast<unsigned>(p.tiles * Hk * p.splits));
   hipStream_t st = to_stream(stream);
   switch (D) {
     case 64: launch_prompt<64, 64>(a, type == QMM_BF16, g, st); break;

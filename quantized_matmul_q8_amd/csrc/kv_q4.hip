@@ -283,7 +283,7 @@ extern "C" int kv_append_q4(const void* k, int64_t k_stride, int k_type, const v
                             const int64_t* slots, void* cache, int64_t pages, int64_t page, int64_t T, int64_t Hk,
                             int64_t D, void* stream) {
   if (!known_type(k_type) || !known_type(v_type)) return QMM_ERR_UNSUPPORTED;
-  if (!kv_q4_shape(pages, page, Hk, D) || T < 0 || T > 0x7fffffff / Hk) return QMM_ERR_SHAPE;
+  if (!kv_q4_shape(pages, page, Hk, D) || T < 0 || T >= kMostRows || T > 0x7fffffff / Hk) return QMM_ERR_SHAPE;
   if (!strided_rows(k_stride, Hk, D) || !strided_rows(v_stride, Hk, D)) return QMM_ERR_SHAPE;
   if (rot < 0 || rot % 16 != 0 || rot > D || (rot > 0 && (P < 1 || P > 0x7fffffff))) return QMM_ERR_SHAPE;
   if (T == 0) return QMM_OK;
@@ -307,7 +307,7 @@ extern "C" int kv_append_q4(const void* k, int64_t k_stride, int k_type, const v
 extern "C" int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* slots, void* k, void* v,
                           int type, int64_t T, int64_t Hk, int64_t D, void* stream) {
   if (!known_type(type)) return QMM_ERR_UNSUPPORTED;
-  if (!kv_q4_shape(pages, page, Hk, D) || T < 0 || T > 0x7fffffff / Hk) return QMM_ERR_SHAPE;
+  if (!kv_q4_shape(pages, page, Hk, D) || T < 0 || T >= kMostRows || T > 0x7fffffff / Hk) return QMM_ERR_SHAPE;
   if (T == 0) return QMM_OK;
   if (!cache || !slots || !k || !v) return QMM_ERR_NULL;
   if (!aligned16(cache) || !aligned16(slots) || !aligned16(k) || !aligned16(v)) return QMM_ERR_ALIGN;

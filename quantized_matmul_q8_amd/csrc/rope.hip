@@ -154,7 +154,8 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
                             int64_t T, int64_t Hq, int64_t Hk, int64_t D, void* stream) {
   if (!known_type(type) || !known_type(out_type) || ((q_weight || k_weight) && !known_type(w_type)))
     return QMM_ERR_UNSUPPORTED;
-  if (Hq < 1 || Hq > 1024 || (k && (Hk < 1 || Hk > 1024)) || T < 0 || T > 0x7fffffff / (Hq + (k ? Hk : 0)) || D < 32 || D > 512 || D % 32 != 0) return QMM_ERR_SHAPE;
+  if (Hq < 1 || Hq > 1024 || (k && (Hk < 1 || Hk > 1024)) || D < 32 || D > 512 || D % 32 != 0) return QMM_ERR_SHAPE;
+  if (T < 0 || T >= kMostRows || T > 0x7fffffff / (Hq + (k ? Hk : 0))) return QMM_ERR_SHAPE;
   if (rot < 0 || rot % 16 != 0 || rot > D || (rot > 0 && (P < 1 || P > 0x7fffffff))) return QMM_ERR_SHAPE;
   if (!(eps >= 0.0f)) return QMM_ERR_SHAPE;
   if (!strided_rows(q_stride, Hq, D) || !strided_rows(q_out_stride, Hq, D)) return QMM_ERR_SHAPE;

@@ -11,6 +11,9 @@ inline bool strided_rows(int64_t stride, int64_t heads, int64_t D) {
   return stride >= heads * D && stride % 8 == 0 && stride < (int64_t{1} << 24);
 }
 
+// Tokens of a call, 32 lanes or a wave each: a grid has to stay below 2^32 of them.
+constexpr int64_t kMostRows = int64_t{1} << 26;
+
 inline bool known_type(int t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_BF16; }
 
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));

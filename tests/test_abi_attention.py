@@ -30,7 +30,7 @@ def test_rope_errors():
     for kw in (dict(T=-1), dict(T=HUGE), dict(Hq=0), dict(Hq=1025, qs=1 << 17, qos=1 << 17), dict(Hk=0), dict(D=48),
                dict(D=0), dict(D=544, qs=8192, qos=8192, ks=8192, kos=8192), dict(rot=8), dict(rot=-16), dict(rot=80),
                dict(P=0), dict(P=HUGE), dict(eps=-1.0), dict(eps=float("nan")), dict(qs=504), dict(qs=516), dict(ks=248),
-               dict(qos=0), dict(kos=260), dict(qs=HUGE)):
+               dict(qos=0), dict(kos=260), dict(qs=HUGE), dict(T=1 << 26), dict(T=1 << 26, k=NUL, Hq=1)):
         assert rope(**kw) == SHAPE, kw
     for p in ("q", "qo", "ko", "r", "p"):
         assert rope(**{p: NUL}) == NULL, p
@@ -53,6 +53,7 @@ def test_append_errors():
                dict(page=0), dict(page=24), dict(page=(1 << 20) + 16), dict(pages=0), dict(pages=HUGE), dict(ks=255),
                dict(vs=260), dict(rot=24), dict(rot=80), dict(P=0)):
         assert append(**kw) == SHAPE, kw
+    assert append(T=1 << 26, Hk=1) == SHAPE and append(T=(1 << 26) - 1, Hk=1, c=NUL) == NULL
     for p in ("k", "v", "r", "p", "s", "c"):
         assert append(**{p: NUL}) == NULL, p
         assert append(**{p: MISAL}) == ALIGN, p
@@ -66,7 +67,7 @@ def read(**kw):
 
 def test_read_errors():
     assert read(t=7) == UNSUP
-    for kw in (dict(T=-1), dict(T=HUGE), dict(Hk=0), dict(D=80), dict(page=8), dict(pages=0)):
+    for kw in (dict(T=-1), dict(T=HUGE), dict(Hk=0), dict(D=80), dict(page=8), dict(pages=0), dict(T=1 << 26, Hk=1)):
         assert read(**kw) == SHAPE, kw
     for p in ("c", "s", "k", "v"):
         assert read(**{p: NUL}) == NULL
@@ -84,7 +85,8 @@ def test_cached_attention_errors():
     assert cached(t=F32) == UNSUP and cached(t=3) == UNSUP and cached(yt=4) == UNSUP
     for kw in (dict(qs=504), dict(qs=513), dict(page=20), dict(pages=0), dict(W=0), dict(W=1 << 27), dict(B=-1), dict(n=0),
                dict(n=9), dict(Hq=6), dict(Hq=2), dict(Hk=0), dict(Hq=1028, qs=1 << 17), dict(D=72), dict(sc=float("inf")),
-               dict(sc=float("nan")), dict(win=-1), dict(win=HUGE), dict(B=1 << 23)):
+               dict(sc=float("nan")), dict(win=-1), dict(win=HUGE), dict(B=1 << 23),
+               dict(B=1 << 11, W=1 << 21)):
         assert cached(**kw) == SHAPE, kw
     for p in ("q", "c", "tab", "lens", "y"):
         assert cached(**{p: NUL}) == NULL, p
@@ -114,7 +116,7 @@ def test_prompt_errors():
     assert prompt(t=F32) == UNSUP and prompt(yt=2) == UNSUP and prompt(win=5, ca=0) == UNSUP
     for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(Tq=1 << 30), dict(Tk=1 << 30), dict(Hq=6), dict(Hk=0), dict(Hq=0),
                dict(D=32), dict(D=320), dict(qs=500), dict(ks=8), dict(vs=257), dict(win=-1), dict(win=HUGE),
-               dict(sc=float("nan")), dict(B=HUGE), dict(Hq=1032, qs=1 << 17)):
+               dict(sc=float("nan")), dict(B=HUGE), dict(B=1 << 20), dict(Hq=1032, qs=1 << 17)):
         assert prompt(**kw) == SHAPE, kw
     for p in ("q", "k", "v", "cq", "ck", "y"):
         assert prompt(**{p: NUL}) == NULL, p
