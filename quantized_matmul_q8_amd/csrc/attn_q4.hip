@@ -75,6 +75,20 @@ __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x150 + K, 0xf, 0xf, false));
 }
 
+// The cache is read past the device's caches: between two calls of a layer the
+// other layers' caches and weights pass through these, and lines that are taken
+// in push out what was written.  164 MB (8 x 16000) behind a pass over 1 GiB:
+// 39 us, with ordinary loads 71; called again and again with nothing between,
+// 403 MB: 79 and 85, and 82 MB, which the caches hold, 28 either way.
+__device__ __forceinline__ uint32_t ld4_nt(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+}
+__device__ __forceinline__ uint2 ld8_nt(const uint8_t* p) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  const v2u v = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(p));
+  return make_uint2(v.x, v.y);
+}
+
 // How a head's NB blocks are dealt out: runs of four blocks (a lane has one), of two (half of one), single ones (a quarter).
 template <int NB>
 struct Runs {
@@ -92,28 +106,40 @@ struct Cell {
     const int key = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int r = 0; r < Runs<NB>::kQuads; ++r) {
-      const uint4 x = ld16_a16(cell + r * 1024 + lane * 16);
+      const uint4 x = ld16_nt(cell + r * 1024 + lane * 16);
       k[4 * r] = x.x, k[4 * r + 1] = x.y, k[4 * r + 2] = x.z, k[4 * r + 3] = x.w;
-      ks[r] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + r * 256 + lane * 4);
+      ks[r] = ld4_nt(cell + 8 * D + r * 256 + lane * 4);
     }
     constexpr int kAt = 4 * Runs<NB>::kQuads;
     if constexpr (Runs<NB>::kPair) {
-      const uint2 x = *reinterpret_cast<const uint2*>(cell + ((kAt + (c >> 1)) * 16 + key) * 16 + (c & 1) * 8);
+      const uint2 x = ld8_nt(cell + ((kAt + (c >> 1)) * 16 + key) * 16 + (c & 1) * 8);
       k[kAt] = x.x, k[kAt + 1] = x.y;
-      ks[Runs<NB>::kQuads] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + ((kAt + (c >> 1)) * 16 + key) * 4);
+      ks[Runs<NB>::kQuads] = ld4_nt(cell + 8 * D + ((kAt + (c >> 1)) * 16 + key) * 4);
     }
     if constexpr (Runs<NB>::kOne) {
-      k[NB - 1] = *reinterpret_cast<const uint32_t*>(cell + ((NB - 1) * 16 + key) * 16 + c * 4);
-      ks[Runs<NB>::kScales - 1] = *reinterpret_cast<const uint32_t*>(cell + 8 * D + ((NB - 1) * 16 + key) * 4);
+      k[NB - 1] = ld4_nt(cell + ((NB - 1) * 16 + key) * 16 + c * 4);
+      ks[Runs<NB>::kScales - 1] = ld4_nt(cell + 8 * D + ((NB - 1) * 16 + key) * 4);
     }
-    struct __attribute__((aligned(NB % 4 == 0 ? 16 : NB % 2 == 0 ? 8 : 4))) Words { uint32_t w[NB]; };
-    const Words x = *reinterpret_cast<const Words*>(cell + 10 * D + lane * (4 * NB));
+    const uint8_t* values = cell + 10 * D + lane * (4 * NB);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) v[b] = x.w[b];
+    for (int b = 0; b < NB;) {
+      if constexpr (NB % 4 == 0) {
+        const uint4 x = ld16_nt(values + 4 * b);
+        v[b] = x.x, v[b + 1] = x.y, v[b + 2] = x.z, v[b + 3] = x.w;
+        b += 4;
+      } else if constexpr (NB % 2 == 0) {
+        const uint2 x = ld8_nt(values + 4 * b);
+        v[b] = x.x, v[b + 1] = x.y;
+        b += 2;
+      } else {
+        v[b] = ld4_nt(values + 4 * b);
+        b += 1;
+      }
+    }
 #pragma unroll
     for (int r = 0; r < kVs; ++r) {
       const int at = min(r * 16 + key, 4 * NB - 1);
-      vs[r] = *reinterpret_cast<const uint32_t*>(cell + 18 * D + (c * (4 * NB) + at) * 4);
+      vs[r] = ld4_nt(cell + 18 * D + (c * (4 * NB) + at) * 4);
     }
   }
 
@@ -250,19 +276,21 @@ struct AttnQ4Shared {
 };
 
 // Steps `from` .. `to` of one sequence, key head and row block; `slot`: where a partial result goes, or -1 for a whole one.
-template <int NB, int RT, int kWaves>
-__device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB, RT, kWaves>& sh, int seq, int kh,
-                                            int row_block, const Extent& ext, int from, int to, int64_t slot) {
+struct Segment {
+  int seq, kh, row_block, from, to;
+  int64_t slot;
+  Extent ext;
+};
+
+// One segment after the other: next(s) moves s to the one behind it and tells
+// whether there is one.  Its first loads begin before the results of the one
+// before are joined and written.
+template <int NB, int RT, int kWaves, typename Next>
+__device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB, RT, kWaves>& sh, Segment seg, const Next& next) {
   constexpr int D = 32 * NB;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
-  const int len = ext.len, floor_at = ext.floor_at;
-  const int begin = ext.first + from * kStep, end = min(len, ext.first + to * kStep);
-
-  const scalar_ints pages = as_scalar(a.table + static_cast<int64_t>(seq) * a.W);
   const uint64_t cell_bytes = 20 * D, head_bytes = a.cells * cell_bytes, page_bytes = a.Hk * head_bytes;
-  const uint8_t* head = a.cache + kh * head_bytes;
-  const uint32_t last_cell = static_cast<uint32_t>(max(0, len - 1)) / kCellTokens;  // nothing behind it is looked up or loaded
   const auto page_of = [&](uint32_t cell) {
     return static_cast<uint32_t>(static_cast<uint64_t>(cell) * a.page_mul >> a.page_shift);
   };
@@ -273,6 +301,10 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
     Cell<NB> cell[2];
     int page[2];
   };
+  // of the segment whose loads are under way
+  scalar_ints pages;
+  const uint8_t* head;
+  uint32_t last_cell;  // nothing behind it is looked up or loaded
   const auto look_up = [&](int t, int (&page)[2]) {
 #pragma unroll
     for (uint32_t u = 0; u < 2; ++u) page[u] = pages[page_of(min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell))];
@@ -288,179 +320,203 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
   };
   // Loads run one step ahead in the other buffer and look-ups two; behind the
   // end they repeat the last cell, so that every step waits for the same loads.
-  // The first ones before the queries, which have to be waited for.
   const int stride = kWaves * kStep;
-  int t = begin + wave * kStep;
+  int t, end;
   Step x, y;
   int page[2], ahead[2];
-  if (t < end) {
-    look_up(t, page);
-    look_up(t + stride, ahead);
-    load(x, t, page);
-  }
-
-  // queries: this lane's row of each tile, its place, and what a product is multiplied with
-  h8 q[RT][NB];
-  float mul[RT];
-  int at[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = (row_block * RT + r) * 16 + col;
-    const bool on = row < a.rows;
-    const int i = on ? row / a.group : a.n - 1, h = kh * a.group + (on ? row % a.group : 0);
-    at[r] = len - a.n + i;
-    const int64_t base = (static_cast<int64_t>(seq) * a.n + i) * a.q_stride + static_cast<int64_t>(h) * D;
-    mul[r] = fabsf(a.scale) * 1.44269504088896340736f;
-    if (!a.bf16) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        q[r][j] = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(a.q) + base + operand_dim<NB>(j, c));
-    } else {
-      // a power of two for the row brings its largest value to 2^13: exact but for what lies 2^-27 below that
-      float f[NB][8], top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        Raw8<QMM_BF16> x;
-        x.load(a.q, (base + operand_dim<NB>(j, c)) / 8);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[j][k] = x.get(k), top = fmaxf(top, fabsf(f[j][k]));
-      }
-      top = rows_max(top);
-      const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 14 : 0;
-      mul[r] = __builtin_amdgcn_ldexpf(mul[r], e);
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(f[j][k], -e));
+  v4u raw[RT][NB];  // the queries as stored
+  const auto enter = [&]() {
+    pages = as_scalar(a.table + static_cast<int64_t>(seg.seq) * a.W);
+    head = a.cache + seg.kh * head_bytes;
+    last_cell = static_cast<uint32_t>(max(0, seg.ext.len - 1)) / kCellTokens;
+    end = min(seg.ext.len, seg.ext.first + seg.to * kStep);
+    t = seg.ext.first + seg.from * kStep + wave * kStep;
+    if (t < end) {
+      look_up(t, page);
+      look_up(t + stride, ahead);
+      load(x, t, page);
     }
-    // in the order of the keys' codes
-#pragma unroll
-    for (int j = 0; j < NB; ++j) q[r][j] = __builtin_shufflevector(q[r][j], q[r][j], 0, 4, 1, 5, 2, 6, 3, 7);
-    // a factor above zero, so that the largest product is the largest score
-    const _Float16 sign = static_cast<_Float16>(mul[r] == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) q[r][j] *= sign;
-    mul[r] = mul[r] == 0.0f ? 1.0f : mul[r];
-  }
-
-  v4f o[RT][2 * NB];
-  // the largest product so far, what is added to a product's exponent for it, and this lane's part of the sum
-  float top[RT], base[RT], sum[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    top[r] = -INFINITY, base[r] = kLift, sum[r] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  const auto work = [&](Step& st, int t) {
-    const bool there0 = there(st.page[0]), there1 = there(st.page[1]);
-    // whether every query sees the whole step
-    const bool whole = t + kStep <= len - a.n + 1 && t >= (a.window > 0 ? len - a.window : 0) && there0 && there1;
-    v4f s[RT][2];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const h8 k = st.cell[u].key_operand(j);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
-      }
-    if (!whole) {
-      const int lo = floor_at - t, hi = len - t;
-      st.cell[0].clear_scales(lane, there0 ? lo : 16, hi);
-      st.cell[1].clear_scales(lane, there1 ? lo - 16 : 16, hi - 16);
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = t + (k >> 2) * kCellTokens + 4 * c + (k & 3);
-          const bool seen = j <= at[r] && (a.window == 0 || j > at[r] - a.window) && (k < 4 ? there0 : there1);
-          s[r][k >> 2][k & 3] = seen ? s[r][k >> 2][k & 3] : -INFINITY;
-        }
-    }
-    st.cell[0].pair_scales(lane);
-    st.cell[1].pair_scales(lane);
-    h8 p[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      float most = top[r];
+      const int row = (seg.row_block * RT + r) * 16 + col;
+      const bool on = row < a.rows;
+      const int i = on ? row / a.group : a.n - 1, h = seg.kh * a.group + (on ? row % a.group : 0);
+      const int64_t base = (static_cast<int64_t>(seg.seq) * a.n + i) * a.q_stride + static_cast<int64_t>(h) * D;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) most = fmaxf(most, s[r][k >> 2][k & 3]);
-      most = rows_max(most);
-      if (__builtin_amdgcn_ballot_w64(most > top[r])) {
-        const float keep = __builtin_amdgcn_exp2f((top[r] - (most == -INFINITY ? 0.0f : most)) * mul[r]);
-        sum[r] *= keep;
-#pragma unroll
-        for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
-        top[r] = most;
-        base[r] = kLift - (most == -INFINITY ? 0.0f : most) * mul[r];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3], mul[r], base[r]));
-        sum[r] += e;
-        p[r][(k & 4) + kv_quad_byte(k & 3)] = static_cast<_Float16>(e);
-      }
+      for (int j = 0; j < NB; ++j)
+        raw[r][j] = *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.q) + base + operand_dim<NB>(j, c));
     }
-    add_values<NB, RT>(st.cell, p, o);
   };
+  enter();
 
-  if (t < end) {
-    // in pairs, with no way out between the two: each step then waits for its own loads alone
-    const int steps = (end - t + stride - 1) / stride;
-    for (int k = 1; k < steps; k += 2) {
-      load(y, t + stride, ahead);
-      look_up(t + 2 * stride, ahead);
-      __builtin_amdgcn_sched_barrier(0);  // all of these before the work, not sunk to their use
-      work(x, t);
-      load(x, t + 2 * stride, ahead);
-      look_up(t + 3 * stride, ahead);
-      __builtin_amdgcn_sched_barrier(0);
-      work(y, t + stride);
-      t += 2 * stride;
-    }
-    if (steps & 1) work(x, t);
-  }
+  for (;;) {
+    const int len = seg.ext.len, floor_at = seg.ext.floor_at;
 
-  // join the waves, tile by tile, and write
+    // queries: this lane's row of each tile, its place, and what a product is multiplied with
+    h8 q[RT][NB];
+    float mul[RT];
+    int at[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const float l = rows_sum(sum[r]);
-    if (c == 0) sh.m[wave][col] = top[r] * mul[r], sh.l[wave][col] = l;
+    for (int r = 0; r < RT; ++r) {
+      const int row = (seg.row_block * RT + r) * 16 + col;
+      at[r] = len - a.n + (row < a.rows ? row / a.group : a.n - 1);
+      mul[r] = fabsf(a.scale) * 1.44269504088896340736f;
+      if (!a.bf16) {
 #pragma unroll
-    for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
-    __syncthreads();
-    const int row0 = (row_block * RT + r) * 16, rows = min(16, a.rows - row0);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
-      const int row = x / (D / 4), d = x % (D / 4) * 4;
-      float m = sh.m[0][row];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
-      const float zero = m == -INFINITY ? 0.0f : m;
-      float total = 0.0f;
-      v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - zero);
-        total += sh.l[w][row] * f;
-        y += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
-      }
-      if (slot >= 0) {
-        const int64_t at_row = slot * a.block_rows + r * 16 + row;
-        *reinterpret_cast<v4f*>(a.part + at_row * D + d) = y;
-        if (d == 0)
-          reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D)[at_row] = make_float2(m, total);
+        for (int j = 0; j < NB; ++j) q[r][j] = __builtin_bit_cast(h8, raw[r][j]);
       } else {
-        const int i = (row0 + row) / a.group, h = kh * a.group + (row0 + row) % a.group;
-        const int64_t out = (static_cast<int64_t>(seq) * a.n + i) * a.Hq + h;
-        y *= total == 0.0f ? 0.0f : 1.0f / total;
-        store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+        // a power of two for the row brings its largest value to 2^13: exact but for what lies 2^-27 below that
+        float f[NB][8], top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t w = raw[r][j][k >> 1];
+            f[j][k] = __builtin_bit_cast(float, k & 1 ? w & 0xffff0000u : w << 16);
+            top = fmaxf(top, fabsf(f[j][k]));
+          }
+        top = rows_max(top);
+        const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 14 : 0;
+        mul[r] = __builtin_amdgcn_ldexpf(mul[r], e);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(f[j][k], -e));
       }
+      // in the order of the keys' codes
+#pragma unroll
+      for (int j = 0; j < NB; ++j) q[r][j] = __builtin_shufflevector(q[r][j], q[r][j], 0, 4, 1, 5, 2, 6, 3, 7);
+      // a factor above zero, so that the largest product is the largest score
+      const _Float16 sign = static_cast<_Float16>(mul[r] == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) q[r][j] *= sign;
+      mul[r] = mul[r] == 0.0f ? 1.0f : mul[r];
     }
-    __syncthreads();
+
+    v4f o[RT][2 * NB];
+    // the largest product so far, what is added to a product's exponent for it, and this lane's part of the sum
+    float top[RT], base[RT], sum[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      top[r] = -INFINITY, base[r] = kLift, sum[r] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    const auto work = [&](Step& st, int t) {
+      const bool there0 = there(st.page[0]), there1 = there(st.page[1]);
+      // whether every query sees the whole step
+      const bool whole = t + kStep <= len - a.n + 1 && t >= (a.window > 0 ? len - a.window : 0) && there0 && there1;
+      v4f s[RT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const h8 k = st.cell[u].key_operand(j);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], s[r][u], 0, 0, 0);
+        }
+      if (!whole) {
+        const int lo = floor_at - t, hi = len - t;
+        st.cell[0].clear_scales(lane, there0 ? lo : 16, hi);
+        st.cell[1].clear_scales(lane, there1 ? lo - 16 : 16, hi - 16);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int j = t + (k >> 2) * kCellTokens + 4 * c + (k & 3);
+            const bool seen = j <= at[r] && (a.window == 0 || j > at[r] - a.window) && (k < 4 ? there0 : there1);
+            s[r][k >> 2][k & 3] = seen ? s[r][k >> 2][k & 3] : -INFINITY;
+          }
+      }
+      st.cell[0].pair_scales(lane);
+      st.cell[1].pair_scales(lane);
+      h8 p[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float most = top[r];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, s[r][k >> 2][k & 3]);
+        most = rows_max(most);
+        if (__builtin_amdgcn_ballot_w64(most > top[r])) {
+          const float keep = __builtin_amdgcn_exp2f((top[r] - (most == -INFINITY ? 0.0f : most)) * mul[r]);
+          sum[r] *= keep;
+#pragma unroll
+          for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
+          top[r] = most;
+          base[r] = kLift - (most == -INFINITY ? 0.0f : most) * mul[r];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3], mul[r], base[r]));
+          sum[r] += e;
+          p[r][(k & 4) + kv_quad_byte(k & 3)] = static_cast<_Float16>(e);
+        }
+      }
+      add_values<NB, RT>(st.cell, p, o);
+    };
+
+    if (t < end) {
+      // in pairs, with no way out between the two: each step then waits for its own loads alone
+      const int steps = (end - t + stride - 1) / stride;
+      for (int k = 1; k < steps; k += 2) {
+        load(y, t + stride, ahead);
+        look_up(t + 2 * stride, ahead);
+        __builtin_amdgcn_sched_barrier(0);  // all of these before the work, not sunk to their use
+        work(x, t);
+        load(x, t + 2 * stride, ahead);
+        look_up(t + 3 * stride, ahead);
+        __builtin_amdgcn_sched_barrier(0);
+        work(y, t + stride);
+        t += 2 * stride;
+      }
+      if (steps & 1) work(x, t);
+    }
+
+    const Segment done = seg;
+    const bool more = next(seg);
+    if (more) enter();
+
+    // join the waves, tile by tile, and write
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float l = rows_sum(sum[r]);
+      if (c == 0) sh.m[wave][col] = top[r] * mul[r], sh.l[wave][col] = l;
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
+      __syncthreads();
+      const int row0 = (done.row_block * RT + r) * 16, rows = min(16, a.rows - row0);
+      for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
+        const int row = x / (D / 4), d = x % (D / 4) * 4;
+        float m = sh.m[0][row];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
+        const float zero = m == -INFINITY ? 0.0f : m;
+        float total = 0.0f;
+        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - zero);
+          total += sh.l[w][row] * f;
+          y += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
+        }
+        if (done.slot >= 0) {
+          const int64_t at_row = done.slot * a.block_rows + r * 16 + row;
+          *reinterpret_cast<v4f*>(a.part + at_row * D + d) = y;
+          if (d == 0)
+            reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D)[at_row] = make_float2(m, total);
+        } else {
+          const int i = (row0 + row) / a.group, h = done.kh * a.group + (row0 + row) % a.group;
+          const int64_t out = (static_cast<int64_t>(done.seq) * a.n + i) * a.Hq + h;
+          y *= total == 0.0f ? 0.0f : 1.0f / total;
+          store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+        }
+      }
+      __syncthreads();
+    }
+    if (!more) break;
   }
 }
 
@@ -471,7 +527,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
   const int row_block = blockIdx.x % a.row_blocks, kh = blockIdx.x / a.row_blocks % a.Hk;
   const int seq = blockIdx.x / a.row_blocks / a.Hk;
   const Extent e = extent_of(a, as_scalar(a.lens)[seq]);
-  attn_q4_run<NB, RT, kWaves>(a, sh, seq, kh, row_block, e, 0, e.steps, -1);
+  attn_q4_run<NB, RT, kWaves>(a, sh, Segment{seq, kh, row_block, 0, e.steps, -1, e}, [](Segment&) { return false; });
 }
 
 // The parts of a sequence of so many steps.
@@ -488,8 +544,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a
   if (part >= parts) return;
   const int each = static_cast<unsigned>(e.steps) / parts, more = e.steps - each * parts;  // the first ones have one more
   const int from = part * each + min(part, more), to = from + each + (part < more ? 1 : 0);
-  attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to,
-                              parts == 1 ? -1 : int64_t{blockIdx.x});
+  attn_q4_run<NB, RT, kWaves>(a, sh,
+                              Segment{static_cast<int>(seq), head / a.row_blocks, head % a.row_blocks, from, to,
+                                      parts == 1 ? -1 : int64_t{blockIdx.x}, e},
+                              [](Segment&) { return false; });
 }
 
 // Equal runs of the steps of all.
@@ -503,24 +561,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a)
   int64_t left = min(total - first, per);  // steps of the run
   if (left <= 0) return;
   const Steps at = find_steps(a, first, 0, lane);
-  int seq = at.seq;
-  Extent e = extent_of(a, as_scalar(a.lens)[seq]);
+  const Extent e = extent_of(a, as_scalar(a.lens)[at.seq]);
   const int64_t in = first - static_cast<int64_t>(at.before) * heads;
-  int head = static_cast<int>(in / e.steps), from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
+  int head = static_cast<int>(in / e.steps);
+  const int from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
   int64_t slot = 2 * int64_t{blockIdx.x};
-  for (;;) {
+  // the segment that begins at `from`: to its item's end or the run's
+  const auto segment = [&](int seq, const Extent& e, int from) {
     const int to = static_cast<int>(min(static_cast<int64_t>(e.steps), from + left));
-    attn_q4_run<NB, RT, kWaves>(a, sh, seq, head / a.row_blocks, head % a.row_blocks, e, from, to,
-                                from == 0 && to == e.steps ? -1 : slot);
     left -= to - from;
-    if (left == 0) break;
-    from = 0;
+    return Segment{seq, head / a.row_blocks, head % a.row_blocks, from, to, from == 0 && to == e.steps ? -1 : slot, e};
+  };
+  attn_q4_run<NB, RT, kWaves>(a, sh, segment(at.seq, e, from), [&](Segment& s) {
+    if (left == 0) return false;
     slot = 2 * int64_t{blockIdx.x} + 1;  // the last one's, should it not be whole
+    int seq = s.seq;
+    Extent e = s.ext;
     if (++head == heads) {
       head = 0;
       e = extent_of(a, as_scalar(a.lens)[++seq]);
     }
-  }
+    s = segment(seq, e, 0);
+    return true;
+  });
 }
 
 // Joins the partial results of one row, a wave each.
