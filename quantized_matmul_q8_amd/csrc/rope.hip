@@ -81,8 +81,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
     if (on) {
       const int64_t at = (t * a.x_stride[side] + static_cast<int64_t>(h) * a.D) / 8;
       Raw8<XT> lo, hi;
-      lo.load(a.x[side], at + ca);
-      hi.load(a.x[side], at + cb);
+      // Large calls read past the caches too: what wrote the rows has filled these, and lines that are taken in push its
+      // stores out (16384 x 72 x 128 behind their writer: 146 -> 124 us).  Not where two loads share lines.
+      if (a.large && !a.interleaved) lo.load_once(a.x[side], at + ca), hi.load_once(a.x[side], at + cb);
+      else lo.load(a.x[side], at + ca), hi.load(a.x[side], at + cb);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = lo.get(j), v[8 + j] = hi.get(j);
     }
