@@ -45,32 +45,57 @@ __device__ __forceinline__ float halves_sum(float v) {
 // One row of four dims per lane from `count` partial results: at `part` + step *
 // at(k) number k's sums of terms times values, in ml[at(k)] its maximum and sum
 // of terms.  The maxima and sums by the lanes, 64 at a time, then the partial
-// results in order, four loads in flight.  Zeros if all sums are 0.
+// results in order, four loads in flight.  The first loads begin with the
+// object, so that what is done before join() hides them.
 template <typename At>
-__device__ __forceinline__ v4f join_parts(const At& at, const float* part, int64_t step, const float2* ml, int count,
-                                          int lane) {
-  float m = -INFINITY, total = 0.0f;
-  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = 0; k0 < count; k0 += 64) {
-    const int here = min(64, count - k0);
-    const float2 own = lane < here ? ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
-    float most = fmaxf(m, rows_max(own.x));
-#pragma unroll
-    for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
-    const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
-    const float f = __builtin_amdgcn_exp2f(own.x - base);
-    total = total * keep + wave_sum(own.y * f);
-    y *= keep;
-    m = most;
-    for (int k = 0; k < here; k += 4) {
-      v4f x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + at(k0 + min(k + i, here - 1)) * step);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y += x[i] * (k + i < here ? __shfl(f, k + i) : 0.0f);
-    }
+struct Parts {
+  const At at;
+  const float* part;
+  const float2* ml;
+  int64_t step;
+  int count, lane;
+  float2 own;
+  v4f x[4];
+
+  __device__ __forceinline__ Parts(const At& at, const float* part, int64_t step, const float2* ml, int count, int lane)
+      : at(at), part(part), ml(ml), step(step), count(count), lane(lane) {
+    load_sums(0);
+    load_rows(0);
   }
-  return y * (total == 0.0f ? 0.0f : 1.0f / total);
-}
+  __device__ __forceinline__ void load_sums(int k0) { own = ml[at(min(k0 + lane, count - 1))]; }
+  __device__ __forceinline__ void load_rows(int k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const v4f*>(part + at(min(k + i, count - 1)) * step);
+  }
+
+  // The row; zeros if all sums are 0.
+  __device__ __forceinline__ v4f join() {
+    float m = -INFINITY, total = 0.0f;
+    v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < count; k0 += 64) {
+      const int here = min(64, count - k0);
+      if (lane >= here) own = make_float2(-INFINITY, 0.0f);
+      float most = fmaxf(m, rows_max(own.x));
+#pragma unroll
+      for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
+      const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
+      const float f = __builtin_amdgcn_exp2f(own.x - base);
+      total = total * keep + wave_sum(own.y * f);
+      y *= keep;
+      m = most;
+      if (k0 + 64 < count) load_sums(k0 + 64);
+      for (int k = 0; k < here; k += 4) {
+        v4f now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = x[i];
+        if (k0 + k + 4 < count) load_rows(k0 + k + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k + i < here) y += now[i] * __shfl(f, k + i);
+      }
+    }
+    return y * (total == 0.0f ? 0.0f : 1.0f / total);
+  }
+};
 
 }  // namespace qmm

@@ -535,12 +535,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
 __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int D) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int part = blockIdx.x % (kRows / 4), kh = blockIdx.x / (kRows / 4) % a.Hk, n = blockIdx.x / (kRows / 4) / a.Hk;
-  const Place pl = find_place(a, n, lane);
-  const int in_tile = part * 4 + wave, row = pl.tile * kRows + in_tile;
-  if (!pl.found || row >= pl.nq * a.group) return;
+  const int in_tile = part * 4 + wave;
   const int64_t slot = (static_cast<int64_t>(n) * a.Hk + kh) * a.splits * kRows + in_tile;
   const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.tiles) * a.Hk * a.splits * kRows * D);
-  const v4f y = join_parts([&](int k) { return slot + k * kRows; }, a.part + min(lane * 4, D - 4), D, ml, a.splits, lane);
+  // every tile has its slots, whether there is such a tile or not
+  Parts parts([&](int k) { return slot + k * kRows; }, a.part + min(lane * 4, D - 4), D, ml, a.splits, lane);
+  const Place pl = find_place(a, n, lane);
+  const int row = pl.tile * kRows + in_tile;
+  if (!pl.found || row >= pl.nq * a.group) return;
+  const v4f y = parts.join();
   const int64_t out = (static_cast<int64_t>(pl.q0 + row / a.group) * a.Hq + kh * a.group + row % a.group) * D;
   if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
 }

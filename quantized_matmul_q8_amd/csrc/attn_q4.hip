@@ -227,13 +227,7 @@ __device__ __forceinline__ Extent extent_of(const AttnQ4Args& a, int32_t stored)
   return e;
 }
 
-// The sequences' steps in a row, by a wave: 64 sequences at a time.  Sums of
-// steps of one head and row block.
-struct Steps {
-  int total = 0;   // of all sequences
-  int before = 0;  // of those before `seq`
-  int seq = 0;
-};
+// Steps of one head and row block, summed over sequences by a wave, 64 of them at a time.
 __device__ __forceinline__ int scan_steps(const AttnQ4Args& a, int b0, int lane, int& mine) {
   mine = b0 + lane < a.B ? extent_of(a, a.lens[min(b0 + lane, a.B - 1)]).steps : 0;
   int upto = mine;
@@ -244,29 +238,42 @@ __device__ __forceinline__ int scan_steps(const AttnQ4Args& a, int b0, int lane,
   }
   return upto;
 }
-__device__ __forceinline__ int total_steps(const AttnQ4Args& a, int lane) {
+// Of all sequences; `before`: of those before `seq`.
+__device__ __forceinline__ int total_steps(const AttnQ4Args& a, int lane, int seq, int& before) {
   int total = 0, mine;
-  for (int b0 = 0; b0 < a.B; b0 += 64) total += __builtin_amdgcn_readlane(scan_steps(a, b0, lane, mine), 63);
+  before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int upto = scan_steps(a, b0, lane, mine);
+    if (seq >= b0 && seq < b0 + 64) before = total + __builtin_amdgcn_readlane(upto - mine, seq - b0);
+    total += __builtin_amdgcn_readlane(upto, 63);
+  }
   return total;
 }
-// The sequence in which step `pos` of all heads' lies, and the steps before it; or those before sequence `seq` (pos < 0).
-__device__ __forceinline__ Steps find_steps(const AttnQ4Args& a, int64_t pos, int seq, int lane) {
-  Steps s;
+// The sequence in which step `pos` of all heads' lies; `before`: the steps before it.
+__device__ __forceinline__ int find_steps(const AttnQ4Args& a, int64_t pos, int lane, int& before) {
   const int64_t heads = static_cast<int64_t>(a.Hk) * a.row_blocks;
+  before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     int mine;
     const int upto = scan_steps(a, b0, lane, mine);
-    const uint64_t here = pos < 0 ? (seq < b0 + 64 ? 1ull << (seq - b0) : 0ull)
-                                  : __builtin_amdgcn_ballot_w64((s.before + upto) * heads > pos);
+    const uint64_t here = __builtin_amdgcn_ballot_w64((before + upto) * heads > pos);
     if (here) {
       const int at = __builtin_ctzll(here);
-      s.seq = b0 + at;
-      s.before += __builtin_amdgcn_readlane(upto - mine, at);
-      return s;
+      before += __builtin_amdgcn_readlane(upto - mine, at);
+      return b0 + at;
     }
-    s.before += __builtin_amdgcn_readlane(upto, 63);
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
-  return s;
+  return 0;
+}
+
+// In 32 bits where both numbers have no more: a quotient of 64 bits takes a hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
+// The steps of a run.
+__device__ __forceinline__ int64_t run_steps(const AttnQ4Args& a, int64_t total) {
+  return max(static_cast<int64_t>(a.least), quotient(total + a.groups - 1, a.groups));
 }
 
 template <int NB, int RT, int kWaves>
@@ -555,15 +562,15 @@ template <int NB, int RT, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a) {
   __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
   const int lane = threadIdx.x & 63, heads = a.Hk * a.row_blocks;
-  const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
-  const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
+  int before;
+  const int64_t total = static_cast<int64_t>(total_steps(a, lane, 0, before)) * heads, per = run_steps(a, total);
   const int64_t first = blockIdx.x * per;
   int64_t left = min(total - first, per);  // steps of the run
   if (left <= 0) return;
-  const Steps at = find_steps(a, first, 0, lane);
-  const Extent e = extent_of(a, as_scalar(a.lens)[at.seq]);
-  const int64_t in = first - static_cast<int64_t>(at.before) * heads;
-  int head = static_cast<int>(in / e.steps);
+  const int seq0 = find_steps(a, first, lane, before);
+  const Extent e = extent_of(a, as_scalar(a.lens)[seq0]);
+  const int64_t in = first - static_cast<int64_t>(before) * heads;
+  int head = static_cast<int>(quotient(in, e.steps));
   const int from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
   int64_t slot = 2 * int64_t{blockIdx.x};
   // the segment that begins at `from`: to its item's end or the run's
@@ -572,7 +579,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a)
     left -= to - from;
     return Segment{seq, head / a.row_blocks, head % a.row_blocks, from, to, from == 0 && to == e.steps ? -1 : slot, e};
   };
-  attn_q4_run<NB, RT, kWaves>(a, sh, segment(at.seq, e, from), [&](Segment& s) {
+  attn_q4_run<NB, RT, kWaves>(a, sh, segment(seq0, e, from), [&](Segment& s) {
     if (left == 0) return false;
     slot = 2 * int64_t{blockIdx.x} + 1;  // the last one's, should it not be whole
     int seq = s.seq;
@@ -600,11 +607,10 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
     first = static_cast<int64_t>(seq) * heads + head;
     second = first + step;
   } else {
-    const Steps at = find_steps(a, -1, seq, lane);
-    const int64_t total = static_cast<int64_t>(total_steps(a, lane)) * heads;
-    const int64_t per = max(static_cast<int64_t>(a.least), (total + a.groups - 1) / a.groups);
-    const int64_t begin = static_cast<int64_t>(at.before) * heads + static_cast<int64_t>(head) * steps;
-    const int64_t g0 = begin / per, g1 = (begin + steps - 1) / per;
+    int before;
+    const int64_t per = run_steps(a, static_cast<int64_t>(total_steps(a, lane, seq, before)) * heads);
+    const int64_t begin = static_cast<int64_t>(before) * heads + static_cast<int64_t>(head) * steps;
+    const int64_t g0 = quotient(begin, per), g1 = quotient(begin + steps - 1, per);
     count = static_cast<int>(g1 - g0 + 1);
     // the first run's second result, unless the run begins with it; the others' first
     first = 2 * g0 + (begin == g0 * per ? 0 : 1);
@@ -613,8 +619,8 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   }
   if (count == 1) return;  // whole, and written
   const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D);
-  const v4f y = join_parts([&](int k) { return (k == 0 ? first : second + (k - 1) * step) * a.block_rows + in; },
-                           a.part + min(lane * 4, D - 4), D, ml, count, lane);
+  const v4f y = Parts([&](int k) { return (k == 0 ? first : second + (k - 1) * step) * a.block_rows + in; },
+                      a.part + min(lane * 4, D - 4), D, ml, count, lane).join();
   const int64_t out = blockIdx.x;
   if (lane * 4 < D) store4(a.y_type, a.y, (out * D + lane * 4) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
