@@ -70,15 +70,21 @@ def check(lens, n=1, Hq=8, Hk=2, D=128, page=16, xt=F16, yt=None, window=0, scal
 
 
 @pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
-@pytest.mark.parametrize("Hq,Hk", [(4, 4), (6, 2), (8, 1), (16, 1), (14, 2), (40, 1)])
+@pytest.mark.parametrize("Hq,Hk", [(4, 4), (6, 2), (8, 1), (15, 1), (14, 2), (40, 1)])
 def test_heads(D, Hq, Hk):
     check([77, 1, 200], 1, Hq, Hk, D, seed=D + Hq)
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 5, 8])
 def test_new_tokens(n):
-    check([100, n, n + 1, 3, 33], n, 8, 2, 128, seed=n)
+    check([100, n, n + 1, 3, 33], n, 10, 2, 128, seed=n)
     check([64, 65, 300], n, 3, 3, 64, 32, BF16, seed=n + 10)
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 16), (2, 8), (4, 8), (8, 8)])
+def test_whole_tiles_of_rows(n, Hq):
+    for D in (64, 128, 256):
+        check([90, n, 35], n, Hq, 1, D, seed=n + D)
 
 
 @pytest.mark.parametrize("n,Hq", [(8, 32), (8, 16), (4, 20), (5, 7)])
@@ -147,7 +153,7 @@ def test_runs_where_no_sequence_is_left():
 
 
 # few sequences: equal parts, with every number of tiles of rows
-@pytest.mark.parametrize("n,Hq", [(8, 32), (8, 16), (4, 20), (5, 7), (2, 9)])
+@pytest.mark.parametrize("n,Hq", [(8, 31), (8, 15), (4, 20), (5, 7), (2, 9)])
 @pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
 def test_parts_of_many_rows(n, Hq, D):
     check([1700, 9, 0, 600], n, Hq, 1, D, seed=Hq + D)

@@ -16,9 +16,9 @@ F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 
 def rows(g, T, Hk, D, xt):
     """k and v as slices of a stacked product's rows, with loud channels."""
-    x = qmm_synth.activations(g, T, (3 * Hk) * D, 0.02) * (1 + 4 * (g.random(3 * Hk * D) < 0.03)).astype(np.float32)
-    x = dev(x).to(xt).view(T, 3 * Hk, D)
-    return x[:, Hk:2 * Hk], x[:, 2 * Hk:]
+    x = qmm_synth.activations(g, T, (3 * Hk + 1) * D, 0.02) * (1 + 4 * (g.random((3 * Hk + 1) * D) < 0.03)).astype(np.float32)
+    x = dev(x).to(xt).view(T, 3 * Hk + 1, D)
+    return x[:, Hk:2 * Hk], x[:, 2 * Hk:3 * Hk]
 
 
 def check(T, Hk, D, page, xt=F32, rot=None, interleaved=False, seed=1, slots=None, pages=None, kv=None):
