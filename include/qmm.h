@@ -51,7 +51,7 @@ typedef enum qmm_status {
     QMM_OK = 0,
     QMM_ERR_NULL = -1,        /* a required pointer is NULL                      */
     QMM_ERR_SHAPE = -2,       /* a size is out of range or not a block multiple  */
-    QMM_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned                */
+    QMM_ERR_ALIGN = -3,       /* a pointer is not aligned (to 16 bytes)            */
     QMM_ERR_WORKSPACE = -4,   /* workspace smaller than qmm_workspace_bytes()    */
     QMM_ERR_HIP = -5,         /* the HIP runtime reported an error               */
     QMM_ERR_UNSUPPORTED = -6, /* unknown format / operation code                 */
@@ -411,7 +411,9 @@ int swiglu_q8_1(const float* g_u, void* hq, int64_t R, int64_t F, void* stream);
  * [T][stride] with a token's heads next to each other from its first value
  * on; a stride is a count of values, at least heads * D, a multiple of 8 and
  * below 2^24, so that slices of the stacked product's rows are taken as they
- * are (each pointer 16-byte aligned).  Other buffers have no gaps.
+ * are (each pointer 16-byte aligned).  Other buffers have no gaps; lists of
+ * whole numbers (positions, slots, table, lens, cu_q, cu_k) need the alignment
+ * of their type only, so that parts of them can be passed.
  *
  * Rotation tables are fp32 [P][rot]: row p holds rot/2 cosines, then rot/2
  * sines, of the angles at position p.  Pair i of a head, at angle i, is values

@@ -614,8 +614,8 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
   if (B == 0 || Tq == 0) return QMM_OK;
   const size_t need = attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D);
   if (!q || !cu_q || !cu_k || !y || (Tk > 0 && (!k || !v)) || (need > 0 && !ws)) return QMM_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cu_q) || !aligned16(cu_k) || !aligned16(y) ||
-      !aligned16(ws))
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned_list(cu_q, 4) || !aligned_list(cu_k, 4) ||
+      !aligned16(y) || !aligned16(ws))
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
   const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);

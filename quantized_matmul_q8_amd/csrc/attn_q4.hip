@@ -713,7 +713,7 @@ extern "C" int attn_q4(const void* q, int64_t q_stride, int type, const void* ca
   if (B == 0) return QMM_OK;
   const size_t need = attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page);
   if (!q || !cache || !table || !lens || !y || (need > 0 && !ws)) return QMM_ERR_NULL;
-  if (!aligned16(q) || !aligned16(cache) || !aligned16(table) || !aligned16(lens) || !aligned16(y) || !aligned16(ws))
+  if (!aligned16(q) || !aligned16(cache) || !aligned_list(table, 4) || !aligned_list(lens, 4) || !aligned16(y) || !aligned16(ws))
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
   const AttnQ4Plan p = attn_q4_plan(B, n, Hq, Hk, D, W * page);

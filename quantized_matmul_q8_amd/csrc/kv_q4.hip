@@ -11,8 +11,8 @@
 //
 // Reading is bound by HBM: 65536 x 8 x 128 to bf16, 353 MB: 60 us, 5.9 TB/s (with
 // stores through the caches 91; with loads past them, which several lanes' share
-// of a line forbids, 95).  Appending by its instructions, 23 a value: 8192 x 8 x
-// 128, 44 MB: 14.4 us, 11 of them VALU time; read back to f16 9.5.
+// of a line forbids, 95).  Appending by its instructions, 21 a value: 8192 x 8 x
+// 128, 44 MB: 14.4 us, 10 of them VALU time; read back to f16 9.5.
 #include "kv_q4.hpp"
 
 #include <algorithm>
@@ -291,8 +291,8 @@ extern "C" int kv_append_q4(const void* k, int64_t k_stride, int k_type, const v
   if (rot < 0 || rot % 16 != 0 || rot > D || (rot > 0 && (P < 1 || P > 0x7fffffff))) return QMM_ERR_SHAPE;
   if (T == 0) return QMM_OK;
   if (!k || !v || !slots || !cache || (rot > 0 && (!rope || !positions))) return QMM_ERR_NULL;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(cache) || !aligned16(rope) ||
-      !aligned16(positions))
+  if (!aligned16(k) || !aligned16(v) || !aligned_list(slots, 8) || !aligned16(cache) || !aligned16(rope) ||
+      !aligned_list(positions, 4))
     return QMM_ERR_ALIGN;
   const int lanes = row_lanes_of(D);
   int heads;
@@ -313,7 +313,7 @@ extern "C" int kv_read_q4(const void* cache, int64_t pages, int64_t page, const 
   if (!kv_q4_shape(pages, page, Hk, D) || T < 0 || T >= kMostRows || T > 0x7fffffff / Hk) return QMM_ERR_SHAPE;
   if (T == 0) return QMM_OK;
   if (!cache || !slots || !k || !v) return QMM_ERR_NULL;
-  if (!aligned16(cache) || !aligned16(slots) || !aligned16(k) || !aligned16(v)) return QMM_ERR_ALIGN;
+  if (!aligned16(cache) || !aligned_list(slots, 8) || !aligned16(k) || !aligned16(v)) return QMM_ERR_ALIGN;
   const int lanes = row_lanes_of(D);
   int heads;
   const dim3 g = kv_grid(T, Hk, lanes, heads), blk(256);

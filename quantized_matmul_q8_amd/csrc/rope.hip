@@ -169,7 +169,7 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   if (T == 0) return QMM_OK;
   if (!q || !q_out || (k && !k_out) || (rot > 0 && (!rope || !positions))) return QMM_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(rope) ||
-      !aligned16(positions) || !aligned16(q_out) || !aligned16(k_out))
+      !aligned_list(positions, 4) || !aligned16(q_out) || !aligned16(k_out))
     return QMM_ERR_ALIGN;
   int lanes = 2;
   while (lanes * 16 < D) lanes *= 2;

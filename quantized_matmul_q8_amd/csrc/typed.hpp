@@ -11,6 +11,9 @@ inline bool strided_rows(int64_t stride, int64_t heads, int64_t D) {
   return stride >= heads * D && stride % 8 == 0 && stride < (int64_t{1} << 24);
 }
 
+// Lists of whole numbers are read one at a time, so any part of one may be passed.
+inline bool aligned_list(const void* p, uintptr_t size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
 // Tokens of a call, 32 lanes or a wave each: a grid has to stay below 2^32 of them.
 constexpr int64_t kMostRows = int64_t{1} << 26;
 

@@ -288,3 +288,23 @@ def test_padded_batch():
                  torch.empty(max(16, need), dtype=torch.uint8, device=DEV))
     assert torch.equal(layer.cache, cache)
     assert torch.equal(o5["y"][:3], small["y"]) and not o5["y"][3:].any() and torch.equal(o5["out"][:3], small["out"])
+
+
+def test_parts_of_lists():
+    # lists of whole numbers from any entry on: a chunk's positions and slots, a batch's last sequences
+    g = qmm_synth.rng(40)
+    T, n = 70, 1
+    x = dev(qmm_synth.activations(g, T, (HQ + 2 * HK) * D)).half().view(T, -1, D)
+    q, k, v = x[:, :HQ], x[:, HQ:HQ + HK], x[:, HQ + HK:]
+    table = dev(oracle.rope_table(200, D))
+    pos, slots = dev(g.integers(0, 200, T).astype(np.int32)), dev(g.permutation(96)[:T].astype(np.int64))
+    seqs, lens = dev(g.permutation(6).reshape(3, 2).astype(np.int32)), dev(np.array([5, 31, 17], np.int32))
+    cu = dev(np.array([0, 3, 10, 40, 70], np.int32))
+    caches = []
+    for at in (lambda t, i: t[i:], lambda t, i: t[i:].clone()):
+        cache = qmm.kv_cache_q4(6, 16, HK, D, DEV)
+        qmm.kv_append_q4(k[1:], v[1:], cache, at(slots, 1), rope=table, positions=at(pos, 1))
+        caches.append((cache, *qmm.kv_read_q4(cache, at(slots, 3)), *qmm.qk_norm_rope(q[3:], k[3:], table, at(pos, 3)),
+                       qmm.attn_q4(q[:2 * n].view(2, n, HQ, D), cache, at(seqs, 1), at(lens, 1)),
+                       qmm.attn_prompt(q, k, v, at(cu, 1))[3:]))
+    assert all(torch.equal(a, b) for a, b in zip(*caches))

@@ -142,7 +142,12 @@ def test_split_keys_that_are_not_seen_have_no_influence(D, xt):
                 k2[:L - n - window + 1], v2[:L - n - window + 1] = inf, nan
                 y = qmm.attn_prompt(q, k2, v2, cu([n]), cu([L]), window=window)
                 assert torch.equal(y[:cut + 1 - (L - n)], clean[:cut + 1 - (L - n)]), (window, cut)
-    # what is seen shows
+    # what is seen shows, from any split; the scale makes terms of about one size
+    for at in (5, L // 2, L - n):
+        v2 = v.clone()
+        v2[at, 0, 3], v2[at, 1, 7] = inf, -inf
+        y = qmm.attn_prompt(q, k, v2, cu([n]), cu([L]), scale=1e-3)
+        assert torch.all(y[:, :2, 3] == inf) and torch.all(y[:, 2:, 7] == -inf), at
     v2 = v.clone()
     v2[5, 0, 3], v2[900, 1, 7] = inf, nan
     clean, y = qmm.attn_prompt(q, k, v, cu([n]), cu([L])), qmm.attn_prompt(q, k, v2, cu([n]), cu([L]))
