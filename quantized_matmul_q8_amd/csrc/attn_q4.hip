@@ -15,7 +15,8 @@
 // that is exact, and one fma: the numbers that the format stands for.
 //
 // How the work is dealt out (the host knows no lengths):
-//   short sequences  a workgroup of eight waves takes a sequence and head whole
+//   short sequences  a workgroup of eight waves takes a sequence and head whole,
+//                    or, where these are few, some blocks of its values
 //   few of them      each is cut into as many equal parts as fill the chip
 //   many             the steps of all are dealt out to a fixed number of
 //                    workgroups in equal runs, found from the lengths by each,
@@ -28,7 +29,7 @@
 // the join, 5.5 TB/s; the loads alone take 65, the instructions alone 50 (of
 // about 300 a step and wave 128 make the values, as few as the format allows).
 // 671 MB in sequences of one length: 115 us, 5.8 TB/s.  A short sequence is bound
-// by one CU's instructions, 1 x 1000: 10 us.
+// by one CU's instructions, 1 x 1000: 8.6 us.
 #include "attn.hpp"
 #include "kv_q4.hpp"
 
@@ -102,13 +103,13 @@ struct Runs {
   static constexpr int kQuads = NB / 4, kPair = (NB % 4) / 2, kOne = NB % 2, kScales = kQuads + kPair + kOne;
 };
 
-// One cell as loaded: this lane's key codes, their scales, the value codes, and its part of the values' scales.
-template <int NB>
+// One cell as loaded: this lane's key codes, their scales, the value codes of VB blocks, and its part of their scales.
+template <int NB, int VB>
 struct Cell {
-  static constexpr int kVs = (4 * NB + 15) / 16;
-  uint32_t k[NB], ks[Runs<NB>::kScales], v[NB], vs[kVs];
+  static constexpr int kVs = (4 * VB + 15) / 16;
+  uint32_t k[NB], ks[Runs<NB>::kScales], v[VB], vs[kVs];
 
-  __device__ __forceinline__ void load(const uint8_t* cell, int lane) {
+  __device__ __forceinline__ void load(const uint8_t* cell, int lane, int block) {
     constexpr int D = 32 * NB;
     const int key = lane & 15, c = lane >> 4;
 #pragma unroll
@@ -127,14 +128,14 @@ struct Cell {
       k[NB - 1] = ld4_nt(cell + ((NB - 1) * 16 + key) * 16 + c * 4);
       ks[Runs<NB>::kScales - 1] = ld4_nt(cell + 8 * D + ((NB - 1) * 16 + key) * 4);
     }
-    const uint8_t* values = cell + 10 * D + lane * (4 * NB);
+    const uint8_t* values = cell + 10 * D + lane * (4 * NB) + 4 * block;
 #pragma unroll
-    for (int b = 0; b < NB;) {
-      if constexpr (NB % 4 == 0) {
+    for (int b = 0; b < VB;) {
+      if constexpr (VB % 4 == 0) {
         const uint4 x = ld16_nt(values + 4 * b);
         v[b] = x.x, v[b + 1] = x.y, v[b + 2] = x.z, v[b + 3] = x.w;
         b += 4;
-      } else if constexpr (NB % 2 == 0) {
+      } else if constexpr (VB % 2 == 0) {
         const uint2 x = ld8_nt(values + 4 * b);
         v[b] = x.x, v[b + 1] = x.y;
         b += 2;
@@ -145,7 +146,7 @@ struct Cell {
     }
 #pragma unroll
     for (int r = 0; r < kVs; ++r) {
-      const int at = min(r * 16 + key, 4 * NB - 1);
+      const int at = 4 * block + min(r * 16 + key, 4 * VB - 1);
       vs[r] = ld4_nt(cell + 18 * D + (c * (4 * NB) + at) * 4);
     }
   }
@@ -206,9 +207,8 @@ __device__ __forceinline__ int operand_dim(int j, int c) {
   return (NB - 1) * 32 + c * 8;
 }
 
-template <int NB, int RT, int b = 0>
-__device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (&p)[RT],
-                                           v4f (&o)[RT][2 * NB]) {
+template <int NB, int VB, int RT, int b = 0>
+__device__ __forceinline__ void add_values(const Cell<NB, VB> (&cell)[2], const h8 (&p)[RT], v4f (&o)[RT][2 * VB]) {
   h2 l0[2], u0[2], l1[2], u1[2];
   cell[0].template value_operands<b>(l0, u0);
   cell[1].template value_operands<b>(l1, u1);
@@ -218,7 +218,7 @@ __device__ __forceinline__ void add_values(const Cell<NB> (&cell)[2], const h8 (
     o[r][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(low, p[r], o[r][2 * b], 0, 0, 0);
     o[r][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(high, p[r], o[r][2 * b + 1], 0, 0, 0);
   }
-  if constexpr (b + 1 < NB) add_values<NB, RT, b + 1>(cell, p, o);
+  if constexpr (b + 1 < VB) add_values<NB, VB, RT, b + 1>(cell, p, o);
 }
 
 // A sequence's length, and the first key that any of its queries sees, in whole steps.
@@ -283,9 +283,9 @@ __device__ __forceinline__ int64_t run_steps(const AttnQ4Args& a, int64_t total)
   return max(static_cast<int64_t>(a.least), quotient(total + a.groups - 1, a.groups));
 }
 
-template <int NB, int RT, int kWaves>
+template <int VB, int kWaves>
 struct AttnQ4Shared {
-  float o[kWaves][16][32 * NB + 4];
+  float o[kWaves][16][32 * VB + 4];
   float m[kWaves][16], l[kWaves][16];
 };
 
@@ -294,13 +294,14 @@ struct Segment {
   int seq, kh, row_block, from, to;
   int64_t slot;
   Extent ext;
+  int block = 0;  // the first of the values' blocks
 };
 
 // One segment after the other: next(s) moves s to the one behind it and tells
 // whether there is one.  Its first loads begin before the results of the one
 // before are joined and written.
-template <int NB, int RT, int kWaves, typename Next>
-__device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB, RT, kWaves>& sh, Segment seg,
+template <int NB, int VB, int RT, int kWaves, typename Next>
+__device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB, kWaves>& sh, Segment seg,
                                             const Next& next) {
   constexpr int D = 32 * NB;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -313,7 +314,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
 
   // one step's two cells and their page numbers
   struct Step {
-    Cell<NB> cell[2];
+    Cell<NB, VB> cell[2];
     int page[2];
   };
   // of the segment whose loads are under way
@@ -329,7 +330,8 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
     for (uint32_t u = 0; u < 2; ++u) {
       const uint32_t cell = min(static_cast<uint32_t>(t) / kCellTokens + u, last_cell);
       const uint32_t pg = there(page[u]) ? page[u] : 0;
-      s.cell[u].load(head + pg * page_bytes + (cell - page_of(cell) * a.cells) * static_cast<uint32_t>(cell_bytes), lane);
+      s.cell[u].load(head + pg * page_bytes + (cell - page_of(cell) * a.cells) * static_cast<uint32_t>(cell_bytes), lane,
+                     seg.block);
       s.page[u] = page[u];
     }
   };
@@ -408,14 +410,14 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
       mul[r] = mul[r] == 0.0f ? 1.0f : mul[r];
     }
 
-    v4f o[RT][2 * NB];
+    v4f o[RT][2 * VB];
     // the largest product so far, what is added to a product's exponent for it, and this lane's part of the sum
     float top[RT], base[RT], sum[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       top[r] = -INFINITY, base[r] = kLift, sum[r] = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2 * NB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int b = 0; b < 2 * VB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
     const auto work = [&](Step& st, int t) {
@@ -459,7 +461,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
           const float keep = __builtin_amdgcn_exp2f((top[r] - (most == -INFINITY ? 0.0f : most)) * mul[r]);
           sum[r] *= keep;
 #pragma unroll
-          for (int b = 0; b < 2 * NB; ++b) o[r][b] *= keep;
+          for (int b = 0; b < 2 * VB; ++b) o[r][b] *= keep;
           top[r] = most;
           base[r] = kLift - (most == -INFINITY ? 0.0f : most) * mul[r];
         }
@@ -470,7 +472,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
           p[r][(k & 4) + kv_quad_byte(k & 3)] = static_cast<_Float16>(e);
         }
       }
-      add_values<NB, RT>(st.cell, p, o);
+      add_values<NB, VB, RT>(st.cell, p, o);
     };
 
     if (t < end) {
@@ -500,11 +502,11 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
       const float l = rows_sum(sum[r]);
       if (c == 0) sh.m[wave][col] = top[r] * mul[r], sh.l[wave][col] = l;
 #pragma unroll
-      for (int b = 0; b < 2 * NB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
+      for (int b = 0; b < 2 * VB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
       __syncthreads();
       const int row0 = (done.row_block * RT + r) * 16, rows = min(16, a.rows - row0);
-      for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
-        const int row = x / (D / 4), d = x % (D / 4) * 4;
+      for (int x = threadIdx.x; x < rows * (8 * VB); x += 64 * kWaves) {
+        const int row = x / (8 * VB), d = x % (8 * VB) * 4;
         float m = sh.m[0][row];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
@@ -526,7 +528,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
           const int i = (row0 + row) / a.group, h = done.kh * a.group + (row0 + row) % a.group;
           const int64_t out = (static_cast<int64_t>(done.seq) * a.n + i) * a.Hq + h;
           y *= total == 0.0f ? 0.0f : 1.0f / total;
-          store4(a.y_type, a.y, (out * D + d) / 4, make_float4(y.x, y.y, y.z, y.w));
+          store4(a.y_type, a.y, (out * D + 32 * done.block + d) / 4, make_float4(y.x, y.y, y.z, y.w));
         }
       }
       __syncthreads();
@@ -535,14 +537,15 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<NB
   }
 }
 
-// One workgroup for each sequence, key head and row block: no partial results.
-template <int NB, int RT, int kWaves>
+// One workgroup for each sequence, key head and VB blocks of the values (which vary slowest): no partial results.
+template <int NB, int VB, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_q4_kernel(AttnQ4Args a) {
-  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
-  const int row_block = blockIdx.x % a.row_blocks, kh = blockIdx.x / a.row_blocks % a.Hk;
-  const int seq = blockIdx.x / a.row_blocks / a.Hk;
+  __shared__ AttnQ4Shared<VB, kWaves> sh;
+  const unsigned items = static_cast<unsigned>(a.B) * a.Hk, item = blockIdx.x % items, part = blockIdx.x / items;
+  const int kh = item % a.Hk, seq = item / a.Hk;
   const Extent e = extent_of(a, as_scalar(a.lens)[seq]);
-  attn_q4_run<NB, RT, kWaves>(a, sh, Segment{seq, kh, row_block, 0, e.steps, -1, e}, [](Segment&) { return false; });
+  attn_q4_run<NB, VB, 1, kWaves>(a, sh, Segment{seq, kh, 0, 0, e.steps, -1, e, static_cast<int>(part) * VB},
+                                 [](Segment&) { return false; });
 }
 
 // The parts of a sequence of so many steps.
@@ -551,7 +554,7 @@ __device__ __forceinline__ int parts_of(const AttnQ4Args& a, int steps) { return
 // Equal parts of a sequence and head each.  The parts vary slowest: the first ones, which every sequence has, over all dies.
 template <int NB, int RT, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a) {
-  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
+  __shared__ AttnQ4Shared<NB, kWaves> sh;
   const unsigned heads = a.Hk * a.row_blocks, items = a.B * heads, item = blockIdx.x % items, seq = item / heads;
   const int part = blockIdx.x / items, head = item % heads;
   const Extent e = extent_of(a, as_scalar(a.lens)[seq]);
@@ -559,7 +562,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a
   if (part >= parts) return;
   const int each = static_cast<unsigned>(e.steps) / parts, more = e.steps - each * parts;  // the first ones have one more
   const int from = part * each + min(part, more), to = from + each + (part < more ? 1 : 0);
-  attn_q4_run<NB, RT, kWaves>(a, sh,
+  attn_q4_run<NB, NB, RT, kWaves>(a, sh,
                               Segment{static_cast<int>(seq), head / a.row_blocks, head % a.row_blocks, from, to,
                                       parts == 1 ? -1 : int64_t{blockIdx.x}, e},
                               [](Segment&) { return false; });
@@ -568,7 +571,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a
 // Equal runs of the steps of all.
 template <int NB, int RT, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a) {
-  __shared__ AttnQ4Shared<NB, RT, kWaves> sh;
+  __shared__ AttnQ4Shared<NB, kWaves> sh;
   const int lane = threadIdx.x & 63, heads = a.Hk * a.row_blocks;
   int before;
   const int64_t total = static_cast<int64_t>(total_steps(a, lane, 0, before)) * heads, per = run_steps(a, total);
@@ -587,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a)
     left -= to - from;
     return Segment{seq, head / a.row_blocks, head % a.row_blocks, from, to, from == 0 && to == e.steps ? -1 : slot, e};
   };
-  attn_q4_run<NB, RT, kWaves>(a, sh, segment(seq0, e, from), [&](Segment& s) {
+  attn_q4_run<NB, NB, RT, kWaves>(a, sh, segment(seq0, e, from), [&](Segment& s) {
     if (left == 0) return false;
     slot = 2 * int64_t{blockIdx.x} + 1;  // the last one's, should it not be whole
     int seq = s.seq;
@@ -640,14 +643,19 @@ struct AttnQ4Plan {
   int64_t slots;
 };
 
-// The longest sequences that are taken whole, in tokens: one launch.  1 x 1000,
-// 32/8 heads of 128: 9.7 us in a graph and 10.7 us a call by itself; as parts
-// 8.5 and 14.3; 32 x 1000: 12.1 and, as parts, 16.2 in a graph.
+// The longest sequences that are taken whole, in tokens: one launch.  32/8 heads
+// of 128, 1 x 1000: 8.6 us in a graph and 10 a call by itself; as parts 8.5 and
+// 14.3; 32 x 1000: 11.8 and, as parts, 16.2 in a graph; 1 x 2000: 12.1 and 9.6.
 constexpr int64_t kWhole = 1024;
 // Two workgroups per CU.  With three 64 x 8192 in pages of 16 takes 79 us for 84, in pages of 64 75 for 73, and 64 rows a
 // key head (16 x 4096, 8 tokens) 75 for 62.
 constexpr int kGroups = 512;
-constexpr int kLeast = 8;          // steps: two a wave
+constexpr int kLeast = 8;  // steps: two a wave
+// Whole sequences that leave most CUs without work: one workgroup for each block
+// or two of the values, all of which find the scores for themselves.  1 x 1000,
+// 32/8 heads of 128: 8.6 us, in one workgroup per key head 10.2; 32/4 of 256: 12.3
+// and 17.0.  With 16 waves 9.3 and (spilt) 24.6.
+constexpr unsigned kFew = 256;
 
 static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   AttnQ4Plan p{4, 1, 1, 0, 0, 0, 0};
@@ -680,15 +688,25 @@ template <int NB>
 static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, hipStream_t st) {
   const unsigned items = static_cast<unsigned>(a.B) * a.Hk * a.row_blocks;
   const dim3 g(p.groups ? static_cast<unsigned>(p.groups) : items * p.parts);
-  if (p.waves == 8) hipLaunchKernelGGL((attn_q4_kernel<NB, 1, 8>), dim3(items), dim3(512), 0, st, a);
-  else if (p.tiles == 1) launch_split<NB, 1>(a, g, st);
-  else if (p.tiles == 2 || NB > 4) launch_split<NB, 2>(a, g, st);
-  else launch_split<NB, NB <= 4 ? 4 : 2>(a, g, st);
+  constexpr int VB = NB <= 4 ? 1 : 2;
+  if (p.waves == 8) {
+    if (items * (NB / VB) <= kFew)
+      hipLaunchKernelGGL((attn_q4_kernel<NB, VB, 8>), dim3(items * (NB / VB)), dim3(512), 0, st, a);
+    else
+      hipLaunchKernelGGL((attn_q4_kernel<NB, NB, 8>), dim3(items), dim3(512), 0, st, a);
+  } else if (p.tiles == 1) {
+    launch_split<NB, 1>(a, g, st);
+  } else if (p.tiles == 2 || NB > 4) {
+    launch_split<NB, 2>(a, g, st);
+  } else {
+    launch_split<NB, NB <= 4 ? 4 : 2>(a, g, st);
+  }
 }
 
+// A grid has to stay below 2^32 lanes, with up to 512 a sequence and key head.
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   return B >= 0 && n >= 1 && n <= QMM_ATTN_MAX_N && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
-         attn_head_dim(D) && max_len >= 1 && max_len <= kMostTokens && B < (int64_t{1} << 26) / (n * Hq) &&
+         attn_head_dim(D) && max_len >= 1 && max_len <= kMostTokens && B < (int64_t{1} << 23) / (n * Hq) &&
          B * ((max_len + kStep - 1) / kStep + 1) < (int64_t{1} << 31);
 }
 

@@ -87,7 +87,7 @@ def test_cached_attention_errors():
     assert cached(t=F32) == UNSUP and cached(t=3) == UNSUP and cached(yt=4) == UNSUP
     for kw in (dict(qs=504), dict(qs=513), dict(page=20), dict(pages=0), dict(W=0), dict(W=1 << 27), dict(B=-1), dict(n=0),
                dict(n=9), dict(Hq=6), dict(Hq=2), dict(Hk=0), dict(Hq=1028, qs=1 << 17), dict(D=72), dict(sc=float("inf")),
-               dict(sc=float("nan")), dict(win=-1), dict(win=HUGE), dict(B=1 << 23),
+               dict(sc=float("nan")), dict(win=-1), dict(win=HUGE), dict(B=1 << 20),
                dict(B=1 << 11, W=1 << 21)):
         assert cached(**kw) == SHAPE, kw
     for p in ("q", "c", "tab", "lens", "y"):

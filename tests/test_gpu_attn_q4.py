@@ -116,6 +116,13 @@ def test_windows(window):
     check([400, 5, 256], 5, 4, 2, 64, 32, BF16, window=window, seed=window % 1000 + 1)
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+def test_short_sequences_of_a_large_batch(D):
+    g = qmm_synth.rng(D)
+    check([int(x) for x in g.integers(0, 70, 130)], 1, 4, 2, D, seed=D + 7)
+    check([int(x) for x in g.integers(0, 40, 140)], 3, 6, 2, D, 32, BF16, F32, window=9, seed=D + 8)
+
+
 @pytest.mark.parametrize("n", [1, 4])
 def test_long_sequences(n):
     check([5000, 17, 2100], n, 8, 2, 128, 64, seed=30 + n)
