@@ -11,8 +11,10 @@
 //
 // Reading is bound by HBM: 65536 x 8 x 128 to bf16, 353 MB: 60 us, 5.9 TB/s (with
 // stores through the caches 91; with loads past them, which several lanes' share
-// of a line forbids, 95).  Appending by its instructions, 21 a value: 8192 x 8 x
-// 128, 44 MB: 14.4 us, 10 of them VALU time; read back to f16 9.5.
+// of a line forbids, 95).  So is appending from some ten thousand tokens on: 32768
+// x 8 x 128, 176 MB, turned: 38 us, as they are 32; at 8192, 44 MB, 14.2 and 11.7,
+// of which 5 are the launch and the first loads (slot, position, table, values).
+// Its instructions, 20 a value, take 10 of the 14.2 and overlap.
 #include "kv_q4.hpp"
 
 #include <algorithm>
@@ -88,20 +90,13 @@ struct Block8 {
     dm = db | mb << 16;
   }
 
-  // 1.5 * 2^23 + code j: rounds to the nearest even and leaves the code in the low bits
-  __device__ __forceinline__ uint32_t code(int j) const {
+  // Code j into a byte of a dword: the conversion rounds to the nearest even and takes what is below 0 as that.
+  __device__ __forceinline__ uint32_t code(int j, int byte, uint32_t word) const {
 #pragma clang fp contract(off)
     const float p = (v[j] - m) * inv;
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(p, 0.0f, 15.0f) + kMagic);
+    return __builtin_amdgcn_cvt_pk_u8_f32(fminf(p, 15.0f), byte, word);
   }
 };
-
-// Sums of kMagicBits << 4i over what a dword of codes joins, modulo 2^32.
-constexpr uint32_t magic_at(uint32_t step, int count) {
-  uint32_t s = 0;
-  for (int i = 0; i < count; ++i) s += kMagicBits << (step * i);
-  return s;
-}
 
 template <int KT, int VT>
 __global__ __launch_bounds__(256) void kv_append_q4_kernel(AppendArgs a) {
@@ -130,13 +125,17 @@ __global__ __launch_bounds__(256) void kv_append_q4_kernel(AppendArgs a) {
       }
     }
   }
+  Raw8<KT> key, next_key;
+  Raw8<VT> val, next_val;
+  const auto load = [&](int h) {
+    if (!on || h >= w.h1) return;
+    next_key.load(a.x[0], (t * a.stride[0] + static_cast<int64_t>(h) * a.D) / 8 + j);
+    next_val.load(a.x[1], (t * a.stride[1] + static_cast<int64_t>(h) * a.D) / 8 + j);
+  };
+  load(w.h0);
   for (int h = w.h0; h < w.h1; ++h) {
-    Raw8<KT> key;
-    Raw8<VT> val;
-    if (on) {
-      key.load(a.x[0], (t * a.stride[0] + static_cast<int64_t>(h) * a.D) / 8 + j);
-      val.load(a.x[1], (t * a.stride[1] + static_cast<int64_t>(h) * a.D) / 8 + j);
-    }
+    key = next_key, val = next_val;
+    load(h + 1);
     Block8 k, v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) k.v[i] = on ? key.get(i) : 0.0f, v.v[i] = on ? val.get(i) : 0.0f;
@@ -161,14 +160,15 @@ __global__ __launch_bounds__(256) void kv_append_q4_kernel(AppendArgs a) {
     }
     k.scales();
     v.scales();
-    // The key's codes 0, 2, 4, 6, 1, 3, 5, 7 from the low end on.  The value's in bytes, 0 to 3 and 4 to 7: a byte of the
+    // The key's codes 0, 2, 4, 6, 1, 3, 5, 7 from the low end on.  The value's 0 to 3 and 4 to 7 as bytes: a byte of the
     // cache joins dims c and c + 16 of a block, so this lane's and those of the lane two further, half of them each.
-    uint32_t kc = 0, v03 = 0, v47 = 0;
+    uint32_t k0415 = 0, k2637 = 0, v03 = 0, v47 = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) kc += k.code(i) << (4 * ((i & 1) * 4 + (i >> 1)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v03 += v.code(i) << (8 * i), v47 += v.code(4 + i) << (8 * i);
-    kc -= magic_at(4, 8), v03 -= magic_at(8, 4), v47 -= magic_at(8, 4);
+    for (int i = 0; i < 4; ++i) {
+      k0415 = k.code(4 * (i & 1) + (i >> 1), i, k0415), k2637 = k.code(4 * (i & 1) + (i >> 1) + 2, i, k2637);
+      v03 = v.code(i, i, v03), v47 = v.code(4 + i, i, v47);
+    }
+    const uint32_t kc = k0415 | k2637 << 4;
     const uint32_t other = static_cast<uint32_t>(lane8_xchg<0x4e>(static_cast<int>(part < 2 ? v47 : v03)));
     const uint32_t vc = part < 2 ? v03 | other << 4 : other | v47 << 4;
     if (!on) continue;
@@ -224,18 +224,26 @@ __global__ __launch_bounds__(256) void kv_read_q4_kernel(ReadArgs a) {
   const int c0 = (part & 1) * 8 + (part >> 1) * 4;
   const int64_t cell0 = there ? kv_cell(slot, a.page, a.shift, 0, a.Hk, a.D) : 0;
   const int64_t head_bytes = a.page / kCellTokens * (20 * a.D);
-  for (int h = w.h0; h < w.h1; ++h) {
-    uint32_t kw = 0, kd = 0, vw = 0, d = 0, m = 0;
-    if (there) {
-      const uint8_t* cell = a.cache + cell0 + h * head_bytes;
-      kw = *reinterpret_cast<const uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4);
-      kd = *reinterpret_cast<const uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4);
-      const uint8_t* from = cell + 10 * a.D + ((quad * 16 + c0) * nb + b) * 4 + kv_quad_byte(tok & 3);
+  struct Raw {
+    uint32_t kw = 0, kd = 0, v[4] = {0, 0, 0, 0}, d = 0, m = 0;
+  } next;
+  const auto load = [&](int h) {
+    if (!there || h >= w.h1) return;
+    const uint8_t* cell = a.cache + cell0 + h * head_bytes;
+    next.kw = *reinterpret_cast<const uint32_t*>(cell + (b * kCellTokens + tok) * 16 + part * 4);
+    next.kd = *reinterpret_cast<const uint32_t*>(cell + 8 * a.D + (b * kCellTokens + tok) * 4);
+    const uint8_t* from = cell + 10 * a.D + ((quad * 16 + c0) * nb + b) * 4 + kv_quad_byte(tok & 3);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vw |= static_cast<uint32_t>(from[i * nb * 4]) << (8 * i);
-      const uint8_t* vs = cell + 18 * a.D + (quad * nb + b) * 16 + (tok & 3) * 2;
-      d = ld_u16(vs), m = ld_u16(vs + 8);
-    }
+    for (int i = 0; i < 4; ++i) next.v[i] = from[i * nb * 4];
+    const uint8_t* vs = cell + 18 * a.D + (quad * nb + b) * 16 + (tok & 3) * 2;
+    next.d = ld_u16(vs), next.m = ld_u16(vs + 8);
+  };
+  load(w.h0);
+  for (int h = w.h0; h < w.h1; ++h) {
+    const Raw now = next;
+    load(h + 1);
+    const uint32_t kw = now.kw, kd = now.kd, d = now.d, m = now.m;
+    const uint32_t vw = now.v[0] | now.v[1] << 8 | now.v[2] << 16 | now.v[3] << 24;
     // bytes of dims c and c + 16: this lane keeps its own dims' codes and takes the rest from the lane two further
     const uint32_t low = vw & 0x0f0f0f0fu, high = (vw >> 4) & 0x0f0f0f0fu;
     const uint32_t other = static_cast<uint32_t>(lane8_xchg<0x4e>(static_cast<int>(part < 2 ? high : low)));
