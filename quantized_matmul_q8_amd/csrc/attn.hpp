@@ -42,6 +42,17 @@ __device__ __forceinline__ float halves_sum(float v) {
   return halves_join(v, [](float a, float b) { return a + b; });
 }
 
+// The sum over this lane and those before it, by moves within rows of 16 lanes and of their last lanes to the rows behind.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
 // One row of four dims per lane from `count` partial results: at `part` + step *
 // at(k) number k's sums of terms times values, in ml[at(k)] its maximum and sum
 // of terms.  The maxima and sums by the lanes, 64 at a time, then the partial

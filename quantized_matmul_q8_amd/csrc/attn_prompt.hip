@@ -117,12 +117,7 @@ __device__ __forceinline__ Place find_place(const PromptArgs& a, int n, int lane
     const int b = min(b0 + lane, a.B - 1);
     const int q0 = max(0, min(a.Tq, a.cu_q[b])), q1 = max(q0, min(a.Tq, a.cu_q[b + 1]));
     const int mine = b0 + lane < a.B ? ((q1 - q0) * a.group + kRows - 1) / kRows : 0;
-    int upto = mine;
-#pragma unroll
-    for (int k = 1; k < 64; k *= 2) {
-      const int o = __shfl_up(upto, k);
-      upto += lane >= k ? o : 0;
-    }
+    const int upto = wave_scan(mine);
     const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > n);
     if (past) {
       const int at = __builtin_ctzll(past);

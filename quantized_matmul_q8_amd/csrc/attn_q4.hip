@@ -237,13 +237,7 @@ __device__ __forceinline__ Extent extent_of(const AttnQ4Args& a, int32_t stored)
 // Steps of one head and row block, summed over sequences by a wave, 64 of them at a time.
 __device__ __forceinline__ int scan_steps(const AttnQ4Args& a, int b0, int lane, int& mine) {
   mine = b0 + lane < a.B ? extent_of(a, a.lens[min(b0 + lane, a.B - 1)]).steps : 0;
-  int upto = mine;
-#pragma unroll
-  for (int k = 1; k < 64; k *= 2) {
-    const int o = __shfl_up(upto, k);
-    upto += lane >= k ? o : 0;
-  }
-  return upto;
+  return wave_scan(mine);
 }
 // Of all sequences; `before`: of those before `seq`.
 __device__ __forceinline__ int total_steps(const AttnQ4Args& a, int lane, int seq, int& before) {
