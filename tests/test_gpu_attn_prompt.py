@@ -79,6 +79,18 @@ def test_packed_sequences_of_many_lengths():
     check([10, 1, 100], [300, 64, 100], Hq=4, Hk=2, seed=4)
 
 
+def test_groups_wider_than_a_tile():
+    check([3, 2, 1], Hq=200, Hk=1, D=64, seed=40)
+    check([2], [700], Hq=300, Hk=2, D=64, xt=F16, seed=41)
+    check([2], [600], Hq=1024, Hk=1, D=64, window=70, seed=42)
+
+
+def test_thousands_of_sequences():
+    g = qmm_synth.rng(43)
+    check([int(x) for x in g.integers(0, 3, 3000)], Hq=2, Hk=1, D=64, seed=43)
+    check([0] * 2500 + [70] + [0] * 300 + [1], Hq=2, Hk=1, D=64, xt=F16, seed=44)
+
+
 @pytest.mark.parametrize("yt", [F32, F16, BF16])
 @pytest.mark.parametrize("xt", [F16, BF16])
 def test_types(xt, yt):

@@ -87,6 +87,18 @@ def test_whole_tiles_of_rows(n, Hq):
         check([90, n, 35], n, Hq, 1, D, seed=n + D)
 
 
+def test_very_many_rows():
+    check([50, 7], 1, 1024, 1, 64, seed=70)
+    check([40, 1500], 8, 520, 2, 64, seed=71)
+    check([1200] * 3, 8, 130, 1, 256, 16, BF16, window=60, seed=72)
+
+
+def test_thousands_of_sequences():
+    g = qmm_synth.rng(73)
+    check([int(x) for x in g.integers(0, 4, 3000)], 1, 2, 1, 64, seed=73)
+    check([0] * 700 + [1100] + [1, 0, 2] * 100 + [0] * 30, 2, 2, 1, 64, seed=74)
+
+
 @pytest.mark.parametrize("n,Hq", [(8, 32), (8, 16), (4, 20), (5, 7)])
 def test_many_rows(n, Hq):
     for D in (64, 128, 256):
