@@ -116,6 +116,7 @@ __device__ __forceinline__ Place find_place(const PromptArgs& a, int n, int lane
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     const int b = min(b0 + lane, a.B - 1);
     const int q0 = max(0, min(a.Tq, a.cu_q[b])), q1 = max(q0, min(a.Tq, a.cu_q[b + 1]));
+    const int k0 = max(0, min(a.Tk, a.cu_k[b])), k1 = max(k0, min(a.Tk, a.cu_k[b + 1]));  // with these, not behind them
     const int mine = b0 + lane < a.B ? ((q1 - q0) * a.group + kRows - 1) / kRows : 0;
     const int upto = wave_scan(mine);
     const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > n);
@@ -125,9 +126,8 @@ __device__ __forceinline__ Place find_place(const PromptArgs& a, int n, int lane
       p.nq = __builtin_amdgcn_readlane(q1, at) - p.q0;
       // a sequence's last tiles, which see the most keys, first
       p.tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - n;
-      const int k0 = max(0, min(a.Tk, a.cu_k[b0 + at])), k1 = max(k0, min(a.Tk, a.cu_k[b0 + at + 1]));
-      p.k0 = __builtin_amdgcn_readfirstlane(k0);
-      p.nk = __builtin_amdgcn_readfirstlane(k1 - k0);
+      p.k0 = __builtin_amdgcn_readlane(k0, at);
+      p.nk = __builtin_amdgcn_readlane(k1, at) - p.k0;
       p.found = true;
       return p;
     }
@@ -555,21 +555,34 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int
   if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
 }
 
-// Workgroups that the chip holds at once: two per CU, one where D > 128 takes a wave's registers past half of them.
-constexpr int prompt_slots(int64_t D) { return D <= 128 ? 512 : 256; }
-
-// The most tiles that sequences of Tq tokens in all may have, and how many ways
-// their keys are split: as many as fill the chip once with the tiles of B
-// sequences of about one size, none below 256 keys of an average sequence.
+// The most tiles that sequences of Tq tokens in all may have, and how many ways their keys are split.
 struct PromptPlan {
   int64_t tiles, splits;
 };
-static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
+// A workgroup takes 1e-4 us per key and dim (0.82 us for 64 keys of 128, 0.78 for
+// 32 of 256).  With s splits that is divided by s, and partial results cost 3.5 us
+// for the second launch, 1.7e-6 us for each float, written and read, and 0.08 us a
+// split; the best s follows.  One workgroup per CU keeps the chip busy, more only
+// make more partial results.  Sequences count as of one size.  us, heads 32/8 x 128:
+//                  1 split  2     4     8     16    32    this
+//   512 of 512     17.4     26.7  29.0  42.5              17.5 (1)
+//   512 of 4608    70.9     55.9  57.5  68.1  95.0        56.9 (2)
+//   64 of 8192     115      66.5  41.2  30.4  27.4  36.7  27.0 (13)
+//   16 of 32768    421      219   116   65.4  41.2  35.5  35.9 (32)
+static PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t BN) {
+  constexpr double kPerKey = 1e-4, kJoin = 3.5, kPerFloat = 1.7e-6, kPerSplit = 0.08;
+  constexpr int64_t kCUs = 256, kMostSplits = 64;
   PromptPlan p;
   const int64_t rows = Tq * (Hq / Hk), whole = (rows + kRows - 1) / kRows;
   p.tiles = std::min(rows, whole + B);
-  const int64_t groups = std::max<int64_t>(1, whole + (B - 1) / 2) * Hk, keys = B > 0 ? Tk / B : 0;
-  p.splits = std::max<int64_t>(1, std::min<int64_t>({prompt_slots(D) / groups, keys / 256, 64}));
+  p.splits = 1;
+  const int64_t groups = std::max<int64_t>(1, whole + (B - 1) / 2) * Hk, key_tiles = B > 0 ? (Tk / B + BN - 1) / BN : 0;
+  const double alone = static_cast<double>(key_tiles * BN * D) * kPerKey;
+  const double each = static_cast<double>(Tq * Hq * D) * kPerFloat + kPerSplit;
+  int64_t s = std::min({static_cast<int64_t>(sqrt(alone / each)), kCUs / groups, key_tiles, kMostSplits});
+  if (s < 2) return p;
+  s = (key_tiles + (key_tiles + s - 1) / s - 1) / ((key_tiles + s - 1) / s);  // none without keys
+  if (alone / s + kJoin + each * s < alone) p.splits = s;
   return p;
 }
 
@@ -581,8 +594,12 @@ static bool prompt_shape(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t 
          attn_head_dim(D) && Tq < kMostTokens / Hq && B < kMostSequences / Hq;
 }
 
-template <int D, int BN>
+// Keys of a tile.
+constexpr int64_t tile_keys(int64_t D) { return D <= 128 ? 64 : 32; }
+
+template <int D>
 static void launch_prompt(const PromptArgs& a, bool bf16, dim3 g, hipStream_t st) {
+  constexpr int BN = static_cast<int>(tile_keys(D));
   if (bf16) hipLaunchKernelGGL((attn_prompt_kernel<D, BN, true>), g, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((attn_prompt_kernel<D, BN, false>), g, dim3(256), 0, st, a);
 }
@@ -593,7 +610,7 @@ using namespace qmm;
 
 extern "C" size_t attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
   if (!prompt_shape(B, Tq, Tk, Hq, Hk, D)) return 0;
-  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D, tile_keys(D));
   return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles * Hk * p.splits * kRows * (D + 2) * 4);
 }
 
@@ -613,7 +630,7 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
       !aligned16(y) || !aligned16(ws))
     return QMM_ERR_ALIGN;
   if (ws_bytes < need) return QMM_ERR_WORKSPACE;
-  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D);
+  const PromptPlan p = prompt_plan(B, Tq, Tk, Hq, Hk, D, tile_keys(D));
   const PromptArgs a{q, k, v, cu_q, cu_k, y, static_cast<float*>(ws), q_stride, k_stride, v_stride, scale,
                      static_cast<int>(std::min(window, kMostTokens)), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(B),
                      static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(Hq / Hk), static_cast<int>(p.splits),
@@ -621,11 +638,11 @@ extern "C" int attn_prompt(const void* q, int64_t q_stride, const void* k, int64
   const dim3 g(static_cast<unsigned>(p.tiles * Hk * p.splits));
   hipStream_t st = to_stream(stream);
   switch (D) {
-    case 64: launch_prompt<64, 64>(a, type == QMM_BF16, g, st); break;
-    case 96: launch_prompt<96, 64>(a, type == QMM_BF16, g, st); break;
-    case 128: launch_prompt<128, 64>(a, type == QMM_BF16, g, st); break;
-    case 192: launch_prompt<192, 32>(a, type == QMM_BF16, g, st); break;
-    default: launch_prompt<256, 32>(a, type == QMM_BF16, g, st); break;
+    case 64: launch_prompt<64>(a, type == QMM_BF16, g, st); break;
+    case 96: launch_prompt<96>(a, type == QMM_BF16, g, st); break;
+    case 128: launch_prompt<128>(a, type == QMM_BF16, g, st); break;
+    case 192: launch_prompt<192>(a, type == QMM_BF16, g, st); break;
+    default: launch_prompt<256>(a, type == QMM_BF16, g, st); break;
   }
   if (p.splits > 1)
     hipLaunchKernelGGL(attn_prompt_join_kernel, dim3(static_cast<unsigned>(p.tiles * Hk * (kRows / 4))), dim3(256), 0, st,
