@@ -644,7 +644,12 @@ constexpr int64_t kWhole = 1024;
 // Two workgroups per CU.  With three 64 x 8192 in pages of 16 takes 79 us for 84, in pages of 64 75 for 73, and 64 rows a
 // key head (16 x 4096, 8 tokens) 75 for 62.
 constexpr int kGroups = 512;
-constexpr int kLeast = 8;  // steps: two a wave
+constexpr int64_t kLeast = 8;  // steps: two a wave
+// Parts: one workgroup per CU, two where a part would be longer than this, in
+// steps.  32/8 heads of 128, two and one: 1 x 16000 18.5 and 14.7 us, 31 x 2000
+// 20.8 and 18.5; 8 x 16000 behind a pass over 1 GiB 40 and 42.5.
+constexpr int64_t kLongPart = 100;
+constexpr int64_t kMostParts = 32;  // the join takes them in order: 1 x 128000 39.5 us, with 64 41.3
 // Whole sequences that leave most CUs without work: one workgroup for each block
 // or two of the values, all of which find the scores for themselves.  1 x 1000,
 // 32/8 heads of 128: 8.6 us, in one workgroup per key head 10.2; 32/4 of 256: 12.3
@@ -661,13 +666,14 @@ static AttnQ4Plan attn_q4_plan(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
     p.waves = 8;
     return p;
   }
-  p.least = kLeast;
+  p.least = static_cast<int>(kLeast);
   if (items >= kGroups / 2) {
     p.groups = static_cast<int>(std::min<int64_t>(kGroups, (items * steps + kLeast - 1) / kLeast));
     p.slots = 2 * p.groups;
   } else {
-    p.parts = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(kGroups / std::max<int64_t>(1, items), (steps + kLeast - 1) / kLeast)));
+    const int64_t one = std::max<int64_t>(1, kGroups / 2 / std::max<int64_t>(1, items));
+    const int64_t most = one * kLongPart < steps ? 2 * one : one;
+    p.parts = static_cast<int>(std::min({most, (steps + kLeast - 1) / kLeast, kMostParts}));
     p.slots = p.parts == 1 ? 0 : items * p.parts;
   }
   return p;
