@@ -514,7 +514,7 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * must be ordered on one stream.  Equal calls give equal bits.
  * Requires B >= 0, 1 <= n <= QMM_ATTN_MAX_N, Hq % Hk == 0, Hq <= 1024, D one
  * of 64, 96, 128, 192, 256, scale finite, 0 <= window < 2^31, W >= 1, W * page
- * <= 2^30, B * n * Hq < 2^23, B * (W * page / 32 + 1) < 2^31, pages as
+ * <= 2^30, B * n * Hq < 2^23, B * (W * page / 32 + 16) < 2^31, pages as
  * kv_append_q4.  B == 0 is a no-op.
  */
 int attn_q4(const void* q, int64_t q_stride, int type, const void* cache, int64_t pages, int64_t page,

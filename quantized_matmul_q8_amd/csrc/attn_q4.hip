@@ -221,6 +221,11 @@ __device__ __forceinline__ void add_values(const Cell<NB, VB> (&cell)[2], const 
   if constexpr (b + 1 < VB) add_values<NB, VB, RT, b + 1>(cell, p, o);
 }
 
+// What a sequence and head costs besides its steps, in steps: it begins with three loads that wait for each other and ends
+// with a join of the waves.  Where runs are equal without it a run over many short sequences takes the longest: 64 of 1 to
+// 2000 tokens, 32/8 heads of 128: 55 us, with 3, 6, 10 and 16 more 40, 28, 26 and 26.
+constexpr int kBetween = 12;
+
 // A sequence's length, and the first key that any of its queries sees, in whole steps.
 struct Extent {
   int len, floor_at, first, steps;  // at least one step, which writes the zeros of an empty sequence
@@ -236,7 +241,7 @@ __device__ __forceinline__ Extent extent_of(const AttnQ4Args& a, int32_t stored)
 
 // Steps of one head and row block, summed over sequences by a wave, 64 of them at a time.
 __device__ __forceinline__ int scan_steps(const AttnQ4Args& a, int b0, int lane, int& mine) {
-  mine = b0 + lane < a.B ? extent_of(a, a.lens[min(b0 + lane, a.B - 1)]).steps : 0;
+  mine = b0 + lane < a.B ? extent_of(a, a.lens[min(b0 + lane, a.B - 1)]).steps + kBetween : 0;
   return wave_scan(mine);
 }
 // Of all sequences; `before`: of those before `seq`.
@@ -562,7 +567,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_parts_kernel(AttnQ4Args a
                               [](Segment&) { return false; });
 }
 
-// Equal runs of the steps of all.
+// Equal runs of the steps of all, and of what stands for the beginning and end of each item.
 template <int NB, int RT, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a) {
   __shared__ AttnQ4Shared<NB, kWaves> sh;
@@ -572,30 +577,34 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q4_runs_kernel(AttnQ4Args a)
   const int64_t first = blockIdx.x * per;
   int64_t left = min(total - first, per);  // steps of the run
   if (left <= 0) return;
-  const int seq0 = find_steps(a, first, lane, before);
-  const Extent e = extent_of(a, as_scalar(a.lens)[seq0]);
+  int seq = find_steps(a, first, lane, before);
+  Extent e = extent_of(a, as_scalar(a.lens)[seq]);
   const int64_t in = first - static_cast<int64_t>(before) * heads;
-  int head = static_cast<int>(quotient(in, e.steps));
-  const int from = static_cast<int>(in - static_cast<int64_t>(head) * e.steps);
-  int64_t slot = 2 * int64_t{blockIdx.x};
-  // the segment that begins at `from`: to its item's end or the run's
-  const auto segment = [&](int seq, const Extent& e, int from) {
-    const int to = static_cast<int>(min(static_cast<int64_t>(e.steps), from + left));
-    left -= to - from;
-    return Segment{seq, head / a.row_blocks, head % a.row_blocks, from, to, from == 0 && to == e.steps ? -1 : slot, e};
-  };
-  attn_q4_run<NB, NB, RT, kWaves>(a, sh, segment(seq0, e, from), [&](Segment& s) {
-    if (left == 0) return false;
-    slot = 2 * int64_t{blockIdx.x} + 1;  // the last one's, should it not be whole
-    int seq = s.seq;
-    Extent e = s.ext;
-    if (++head == heads) {
-      head = 0;
-      e = extent_of(a, as_scalar(a.lens)[++seq]);
+  int head = static_cast<int>(quotient(in, e.steps + kBetween));
+  int from = static_cast<int>(in - static_cast<int64_t>(head) * (e.steps + kBetween));
+  int64_t slot = 2 * int64_t{blockIdx.x};  // of the run's first item; then of the last one, should it not be whole
+  // the run's next item with steps in it
+  const auto next = [&](Segment& s) {
+    while (left > 0) {
+      const int to = static_cast<int>(min(static_cast<int64_t>(e.steps + kBetween), from + left)), end = min(to, e.steps);
+      const bool any = from < e.steps;
+      if (any) {
+        const bool whole = from == 0 && end == e.steps;
+        s = Segment{seq, head / a.row_blocks, head % a.row_blocks, from, end, whole ? -1 : slot, e};
+      }
+      left -= to - from;
+      slot = 2 * int64_t{blockIdx.x} + 1;
+      from = 0;
+      if (left > 0 && ++head == heads) {
+        head = 0;
+        e = extent_of(a, as_scalar(a.lens)[++seq]);
+      }
+      if (any) return true;
     }
-    s = segment(seq, e, 0);
-    return true;
-  });
+    return false;
+  };
+  Segment s;
+  if (next(s)) attn_q4_run<NB, NB, RT, kWaves>(a, sh, s, next);
 }
 
 // Joins the partial results of one row, a wave each.
@@ -614,7 +623,7 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   } else {
     int before;
     const int64_t per = run_steps(a, static_cast<int64_t>(total_steps(a, lane, seq, before)) * heads);
-    const int64_t begin = static_cast<int64_t>(before) * heads + static_cast<int64_t>(head) * steps;
+    const int64_t begin = static_cast<int64_t>(before) * heads + static_cast<int64_t>(head) * (steps + kBetween);
     const int64_t g0 = quotient(begin, per), g1 = quotient(begin + steps - 1, per);
     count = static_cast<int>(g1 - g0 + 1);
     // the first run's second result, unless the run begins with it; the others' first
@@ -707,7 +716,7 @@ static void launch_attn_q4(const AttnQ4Args& a, const AttnQ4Plan& p, hipStream_t
 static bool attn_q4_shape(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   return B >= 0 && n >= 1 && n <= QMM_ATTN_MAX_N && Hk >= 1 && Hq >= Hk && Hq <= 1024 && Hq % Hk == 0 &&
          attn_head_dim(D) && max_len >= 1 && max_len <= kMostTokens && B < (int64_t{1} << 23) / (n * Hq) &&
-         B * ((max_len + kStep - 1) / kStep + 1) < (int64_t{1} << 31);
+         B * ((max_len + kStep - 1) / kStep + 1 + kBetween) < (int64_t{1} << 31);
 }
 
 }  // namespace qmm
