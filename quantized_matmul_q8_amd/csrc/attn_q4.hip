@@ -25,10 +25,10 @@
 // the workspace, and a second kernel joins these.
 //
 // Bound by HBM and, next to it, by the instructions that make numbers of codes.
-// 64 sequences of 1 to 8192 tokens, 32/8 heads of 128, 403 MB: 73 us and 5 for
-// the join, 5.5 TB/s; the loads alone take 65, the instructions alone 50 (of
+// 64 sequences of 2048 to 8192 tokens, 32/8 heads of 128, 403 MB: 73 to 77 us and
+// 5 for the join, 5.4 TB/s; the loads alone take 65, the instructions alone 50 (of
 // about 300 a step and wave 128 make the values, as few as the format allows).
-// 671 MB in sequences of one length: 115 us, 5.8 TB/s.  A short sequence is bound
+// 671 MB in sequences of one length: 114 us, 5.9 TB/s.  A short sequence is bound
 // by one CU's instructions, 1 x 1000: 8.6 us.
 #include "attn.hpp"
 #include "kv_q4.hpp"
@@ -650,8 +650,8 @@ struct AttnQ4Plan {
 // of 128, 1 x 1000: 8.6 us in a graph and 10 a call by itself; as parts 8.5 and
 // 14.3; 32 x 1000: 11.8 and, as parts, 16.2 in a graph; 1 x 2000: 12.1 and 9.6.
 constexpr int64_t kWhole = 1024;
-// Two workgroups per CU.  With three 64 x 8192 in pages of 16 takes 79 us for 84, in pages of 64 75 for 73, and 64 rows a
-// key head (16 x 4096, 8 tokens) 75 for 62.
+// Two workgroups per CU.  With three 64 sequences of 1 to 8192 tokens take 64 us for 61, of 8192 119 for 114, and 16 x
+// 4096 with 64 rows a key head 71 for 50.
 constexpr int kGroups = 512;
 constexpr int64_t kLeast = 8;  // steps: two a wave
 // Parts: one workgroup per CU, two where a part would be longer than this, in
