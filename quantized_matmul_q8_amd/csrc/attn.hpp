@@ -53,10 +53,19 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// What the difference of two products q k is multiplied with for the exponent
+// between their terms; 1 where that is 0 (the queries count as zeros then).
+// Differences are taken first, everywhere: of products past 2^24 or so, multiplied
+// each by itself, only the rounding would be left.
+__device__ __forceinline__ float exponent_mul(float scale) {
+  const float mul = fabsf(scale) * 1.44269504088896340736f;
+  return mul == 0.0f ? 1.0f : mul;
+}
+
 // One row of four dims per lane from `count` partial results: at `part` + step *
-// at(k) number k's sums of terms times values, in ml[at(k)] its maximum and sum
-// of terms.  The maxima and sums by the lanes, 64 at a time, then the partial
-// results in order, four loads in flight.  The first loads begin with the
+// at(k) number k's sums of terms times values, in ml[at(k)] its largest product and
+// its sum of terms.  The products and sums by the lanes, 64 at a time, then the
+// partial results in order, four loads in flight.  The first loads begin with the
 // object, so that what is done before join() hides them.
 template <typename At>
 struct Parts {
@@ -80,7 +89,7 @@ struct Parts {
   }
 
   // The row; zeros if all sums are 0.
-  __device__ __forceinline__ v4f join() {
+  __device__ __forceinline__ v4f join(float mul) {
     float m = -INFINITY, total = 0.0f;
     v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k0 = 0; k0 < count; k0 += 64) {
@@ -89,8 +98,8 @@ struct Parts {
       float most = fmaxf(m, rows_max(own.x));
 #pragma unroll
       for (int k = 1; k < 16; k *= 2) most = fmaxf(most, __shfl_xor(most, k));
-      const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f(m - base);
-      const float f = __builtin_amdgcn_exp2f(own.x - base);
+      const float base = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f((m - base) * mul);
+      const float f = __builtin_amdgcn_exp2f((own.x - base) * mul);
       total = total * keep + wave_sum(own.y * f);
       y *= keep;
       m = most;

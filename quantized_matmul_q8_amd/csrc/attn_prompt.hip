@@ -524,7 +524,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
           *reinterpret_cast<v4f*>(part + b * 32 + 2 * i + 4 * h) = v4f{o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
       if (h == 0)
         reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.tiles) * a.Hk * a.splits * kRows * D)[slot] =
-            make_float2(top * mul, sum);
+            make_float2(top, sum);
     }
   } else if (mine) {
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a, int
   const Place pl = find_place(a, n, lane);
   const int row = pl.tile * kRows + in_tile;
   if (!pl.found || row >= pl.nq * a.group) return;
-  const v4f y = parts.join();
+  const v4f y = parts.join(exponent_mul(a.scale));
   const int64_t out = (static_cast<int64_t>(pl.q0 + row / a.group) * a.Hq + kh * a.group + row % a.group) * D;
   if (lane * 4 < D) store4(a.y_type, a.y, out / 4 + lane, make_float4(y.x, y.y, y.z, y.w));
 }

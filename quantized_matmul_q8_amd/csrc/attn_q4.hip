@@ -1,6 +1,6 @@
 // Attention of a sequence's last tokens over the paged 4-bit cache.
 //
-//   S^T = K Q^T,  p = 2^(c s - m),  O^T = V^T P^T,  y = O / sum p
+//   S^T = K Q^T,  p = 2^(c (s - max s)),  O^T = V^T P^T,  y = O / sum p
 //
 // The query rows of one key head (new tokens x heads of the group) are the
 // columns of 16 x 16 tiles.  A wave takes 32 tokens, two cells of the cache, at
@@ -285,7 +285,7 @@ __device__ __forceinline__ int64_t run_steps(const AttnQ4Args& a, int64_t total)
 template <int VB, int kWaves>
 struct AttnQ4Shared {
   float o[kWaves][16][32 * VB + 4];
-  float m[kWaves][16], l[kWaves][16];
+  float m[kWaves][16], l[kWaves][16], mul[16];
 };
 
 // Steps `from` .. `to` of one sequence, key head and row block; `slot`: where a partial result goes, or -1 for a whole one.
@@ -410,11 +410,11 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
     }
 
     v4f o[RT][2 * VB];
-    // the largest product so far, what is added to a product's exponent for it, and this lane's part of the sum
-    float top[RT], base[RT], sum[RT];
+    // the largest product so far, and this lane's part of the sum
+    float top[RT], sum[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      top[r] = -INFINITY, base[r] = kLift, sum[r] = 0.0f;
+      top[r] = -INFINITY, sum[r] = 0.0f;
 #pragma unroll
       for (int b = 0; b < 2 * VB; ++b) o[r][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -456,17 +456,17 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
 #pragma unroll
         for (int k = 0; k < 8; ++k) most = fmaxf(most, s[r][k >> 2][k & 3]);
         most = rows_max(most);
+        const float zero = most == -INFINITY ? 0.0f : most;
         if (__builtin_amdgcn_ballot_w64(most > top[r])) {
-          const float keep = __builtin_amdgcn_exp2f((top[r] - (most == -INFINITY ? 0.0f : most)) * mul[r]);
+          const float keep = __builtin_amdgcn_exp2f((top[r] - zero) * mul[r]);
           sum[r] *= keep;
 #pragma unroll
           for (int b = 0; b < 2 * VB; ++b) o[r][b] *= keep;
           top[r] = most;
-          base[r] = kLift - (most == -INFINITY ? 0.0f : most) * mul[r];
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3], mul[r], base[r]));
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][k >> 2][k & 3] - zero, mul[r], kLift));
           sum[r] += e;
           p[r][(k & 4) + kv_quad_byte(k & 3)] = static_cast<_Float16>(e);
         }
@@ -499,7 +499,8 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const float l = rows_sum(sum[r]);
-      if (c == 0) sh.m[wave][col] = top[r] * mul[r], sh.l[wave][col] = l;
+      if (c == 0) sh.m[wave][col] = top[r], sh.l[wave][col] = l;
+      if (wave == 0 && c == 0) sh.mul[col] = mul[r];
 #pragma unroll
       for (int b = 0; b < 2 * VB; ++b) *reinterpret_cast<v4f*>(&sh.o[wave][col][b * 16 + 4 * c]) = o[r][b];
       __syncthreads();
@@ -509,20 +510,24 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
         float m = sh.m[0][row];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
-        const float zero = m == -INFINITY ? 0.0f : m;
+        const float zero = m == -INFINITY ? 0.0f : m, mul = sh.mul[row];
         float total = 0.0f;
         v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - zero);
+          const float f = __builtin_amdgcn_exp2f((sh.m[w][row] - zero) * mul);
           total += sh.l[w][row] * f;
           y += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
         }
         if (done.slot >= 0) {
           const int64_t at_row = done.slot * a.block_rows + r * 16 + row;
           *reinterpret_cast<v4f*>(a.part + at_row * D + d) = y;
-          if (d == 0)
-            reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D)[at_row] = make_float2(m, total);
+          if (d == 0) {
+            // the product of the keys with the query as it was, without its power of two
+            const int e = __builtin_amdgcn_frexp_expf(mul) - __builtin_amdgcn_frexp_expf(exponent_mul(a.scale));
+            reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D)[at_row] =
+                make_float2(__builtin_amdgcn_ldexpf(m, e), total);
+          }
         } else {
           const int i = (row0 + row) / a.group, h = done.kh * a.group + (row0 + row) % a.group;
           const int64_t out = (static_cast<int64_t>(done.seq) * a.n + i) * a.Hq + h;
@@ -634,7 +639,7 @@ __global__ __launch_bounds__(64) void attn_q4_join_kernel(AttnQ4Args a, int D) {
   if (count == 1) return;  // whole, and written
   const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(a.slots) * a.block_rows * D);
   const v4f y = Parts([&](int k) { return (k == 0 ? first : second + (k - 1) * step) * a.block_rows + in; },
-                      a.part + min(lane * 4, D - 4), D, ml, count, lane).join();
+                      a.part + min(lane * 4, D - 4), D, ml, count, lane).join(exponent_mul(a.scale));
   const int64_t out = blockIdx.x;
   if (lane * 4 < D) store4(a.y_type, a.y, (out * D + lane * 4) / 4, make_float4(y.x, y.y, y.z, y.w));
 }
