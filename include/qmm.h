@@ -507,8 +507,8 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * zeros, and so does one whose every score is -inf.  lens above W * page count
  * as that, negative ones as 0; keys of a page number outside [0, pages) are not
  * seen; nothing of a page behind a sequence's end is used, whatever it holds.
- * Scores, softmax statistics and sums are fp32; the softmax's terms are
- * rounded to f16 (half a step, 2^-11 relative) where they meet the values.
+ * Products, scores, softmax statistics and sums are fp32 (a product past its
+ * range is an infinity); the softmax's terms are rounded to f16 (half a step, 2^-11 relative) where they meet the values.
  * ws: attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page) bytes of scratch, no
  * initialisation needed; may be NULL where that is 0.  Calls that share it
  * must be ordered on one stream.  Equal calls give equal bits.
@@ -542,8 +542,8 @@ size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
  * outside [cu_q[0], cu_q[B]) are left as they were.  The entries of cu_q and
  * cu_k are expected in order and within [0, Tq] and [0, Tk]; rows beyond these
  * are never touched.
- * Scores, softmax statistics and sums are fp32; the softmax's terms are
- * rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
+ * Products, scores, softmax statistics and sums are fp32 (a product past its
+ * range is an infinity); the softmax's terms are rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
  * values.
  * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
  * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, Tq * Hq < 2^30,

@@ -57,10 +57,9 @@ __device__ __forceinline__ int wave_scan(int v) {
 // between their terms; 1 where that is 0 (the queries count as zeros then).
 // Differences are taken first, everywhere: of products past 2^24 or so, multiplied
 // each by itself, only the rounding would be left.
-__device__ __forceinline__ float exponent_mul(float scale) {
-  const float mul = fabsf(scale) * 1.44269504088896340736f;
-  return mul == 0.0f ? 1.0f : mul;
-}
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ bool vanishes(float scale) { return fabsf(scale) * kLog2e == 0.0f; }
+__device__ __forceinline__ float exponent_mul(float scale) { return vanishes(scale) ? 1.0f : fabsf(scale) * kLog2e; }
 
 // One row of four dims per lane from `count` partial results: at `part` + step *
 // at(k) number k's sums of terms times values, in ml[at(k)] its largest product and

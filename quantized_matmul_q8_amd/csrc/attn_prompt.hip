@@ -1,6 +1,6 @@
 // Attention over whole prompts, packed sequences.
 //
-//   S^T = K Q^T,  p = 2^(c s - m),  O^T = V^T P^T,  y = O / sum p
+//   S^T = K Q^T,  p = 2^(c (s - m)),  O^T = V^T P^T,  y = O / sum p
 //
 // The rows of one key head (tokens x heads of the group) are the columns of
 // 32 x 32 tiles; a wave has 32 of them, a workgroup 128, which share tiles of K
@@ -145,6 +145,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   constexpr int kSteps = D / 16, kBlocks = D / 32, kKeys = BN / 32;
   constexpr float kLift = BF16 ? 0.0f : 7.0f;  // terms of up to 2^(8 + kLift): f16 holds them, and those down to 2^-31
   constexpr float kSlack = 8.0f;               // a maximum is followed when it is passed by 2^8
+  constexpr float kFar = 1024.0f;              // up to here `base` is off by 2^-14 at most, and alike for all terms
   constexpr int kKeyBufs = 3;
   __shared__ __attribute__((aligned(1024))) uint8_t s_k[kKeyBufs][kTile], s_v[2][kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -161,21 +162,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   // this lane's query, and the keys it sees: lo .. at
   const int row = min(row0 + col, rows - 1), tok = row / a.group, head = kh * a.group + row % a.group;
   const int at = a.causal ? before + tok : pl.nk - 1, lo = a.window > 0 ? max(0, at - a.window + 1) : 0;
-  float mul = fabsf(a.scale) * 1.44269504088896340736f;
+  const float mul = exponent_mul(a.scale);
   v4u q[kSteps];
   {
     // the scale's sign into the query, so that the largest product is the largest score
     const uint16_t* src = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(pl.q0 + tok) * a.q_stride + head * D;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = mul == 0.0f ? 0u : ~0u;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = vanishes(a.scale) ? 0u : ~0u;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       q[s] = *reinterpret_cast<const v4u*>(src + s * 16 + h * 8);
       q[s].x = (q[s].x ^ flip) & keep, q[s].y = (q[s].y ^ flip) & keep;
       q[s].z = (q[s].z ^ flip) & keep, q[s].w = (q[s].w ^ flip) & keep;
     }
-    mul = mul == 0.0f ? 1.0f : mul;
   }
-  const float slack = fminf(kSlack / mul, 3.0e38f);  // finite: -inf, the first maximum, plus it stays -inf
+  const float slack = fminf(kSlack / mul, 3.0e38f);  // finite: the first maximum lies infinitely far above -inf
 
   // the bounds of the wave's rows and of the workgroup's, the same for all lanes
   const bool active = row0 < rows;
@@ -273,7 +273,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   v16f o[kBlocks];
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) o[b] = v16f{};
-  float top = -INFINITY, base = kLift, sum = 0.0f;
+  float top = -INFINITY, base = kLift, sum = 0.0f;  // what terms go by, what a scaled product takes to their exponents
+  bool far = false;  // some row's exponent leaves fp32 too little behind the point: products are settled first
 
   const auto products = [&](v16f (&s)[kKeys], uint32_t buf) {
     const uint32_t here = k_at + buf;
@@ -380,14 +381,25 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   };
   // The maximum of new products: where it passes what all so far goes by too far, that is brought to it.
   const auto follow = [&](float most) {
-    if (__builtin_amdgcn_ballot_w64(most > top + slack)) {
+    if (__builtin_amdgcn_ballot_w64(most - top > slack)) {
       most = fmaxf(most, top);
-      const float keep = __builtin_amdgcn_exp2f((top - (most == -INFINITY ? 0.0f : most)) * mul);
+      const float zero = most == -INFINITY ? 0.0f : most, keep = __builtin_amdgcn_exp2f((top - zero) * mul);
       sum *= keep;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
       top = most;
-      base = kLift - (most == -INFINITY ? 0.0f : most) * mul;
+      far = __builtin_amdgcn_ballot_w64(!(fabsf(zero * mul) <= kFar)) != 0;
+      base = far ? kLift : kLift - zero * mul;
+    }
+  };
+  // Products as `base` takes them.  A term beside the matrix instructions costs one
+  // fma; its offset, rounded by itself, is a whole step of the exponent for products
+  // of 2^24, so past kFar the difference is taken first.
+  const auto settle = [&](v16f (&s)[kKeys]) {
+    if (far) {
+      const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int kb = 0; kb < kKeys; ++kb) s[kb] -= zero;
     }
   };
 
@@ -412,6 +424,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
             s[kb][i] = key_of(kb, i) <= at_here && key_of(kb, i) >= lo_here ? s[kb][i] : -INFINITY;
       }
       follow(highest(s));
+      settle(s);
       terms(s, p);
       if (whole) values(v_at + value_buf, p);
       else part_values(v_at + value_buf, p, at_here, lo_here);
@@ -428,7 +441,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
     // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
     // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
-    const auto step = [&](const v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
+    const auto step = [&](v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
+      settle(cur);
       const v4u k_tile = tile_of(k_next, k_bytes, t + 2), v_tile = tile_of(v_next, v_bytes, t + 1);
       k_next += k_step;
       v_next += v_step;
@@ -502,6 +516,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
       for (int kb = 0; kb < kKeys; ++kb) x[kb] = y[kb];
     }
     fill(t);
+    settle(x);
     terms(x, p);
     values(v_at + value_buf, p);
     leave();

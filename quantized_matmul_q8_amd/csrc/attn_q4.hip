@@ -376,7 +376,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
     for (int r = 0; r < RT; ++r) {
       const int row = (seg.row_block * RT + r) * 16 + col;
       at[r] = len - a.n + (row < a.rows ? row / a.group : a.n - 1);
-      mul[r] = fabsf(a.scale) * 1.44269504088896340736f;
+      mul[r] = fabsf(a.scale) * kLog2e;
       if (!a.bf16) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) q[r][j] = __builtin_bit_cast(h8, raw[r][j]);
