@@ -103,6 +103,10 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
          static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x)));
 }
 
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+
 constexpr int gcd16(int c) { return c % 16 == 0 ? 16 : c % 8 == 0 ? 8 : c % 4 == 0 ? 4 : c % 2 == 0 ? 2 : 1; }
 
 // Which sequence a tile belongs to, by the waves' lanes: 64 sequences at a time.
@@ -143,7 +147,6 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   constexpr int kVShift = C % 16 == 0 ? 0 : 1, kVMask = C % 16 == 0 ? 3 : C % 8 == 0 ? 1 : 0;  // V: chunk ^ 4 * ...
   constexpr int kCopies = BN * C / 256;                                // a wave's copies of a tile
   constexpr int kSteps = D / 16, kBlocks = D / 32, kKeys = BN / 32;
-  constexpr float kLift = BF16 ? 0.0f : 7.0f;  // terms of up to 2^(8 + kLift): f16 holds them, and those down to 2^-31
   constexpr float kSlack = 8.0f;               // a maximum is followed when it is passed by 2^8
   constexpr float kFar = 1024.0f;              // up to here `base` is off by 2^-14 at most, and alike for all terms
   constexpr int kKeyBufs = 3;
@@ -158,6 +161,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   const Place pl = find_place(a, n, lane);
   if (!pl.found) return;
   const int rows = pl.nq * a.group, row0 = pl.tile * kRows + wave * 32, before = pl.nk - pl.nq;
+
+  // What terms of the maximum are, as an exponent of two; others are up to 2^8 times that.  In f16 those of 2^15 and, down
+  // to 2^-31 of the maximum, all can be told.  In bf16 the terms of all keys sum to less than 1/2, so that no sum of them
+  // times values leaves fp32 (values below 2^(-126 - lift) lose bits).
+  const float lift = BF16 ? uniform(-9.0f - static_cast<float>(32 - __builtin_clz(pl.nk | 1))) : 7.0f;
 
   // this lane's query, and the keys it sees: lo .. at
   const int row = min(row0 + col, rows - 1), tok = row / a.group, head = kh * a.group + row % a.group;
@@ -273,7 +281,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
   v16f o[kBlocks];
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) o[b] = v16f{};
-  float top = -INFINITY, base = kLift, sum = 0.0f;  // what terms go by, what a scaled product takes to their exponents
+  float top = -INFINITY, base = lift, sum = 0.0f;  // what terms go by, what a scaled product takes to their exponents
   bool far = false;  // some row's exponent leaves fp32 too little behind the point: products are settled first
 
   const auto products = [&](v16f (&s)[kKeys], uint32_t buf) {
@@ -389,7 +397,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
       for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
       top = most;
       far = __builtin_amdgcn_ballot_w64(!(fabsf(zero * mul) <= kFar)) != 0;
-      base = far ? kLift : kLift - zero * mul;
+      base = far ? lift : lift - zero * mul;
     }
   };
   // Products as `base` takes them.  A term beside the matrix instructions costs one

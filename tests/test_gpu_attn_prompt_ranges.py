@@ -5,8 +5,8 @@ import torch
 
 import oracle
 import qmm_synth
-from _attention import U
-from _gpu import dev, say
+from _attention import U, allowed
+from _gpu import DEV, dev, say
 from _ranges import compare, ints, levels
 
 import quantized_matmul_q8_amd as qmm
@@ -89,3 +89,45 @@ def test_prompt_one_key(D, xt):
     y = qmm.attn_prompt(q[:7], k2, v2, ints([0, 7]), ints([0, 1600]), causal=False, out_dtype=F32)
     mean = v2.double().mean(0).repeat_interleave(Hq // Hk, 0).expand(7, Hq, D)
     assert torch.all((y.double() - mean).abs() <= 4 * U * mean.abs())      # whole numbers: the quotient alone rounds
+
+
+# ---------------------------------------------------------------- values near the end of their range
+
+@pytest.mark.parametrize("xt", [F16, BF16])
+@pytest.mark.parametrize("nq,nk,D,causal", [(300, 300, 64, True), (90, 400, 128, False), (70, 200, 256, True),
+                                            (40, 1700, 128, True), (3, 3000, 64, False)])
+def test_prompt_values_near_the_end_of_their_range(nq, nk, D, causal, xt):
+    """An average of finite values is finite, whatever their sum would be."""
+    say("attn_prompt large values", f"nq={nq} nk={nk} D={D} x={xt}")
+    g = qmm_synth.rng(nk + D)
+    top = torch.finfo(xt).max
+    q, k = dev(g.standard_normal((nq, 2, D))).to(xt), dev(g.standard_normal((nk, 1, D))).to(xt)
+    v = dev(g.standard_normal((nk, 1, D))).to(xt)
+    v[..., 0::4], v[..., 1::4] = top, -top
+    v[..., 2::4] = dev(np.where(g.random((nk, 1, D // 4)) < 0.5, 1.0, -1.0) * float(top)).to(xt)
+    seen = oracle.visible(nq, nk, causal)
+    qb, kb, vb = (t.double().cpu().numpy() for t in (q, k, v))
+    ref, spread = oracle.attention(qb, kb, vb, D**-0.5, seen)
+    tol = allowed(qb, kb, D**-0.5, seen, ref, spread, TERM[xt], F32)
+    y = qmm.attn_prompt(q, k, v, ints([0, nq]), ints([0, nk]), causal=causal, out_dtype=F32)
+    got = y.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - ref) <= tol)
+    # in the values' own type too: an average that rounds to the largest number stays that
+    z = qmm.attn_prompt(q, k, v, ints([0, nq]), ints([0, nk]), causal=causal)
+    whole = torch.as_tensor(seen.any(1), device=DEV)
+    assert torch.isfinite(z).all() and torch.all(z[whole][..., 0::4] >= top * (1 - 2.0**-7))
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_prompt_values_near_the_end_under_terms_above_one(D):
+    """All keys but the first few lie just below the distance at which a maximum is followed."""
+    L = 5000
+    k = torch.zeros(L, 1, D, dtype=BF16, device=DEV)
+    k[70:, 0, 0] = 1.0
+    q = torch.zeros(9, 1, D, dtype=BF16, device=DEV)
+    q[:, 0, 0] = 5.5                                                    # e^5.5 = 2^7.93
+    v = torch.full((L, 1, D), torch.finfo(BF16).max, dtype=BF16, device=DEV)
+    y = qmm.attn_prompt(q, k, v, ints([0, 9]), ints([0, L]), scale=1.0, causal=False, out_dtype=F32)
+    # the average of equal numbers, by terms rounded alike on both sides: the sums' roundings and the quotient's
+    assert torch.all((y.double() - v[0, 0, 0].double()).abs() <= 2 * (L + 64) * U * v[0, 0, 0].double())
