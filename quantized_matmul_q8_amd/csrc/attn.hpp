@@ -4,6 +4,8 @@
 
 #include "typed.hpp"
 
+#include <float.h>
+
 namespace qmm {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -54,12 +56,15 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // What the difference of two products q k is multiplied with for the exponent
-// between their terms; 1 where that is 0 (the queries count as zeros then).
+// between their terms; 1 where that is 0 (the queries count as zeros then), and the
+// largest number where it is past fp32 (infinity times no difference would be NaN).
 // Differences are taken first, everywhere: of products past 2^24 or so, multiplied
 // each by itself, only the rounding would be left.
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ bool vanishes(float scale) { return fabsf(scale) * kLog2e == 0.0f; }
-__device__ __forceinline__ float exponent_mul(float scale) { return vanishes(scale) ? 1.0f : fabsf(scale) * kLog2e; }
+__device__ __forceinline__ float exponent_mul(float scale) {
+  return vanishes(scale) ? 1.0f : fminf(fabsf(scale) * kLog2e, FLT_MAX);
+}
 
 // One row of four dims per lane from `count` partial results: at `part` + step *
 // at(k) number k's sums of terms times values, in ml[at(k)] its largest product and

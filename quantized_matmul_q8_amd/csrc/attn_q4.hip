@@ -406,7 +406,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
       const _Float16 sign = static_cast<_Float16>(mul[r] == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
       for (int j = 0; j < NB; ++j) q[r][j] *= sign;
-      mul[r] = mul[r] == 0.0f ? 1.0f : mul[r];
+      mul[r] = mul[r] == 0.0f ? 1.0f : fminf(mul[r], FLT_MAX);
     }
 
     v4f o[RT][2 * VB];

@@ -131,3 +131,19 @@ def test_prompt_values_near_the_end_under_terms_above_one(D):
     y = qmm.attn_prompt(q, k, v, ints([0, 9]), ints([0, L]), scale=1.0, causal=False, out_dtype=F32)
     # the average of equal numbers, by terms rounded alike on both sides: the sums' roundings and the quotient's
     assert torch.all((y.double() - v[0, 0, 0].double()).abs() <= 2 * (L + 64) * U * v[0, 0, 0].double())
+
+
+# ---------------------------------------------------------------- scales near the end of their range
+
+@pytest.mark.parametrize("xt", [F16, BF16])
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38, -3.4e38])
+@pytest.mark.parametrize("nq,nk,D", [(100, 100, 64), (300, 300, 128), (20, 1500, 128), (40, 100, 256)])
+def test_prompt_scales_near_the_end_of_their_range(nq, nk, D, scale, xt):
+    """Products of zero are scores of zero, and the largest of others takes all."""
+    g = qmm_synth.rng(nk + D)
+    q = torch.zeros(nq, 2, D, dtype=xt, device=DEV)
+    k, v = (dev(g.standard_normal((nk, 1, D))).to(xt) for _ in range(2))
+    q[:, 1, 0], k[:, 0, 0] = 2.0**-20, dev(g.integers(-3, 4, nk)).to(xt)
+    seen = oracle.visible(nq, nk, True)
+    y = qmm.attn_prompt(q, k, v, ints([0, nq]), ints([0, nk]), scale=scale, out_dtype=F32)
+    compare(y, q.double().cpu().numpy(), k.double().cpu().numpy(), v.double().cpu().numpy(), scale, seen, 7, TERM[xt], F32)

@@ -83,3 +83,30 @@ def test_cache_one_key(D, xt):
             y = qmm.attn_q4(q, cache, table, ints([1] * B), scale=scale, out_dtype=F32)
             want = dev(np.repeat(np.stack([v for _, v in kv]), Hq // Hk, 2))
             assert torch.equal(y, want), (W, scale, int((y != want).sum()))
+
+
+@pytest.mark.parametrize("xt", [F16, BF16])
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38, -3.4e38])
+@pytest.mark.parametrize("lens,Hq,D", [([100, 1], 4, 128), ([1500, 33], 4, 64), ([1100, 3, 600] * 44, 4, 64), ([1300], 40, 256)])
+def test_cache_scales_near_the_end_of_their_range(lens, Hq, D, scale, xt):
+    """Products of zero are scores of zero, and the largest of others takes all."""
+    g = qmm_synth.rng(len(lens) + D)
+    cache, table, kv = cached(g, lens, 2, D, 16, lambda b, x: np.repeat(g.integers(-3, 4, (x, 2, D // 32)), 32, -1))
+    q = np.zeros((len(lens), 1, Hq, D))
+    q[:, :, 1::2, 0] = 2.0**-20
+    y = qmm.attn_q4(dev(q).to(xt), cache, table, ints(lens), scale=scale, out_dtype=F32)
+    for b, x in enumerate(lens[:6]):
+        compare(y[b], q[b], *kv[b], scale, oracle.visible(1, x, True), 7, 2.0**-11, F32)
+    assert torch.isfinite(y).all()
+
+
+def test_cache_queries_of_bf16_under_large_scales():
+    """A scale whose product with a query's power of two leaves fp32, though the scores do not."""
+    g = qmm_synth.rng(20)
+    for lens in ([90], [1500]):
+        cache, table, kv = cached(g, lens, 2, 64, 16, lambda b, x: np.repeat(g.integers(-3, 4, (x, 2, 2)), 32, -1) * 2.0**-16)
+        q = np.zeros((1, 1, 4, 64))
+        q[..., 0] = 2.0**121
+        q[..., 1::2, 1] = 2.0**115
+        y = qmm.attn_q4(dev(q).bfloat16(), cache, table, ints(lens), scale=2.0**20, out_dtype=F32)
+        compare(y[0], q[0], *kv[0], 2.0**20, oracle.visible(1, lens[0], True), 7, 2.0**-11, F32)
