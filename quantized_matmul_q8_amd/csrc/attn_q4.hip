@@ -381,7 +381,8 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
 #pragma unroll
         for (int j = 0; j < NB; ++j) q[r][j] = __builtin_bit_cast(h8, raw[r][j]);
       } else {
-        // a power of two for the row brings its largest value to 2^13: exact but for what lies 2^-27 below that
+        // a power of two for the row brings its largest value to 2^13: exact but for what lies 2^-27 below that; next to
+        // an infinity the largest power keeps all other values finite
         float f[NB][8], top = 0.0f;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
@@ -392,7 +393,7 @@ __device__ __forceinline__ void attn_q4_run(const AttnQ4Args& a, AttnQ4Shared<VB
             top = fmaxf(top, fabsf(f[j][k]));
           }
         top = rows_max(top);
-        const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 14 : 0;
+        const int e = top == 0.0f ? 0 : top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 14 : 128 - 14;
         mul[r] = __builtin_amdgcn_ldexpf(mul[r], e);
 #pragma unroll
         for (int j = 0; j < NB; ++j)

@@ -110,3 +110,17 @@ def test_cache_queries_of_bf16_under_large_scales():
         q[..., 1::2, 1] = 2.0**115
         y = qmm.attn_q4(dev(q).bfloat16(), cache, table, ints(lens), scale=2.0**20, out_dtype=F32)
         compare(y[0], q[0], *kv[0], 2.0**20, oracle.visible(1, lens[0], True), 7, 2.0**-11, F32)
+
+
+@pytest.mark.parametrize("L", [70, 1500])
+def test_cache_infinite_queries_next_to_large_ones(L):
+    """Scores of -inf take no part however large the query's other values are: zeros where all are."""
+    g = qmm_synth.rng(L)
+    D = 64
+    cache, table, kv = cached(g, [L], 1, D, 16, lambda b, x: np.full((x, 1, D), -1.0))
+    q = np.zeros((1, 1, 4, D))
+    q[..., 0] = np.inf
+    q[0, 0, 1:, 1] = (-1e5, -1e30, 3e38)
+    for xt in (BF16, F16):
+        y = qmm.attn_q4(dev(np.clip(q, -6e4, None) if xt == F16 else q).to(xt), cache, table, ints([L]), out_dtype=F32)
+        assert not y.any(), (xt, y[0, 0, :, 0])
