@@ -314,7 +314,7 @@ def _heads(t: torch.Tensor, name: str, H: int | None = None, D: int | None = Non
                          f"{tuple(shape)}")
     T, H, D = shape
     st, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (H > 1 and sh != D):
+    if T and ((sd != 1 and D > 1) or (H > 1 and sh != D)):
         raise ValueError(f"{name}: a token's heads must stand next to each other, got strides {t.stride()}")
     if T <= 1:
         st = H * D
