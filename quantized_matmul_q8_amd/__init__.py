@@ -505,14 +505,17 @@ def _half(code: int, t: torch.Tensor, name: str) -> None:
         raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
 
 
-def _attn_out(out, q: torch.Tensor, dtype, index: int):
-    """(out, type code): a new output of q's shape, or the caller's, checked."""
+def _attn_out(out, q: torch.Tensor, dtype, *others: torch.Tensor):
+    """(out, type code): a new output of q's shape, or the caller's, checked; not over an input, which other
+    workgroups still read."""
     if out is None:
         t = q.dtype if dtype is None else dtype
         if t not in _TYPES:
             raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {t}")
         return torch.empty_like(q, dtype=t), _TYPES[t]
     _out(out, tuple(q.shape), out.dtype if dtype is None else dtype, q.device)
+    if out.numel() and any(out.data_ptr() == t.data_ptr() for t in (q, *others)):
+        raise ValueError("out must not be an input: there is no attention in place")
     return out, _typed(out, "out", q.dim())
 
 
@@ -562,7 +565,7 @@ def attn_q4(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
         _need(table, torch.int32, "table", 2)
         raise ValueError(f"table must be [{B}, W], got {tuple(table.shape)}")
     tp, lp = _ints(table, torch.int32, "table", index, (B, W)), _ints(lens, torch.int32, "lens", index, (B,))
-    out, yt = _attn_out(out, q, out_dtype, index)
+    out, yt = _attn_out(out, q, out_dtype)
     ws, wp, size = _attn_ws(ws, attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page), q, index)
     _enqueue(index, _lib.LIB.attn_q4, q.data_ptr(), qs, code, cache.data_ptr(), pages, page, tp, W, lp,
              D ** -0.5 if scale is None else scale, window, out.data_ptr(), yt, B, n, Hq, Hk, D, wp, size)
@@ -607,7 +610,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
         raise ValueError("cu_q must have at least one entry")
     cq = _ints(cu_q, torch.int32, "cu_q", index, (B + 1,))
     ck = cq if cu_k is None else _ints(cu_k, torch.int32, "cu_k", index, (B + 1,))
-    out, yt = _attn_out(out, q, out_dtype, index)
+    out, yt = _attn_out(out, q, out_dtype, k, v)
     ws, wp, size = _attn_ws(ws, attn_prompt_workspace_bytes(B, Tq, Tk, Hq, Hk, D), q, index)
     _enqueue(index, _lib.LIB.attn_prompt, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, cq, ck, B,
              D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), yt, Tq, Tk, Hq, Hk, D,

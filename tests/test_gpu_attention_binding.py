@@ -27,3 +27,19 @@ def test_no_tokens_in_tensors_of_any_strides():
     assert qmm.attn_prompt(none(0, 4, 64), none(0, 2, 64), none(0, 2, 64), i(1)).shape == (0, 4, 64)
     q = torch.ones(3, 4, 64, dtype=F16, device=DEV)
     assert not qmm.attn_prompt(q, none(0, 2, 64), none(0, 2, 64), torch.tensor([0, 3], dtype=torch.int32, device=DEV), i(2)).any()
+
+
+def test_outputs_over_an_input_are_refused():
+    """Several workgroups read a query, and one may have written its output by then."""
+    cache = qmm.kv_cache_q4(2, 16, 2, 64, DEV)
+    q, k = torch.ones(3, 4, 64, dtype=F16, device=DEV), torch.ones(3, 4, 64, dtype=F16, device=DEV)
+    table, lens = torch.zeros(3, 1, dtype=torch.int32, device=DEV), torch.ones(3, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="out"):
+        qmm.attn_q4(q, cache, table, lens, out=q)
+    for out in (q, k):
+        with pytest.raises(ValueError, match="out"):
+            qmm.attn_prompt(q, k, torch.ones_like(k), cu, out=out)
+        with pytest.raises(ValueError, match="out"):
+            qmm.attn_prompt(q, torch.ones_like(k), k, cu, out=out)
+    assert torch.all(q == 1) and torch.all(k == 1)
