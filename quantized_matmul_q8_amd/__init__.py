@@ -433,8 +433,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, rope: torch.Ten
 
 def kv_cache_q4(pages: int, page: int, Hk: int, D: int, device) -> torch.Tensor:
     """A zeroed paged 4-bit cache of keys and values, uint8 ``[pages, Hk, page/16, 20 D]`` (see include/qmm.h)."""
-    if page < 16 or page % 16 or D not in (64, 96, 128, 192, 256) or pages < 1 or Hk < 1:
-        raise ValueError("page must be a multiple of 16, D one of 64, 96, 128, 192, 256, pages and Hk at least 1")
+    if not 16 <= page <= 1 << 20 or page % 16 or D not in (64, 96, 128, 192, 256) or not 1 <= pages < 1 << 31 or not 1 <= Hk <= 1024:
+        raise ValueError("page must be a multiple of 16 up to 2^20, D one of 64, 96, 128, 192, 256, pages at least 1 and below "
+                         "2^31, Hk 1 to 1024")
     return torch.zeros((pages, Hk, page // 16, 20 * D), dtype=torch.uint8, device=device)
 
 
