@@ -32,11 +32,6 @@ __device__ __forceinline__ scalar_ints as_scalar(const int32_t* p) {
   return reinterpret_cast<scalar_ints>(reinterpret_cast<uintptr_t>(p));
 }
 
-__device__ __forceinline__ int64_t scalar_int64(const int64_t* p, int64_t i) {
-  const scalar_ints q = as_scalar(reinterpret_cast<const int32_t*>(p + i));
-  return static_cast<int64_t>(q[1]) << 32 | static_cast<uint32_t>(q[0]);
-}
-
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
 
