@@ -508,7 +508,10 @@ int kv_read_q4(const void* cache, int64_t pages, int64_t page, const int64_t* sl
  * as that, negative ones as 0; keys of a page number outside [0, pages) are not
  * seen; nothing of a page behind a sequence's end is used, whatever it holds.
  * Products, scores, softmax statistics and sums are fp32 (a product past its
- * range is an infinity); the softmax's terms are rounded to f16 (half a step, 2^-11 relative) where they meet the values.
+ * range is an infinity); the softmax's terms are rounded to f16 (half a step,
+ * 2^-11 relative) where they meet the values, and bf16 queries are taken as f16
+ * numbers times a power of two for the row: exact but for values below 2^-27 of
+ * its largest, which are rounded to steps of 2^-37 of that.
  * ws: attn_q4_workspace_bytes(B, n, Hq, Hk, D, W * page) bytes of scratch, no
  * initialisation needed; may be NULL where that is 0.  Calls that share it
  * must be ordered on one stream.  Equal calls give equal bits.
@@ -543,8 +546,10 @@ size_t attn_q4_workspace_bytes(int64_t B, int64_t n, int64_t Hq, int64_t Hk, int
  * cu_k are expected in order and within [0, Tq] and [0, Tk]; rows beyond these
  * are never touched.
  * Products, scores, softmax statistics and sums are fp32 (a product past its
- * range is an infinity); the softmax's terms are rounded to `type` (half a step, 2^-11 or 2^-8 relative) where they meet the
- * values.
+ * range is an infinity); the softmax's terms are rounded to `type` (half a step,
+ * 2^-11 or 2^-8 relative) where they meet the values, and summed as rounded.
+ * Finite values give a finite y; in bf16 those below 2^-116 times the count of
+ * the sequence's keys may lose bits.
  * Requires B >= 0, 0 <= Tq, Tk < 2^30, Hq % Hk == 0, Hq <= 1024, D one of 64,
  * 96, 128, 192, 256, scale finite, 0 <= window < 2^31, Tq * Hq < 2^30,
  * B * Hq < 2^23.  B == 0 and Tq == 0 are no-ops.  Equal calls give equal bits.

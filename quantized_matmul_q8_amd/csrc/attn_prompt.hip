@@ -20,12 +20,14 @@
 // Few rows against many keys: the keys are split, and a second kernel joins.
 //
 // Bound by the matrix cores and the power they take.  6000 + 2192 tokens, 32/8
-// heads of 128, bf16: 331 us, 1010 TFLOP/s (its matrix instructions alone,
-// without copies and exponentials: 256 us).  16/4 heads of 256, 512 tokens behind 4096: 50 us and 8
-// for the join, of which 29 do not grow with the keys (8192 more: 60 us, 1150
-// TFLOP/s): the partial results of four splits, 33 MB, written and read, the
-// first loads, and the masked tiles.  Half of the operands' LDS reads left out
-// gains 4 %, eight waves on the same tiles 1 %.
+// heads of 128, bf16: 318 to 340 us, 990 to 1050 TFLOP/s, on one card of five 357
+// (on one with 331 its matrix instructions alone, without copies and exponentials,
+// took 256).  Its 38 spilled registers are of the last of an odd number of whole
+// tiles and of masked ones, none of the steady loop.  16/4 heads of 256, 512 tokens
+// behind 4096: 50 us and 8 for the join, of which 29 do not grow with the keys
+// (8192 more: 60 us, 1150 TFLOP/s): the partial results of four splits, 33 MB,
+// written and read, the first loads, and the masked tiles.  Half of the operands'
+// LDS reads left out gains 4 %, eight waves on the same tiles 1 %.
 #include "attn.hpp"
 
 #include <algorithm>
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prompt_kernel(Prom
     v16f x[kKeys], y[kKeys];
     v4u p[BN / 16];
     // A tile's terms beside the products of the next tile's keys, then the products of the terms with the values.  The
-    // order is written out: matrix instructions without a pause, their operands read four ahead, and behind each of the
+    // order is written out: matrix instructions without a pause, their operands read five ahead, and behind each of the
     // first ones its share of the terms, two of them exponentiated and the two before packed, and now and then a copy.
     const auto step = [&](v16f (&cur)[kKeys], v16f (&next)[kKeys]) {
       settle(cur);

@@ -10,9 +10,9 @@
 // and a quad of tokens of each cell, whose scales come from a load of the whole
 // cell's by row broadcasts.  The tile of S^T leaves in each lane the terms of
 // one query and the same quads of tokens, which is the operand that O^T takes:
-// nothing goes through LDS between the products.  Codes become f16 numbers by
-// their bits (0x6400 | n = 1024 + n, 0x5400 | n << 4 = 64 + n), a subtraction
-// that is exact, and one fma: the numbers that the format stands for.
+// nothing goes through LDS between the products.  Codes become f16 numbers, two
+// an instruction, by the conversion of 8-bit floats (codes_to_f16), and by one fma
+// the numbers that the format stands for.
 //
 // How the work is dealt out (the host knows no lengths):
 //   short sequences  a workgroup of eight waves takes a sequence and head whole,
@@ -27,7 +27,7 @@
 // Bound by HBM and, next to it, by the instructions that make numbers of codes.
 // 64 sequences of 2048 to 8192 tokens, 32/8 heads of 128, 403 MB: 73 to 77 us and
 // 5 for the join, 5.4 TB/s; the loads alone take 65, the instructions alone 50 (of
-// about 300 a step and wave 128 make the values, as few as the format allows).
+// about 310 a step and wave 128 make the values, as few as the format allows).
 // 671 MB in sequences of one length: 114 us, 5.9 TB/s.  A short sequence is bound
 // by one CU's instructions, 1 x 1000: 8.6 us.
 #include "attn.hpp"

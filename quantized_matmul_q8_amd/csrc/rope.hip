@@ -8,8 +8,8 @@
 // lane.  A wave holds one token's cosines and sines in registers while it goes
 // over heads of that token.
 //
-// Bound by HBM: 16384 x 72 x 128 in bf16, 612 MB, 111 us, 5.5 TB/s, the rate of a
-// copy; one token by the launch, 3.4 us.
+// Bound by HBM: 16384 x 72 x 128 in bf16, 612 MB, 111 to 116 us on three cards,
+// 5.3 to 5.5 TB/s, the rate of a copy; one token by the launch, 3.6 us.
 #include "typed.hpp"
 
 #include <algorithm>
